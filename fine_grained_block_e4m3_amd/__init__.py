@@ -9,7 +9,9 @@ CPU fallback.
 
 Names follow the C ABI: ``quant_1x128``, ``quant_128x128``, ``gemm_nt``,
 ``grouped_gemm_contiguous``, ``grouped_gemm_masked``,
-``get_mk_alignment_for_contiguous_layout``.
+``get_mk_alignment_for_contiguous_layout``; the feed-forward operators
+``gated_nt``, ``gated_nt_qout``, ``gated_nt_grad``, ``gemv_w4``,
+``gated_gemv_w4``, ``quant_int4``, ``clip_grad_norm``.
 """
 from __future__ import annotations
 
@@ -25,6 +27,9 @@ FLAG_UE8M0 = 1
 FLAG_FAST_ACCUM = 2
 PLAN_MX = 0x100
 PLAN_QOUT = 0x200
+ACT = {"silu": 0, "gelu": 1}
+W4_MXFP4 = 0
+CLIP_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 LAYOUT = {"dense": 0, "contiguous": 1, "masked": 2}
 
 STATUS = {
@@ -54,6 +59,16 @@ SYMBOLS = (
     "fp8_gemm_nt_mx",
     "fp8_quant_mxfp4",
     "fp8_gemm_nt_mx_w4",
+    "fp8_gated_nt",
+    "fp8_gated_nt_qout",
+    "fp8_gated_workspace_size",
+    "fp8_gated_nt_grad",
+    "fp8_gated_grad_workspace_size",
+    "fp8_gemv_w4",
+    "fp8_gated_gemv_w4",
+    "fp8_quant_int4",
+    "fp8_clip_grad_norm",
+    "fp8_clip_workspace_size",
     "fp8_get_mk_alignment_for_contiguous_layout",
     "fp8_status_string",
 )
@@ -108,11 +123,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fp8_gemm_nt_mx.argtypes = [P, P, P, P, P, I64, I64, I64, U32, P]
     L.fp8_quant_mxfp4.argtypes = [P, I64, I64, P, P, P]
     L.fp8_gemm_nt_mx_w4.argtypes = [P, P, P, P, P, I64, I64, I64, U32, P]
+    L.fp8_gated_nt.argtypes = [P] * 9 + [I64, I64, I64, I32, U32, P, ctypes.c_size_t, P]
+    L.fp8_gated_nt_qout.argtypes = [P] * 8 + [I64, I64, I64, I32, U32, P, ctypes.c_size_t, P]
+    L.fp8_gated_workspace_size.argtypes = [I64, I64, I64, I32]
+    L.fp8_gated_workspace_size.restype = ctypes.c_size_t
+    L.fp8_gated_nt_grad.argtypes = [P] * 9 + [I64, I64, I64, I32, P, ctypes.c_size_t, P]
+    L.fp8_gated_grad_workspace_size.argtypes = [I64, I64]
+    L.fp8_gated_grad_workspace_size.restype = ctypes.c_size_t
+    L.fp8_gemv_w4.argtypes = [P] * 5 + [I64, I64, I64, I32, P]
+    L.fp8_gated_gemv_w4.argtypes = [P] * 8 + [I64, I64, I64, I32, I32, P]
+    L.fp8_quant_int4.argtypes = [P, I64, I64, I32, P, P, P, P]
+    PTRS, I64S, I32S = ctypes.POINTER(P), ctypes.POINTER(I64), ctypes.POINTER(I32)
+    L.fp8_clip_grad_norm.argtypes = [PTRS, PTRS, I64S, I32S, I32, ctypes.c_float, P, P, ctypes.c_size_t, P]
+    L.fp8_clip_workspace_size.argtypes = [I64S, I32]
+    L.fp8_clip_workspace_size.restype = ctypes.c_size_t
     for fn in ("fp8_quant_1x128", "fp8_quant_128x128", "fp8_gemm_nt", "fp8_gemm_nt_ws", "fp8_gemm_nt_noalloc",
                "fp8_gemm_plan",
                "fp8_gemm_nt_qout",
                "fp8_grouped_gemm_contiguous", "fp8_grouped_gemm_masked", "fp8_quant_mx",
-               "fp8_gemm_nt_mx", "fp8_quant_mxfp4", "fp8_gemm_nt_mx_w4"):
+               "fp8_gemm_nt_mx", "fp8_quant_mxfp4", "fp8_gemm_nt_mx_w4", "fp8_gated_nt", "fp8_gated_nt_qout",
+               "fp8_gated_nt_grad", "fp8_gemv_w4", "fp8_gated_gemv_w4", "fp8_quant_int4", "fp8_clip_grad_norm"):
         getattr(L, fn).restype = ctypes.c_int
     L.fp8_get_mk_alignment_for_contiguous_layout.argtypes = []
     L.fp8_get_mk_alignment_for_contiguous_layout.restype = I32
@@ -398,3 +428,226 @@ def gemm_nt_mx_w4(xq, ea, wq, eb, out=None) -> torch.Tensor:
     _check("fp8_gemm_nt_mx_w4", L.fp8_gemm_nt_mx_w4(_ptr(xq), _ptr(ea), _ptr(wq), _ptr(eb), _ptr(y),
                                                     M, N, K, 0, _stream(xq)))
     return y
+
+
+def _act(act: str) -> int:
+    if act not in ACT:
+        raise ValueError(f"act must be one of {sorted(ACT)}, got {act!r}")
+    return ACT[act]
+
+
+def _workspace(workspace, nbytes: int, like: torch.Tensor):
+    """(pointer, bytes) of the caller's workspace, or of one of nbytes allocated
+    through torch, and the tensor that holds it."""
+    if workspace is None:
+        if not nbytes:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    _need(workspace, "workspace", torch.uint8, 1)
+    _same_device(like, workspace)
+    return _ptr(workspace), workspace.numel(), workspace
+
+
+def _gated_operands(xq, sa, wgq, sbg, wuq, sbu, fn: str):
+    for t, name, dtype in ((xq, "xq", torch.uint8), (sa, "sa", torch.float32), (wgq, "wgq", torch.uint8),
+                           (sbg, "sbg", torch.float32), (wuq, "wuq", torch.uint8), (sbu, "sbu", torch.float32)):
+        _need(t, name, dtype, 2)
+    M, K = xq.shape
+    N = wgq.shape[0]
+    blocks = ((N + 127) // 128, K // 128)
+    if wgq.shape[1] != K or wuq.shape != (N, K) or sa.shape != (K // 128, M) or sbg.shape != blocks \
+            or sbu.shape != blocks:
+        raise ValueError(f"{fn}: inconsistent operand shapes")
+    _same_device(xq, sa, wgq, sbg, wuq, sbu)
+    return M, N, K
+
+
+def gated_nt(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = False, save: bool = False, out=None,
+             workspace=None):
+    """Gated feed-forward block on block-scaled E4M3 operands: h (M, N) bf16 =
+    act(X Wg^T) * (X Wu^T), act "silu" or "gelu" (tanh form).  With save the
+    projections are returned too: (h, g, u), which gated_nt_grad takes.  out:
+    h, or (h, g, u).  workspace: for decode-sized M, as for gemm_nt."""
+    L = load_library()
+    a = _act(act)
+    M, N, K = _gated_operands(xq, sa, wgq, sbg, wuq, sbu, "gated_nt")
+    count = 3 if save else 1
+    if out is None:
+        ys = [torch.empty((M, N), dtype=torch.bfloat16, device=xq.device) for _ in range(count)]
+    else:
+        ys = list(out) if save else [out]
+        if len(ys) != count:
+            raise ValueError("gated_nt: out must be (h, g, u) with save")
+        ys = [_out(t, f"out[{i}]", torch.bfloat16, (M, N), xq) for i, t in enumerate(ys)]
+    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_gated_workspace_size(M, N, K, 1 if save else 0)), xq)
+    _check("fp8_gated_nt", L.fp8_gated_nt(
+        _ptr(xq), _ptr(sa), _ptr(wgq), _ptr(sbg), _ptr(wuq), _ptr(sbu), _ptr(ys[0]),
+        _ptr(ys[1]) if save else None, _ptr(ys[2]) if save else None, M, N, K, a, _flags(ue8m0), ws, ws_bytes,
+        _stream(xq)))
+    return tuple(ys) if save else ys[0]
+
+
+def gated_nt_qout(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = False, out=None, workspace=None):
+    """gated_nt with h quantized for the down projection: (hq uint8 (M, N) E4M3
+    codes, sh fp32 (N/128, M) 1x128 scales); N % 128 == 0."""
+    L = load_library()
+    a = _act(act)
+    M, N, K = _gated_operands(xq, sa, wgq, sbg, wuq, sbu, "gated_nt_qout")
+    if out is None:
+        hq = torch.empty((M, N), dtype=torch.uint8, device=xq.device)
+        sh = torch.empty((N // 128, M), dtype=torch.float32, device=xq.device)
+    else:
+        hq = _out(out[0], "out[0]", torch.uint8, (M, N), xq)
+        sh = _out(out[1], "out[1]", torch.float32, (N // 128, M), xq)
+    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_gated_workspace_size(M, N, K, 2)), xq)
+    _check("fp8_gated_nt_qout", L.fp8_gated_nt_qout(
+        _ptr(xq), _ptr(sa), _ptr(wgq), _ptr(sbg), _ptr(wuq), _ptr(sbu), _ptr(hq), _ptr(sh), M, N, K, a,
+        _flags(ue8m0), ws, ws_bytes, _stream(xq)))
+    return hq, sh
+
+
+def gated_nt_grad(dh, g, u, x, wg, wu, act: str = "silu", need_dx: bool = True, need_dw: bool = True, out=None,
+                  workspace=None):
+    """Gradient of the gated block, BF16: dh, g, u (M, N), x (M, K), wg, wu
+    (N, K) -> (dx (M, K), dwg (N, K), dwu (N, K)); dx is None without need_dx,
+    dwg and dwu without need_dw.  out: (dx, dwg, dwu) buffers."""
+    L = load_library()
+    a = _act(act)
+    for t, name in ((dh, "dh"), (g, "g"), (u, "u"), (x, "x"), (wg, "wg"), (wu, "wu")):
+        _need(t, name, torch.bfloat16, 2)
+    M, N = dh.shape
+    K = x.shape[1]
+    if g.shape != (M, N) or u.shape != (M, N) or x.shape[0] != M or wg.shape != (N, K) or wu.shape != (N, K):
+        raise ValueError("gated_nt_grad: inconsistent operand shapes")
+    _same_device(dh, g, u, x, wg, wu)
+    shapes, wanted = ((M, K), (N, K), (N, K)), (need_dx, need_dw, need_dw)
+    if out is None:
+        ys = [torch.empty(shape, dtype=torch.bfloat16, device=dh.device) if w else None
+              for shape, w in zip(shapes, wanted)]
+    else:
+        ys = [_out(t, f"out[{i}]", torch.bfloat16, shape, dh) if w else None
+              for i, (t, shape, w) in enumerate(zip(out, shapes, wanted))]
+    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_gated_grad_workspace_size(M, N)), dh)
+    _check("fp8_gated_nt_grad", L.fp8_gated_nt_grad(
+        _ptr(dh), _ptr(g), _ptr(u), _ptr(x), _ptr(wg), _ptr(wu), *[_ptr(t) if t is not None else None for t in ys],
+        M, N, K, a, ws, ws_bytes, _stream(dh)))
+    return tuple(ys)
+
+
+def _w4(w, s, z, N: int, K: int, name: str) -> int:
+    """Checks one 4-bit weight and returns its `group` (W4_MXFP4 for packed
+    E8M0 scales)."""
+    _need(w, name, torch.uint8, 2)
+    if w.shape != (N, K // 2):
+        raise ValueError(f"{name} must have shape {(N, K // 2)}, got {tuple(w.shape)}")
+    if isinstance(s, torch.Tensor) and s.dtype == torch.int32:
+        _need(s, f"scales of {name}", torch.int32, 2)
+        if s.shape != (K // 128, N) or z is not None:
+            raise ValueError(f"MXFP4 {name}: scales must be (K/128, N), without zeros")
+        return W4_MXFP4
+    _need(s, f"scales of {name}", torch.bfloat16, 2)
+    groups = s.shape[0]
+    if s.shape[1] != N or groups == 0 or K % groups or K // groups not in (32, 64, 128):
+        raise ValueError(f"scales of {name} must be (K/group, N) with a group of 32, 64 or 128")
+    if z is not None:
+        _need(z, f"zeros of {name}", torch.uint8, 2)
+        if z.shape != s.shape:
+            raise ValueError(f"zeros of {name} must have the scales' shape")
+        _same_device(s, z)
+    return K // groups
+
+
+def gemv_w4(x, w, scales, zeros=None, out=None) -> torch.Tensor:
+    """y (M, N) bf16 = x (M, K) bf16 * W^T for up to 16 tokens, W in 4 bits:
+    w uint8 (N, K/2) with either the int32 (K/128, N) scales of quant_mxfp4, or
+    the bf16 (K/group, N) scales (and uint8 zeros, else 8) of quant_int4."""
+    L = load_library()
+    _need(x, "x", torch.bfloat16, 2)
+    M, K = x.shape
+    N = w.shape[0]
+    group = _w4(w, scales, zeros, N, K, "w")
+    _same_device(x, w, scales)
+    y = _out(out, "out", torch.bfloat16, (M, N), x) if out is not None \
+        else torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    _check("fp8_gemv_w4", L.fp8_gemv_w4(_ptr(x), _ptr(w), _ptr(scales), _ptr(zeros) if zeros is not None else None,
+                                        _ptr(y), M, N, K, group, _stream(x)))
+    return y
+
+
+def gated_gemv_w4(x, wg, scales_g, wu, scales_u, zeros_g=None, zeros_u=None, act: str = "silu",
+                  out=None) -> torch.Tensor:
+    """The gated block on 4-bit weights for up to 16 tokens: y (M, N) bf16 =
+    act(x Wg^T) * (x Wu^T); weights as for gemv_w4, both of one format."""
+    L = load_library()
+    a = _act(act)
+    _need(x, "x", torch.bfloat16, 2)
+    M, K = x.shape
+    N = wg.shape[0]
+    group = _w4(wg, scales_g, zeros_g, N, K, "wg")
+    if _w4(wu, scales_u, zeros_u, N, K, "wu") != group or (zeros_g is None) != (zeros_u is None):
+        raise ValueError("gated_gemv_w4: both weights must have one format")
+    _same_device(x, wg, scales_g, wu, scales_u)
+    y = _out(out, "out", torch.bfloat16, (M, N), x) if out is not None \
+        else torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    _check("fp8_gated_gemv_w4", L.fp8_gated_gemv_w4(
+        _ptr(x), _ptr(wg), _ptr(scales_g), _ptr(zeros_g) if zeros_g is not None else None, _ptr(wu), _ptr(scales_u),
+        _ptr(zeros_u) if zeros_u is not None else None, _ptr(y), M, N, K, group, a, _stream(x)))
+    return y
+
+
+def quant_int4(w: torch.Tensor, group: int = 128, symmetric: bool = False, out=None):
+    """4-bit integer weights: w fp32 (N, K) -> (q uint8 (N, K/2), scales bf16
+    (K/group, N), zeros uint8 (K/group, N), or None when symmetric)."""
+    L = load_library()
+    _need(w, "w", torch.float32, 2)
+    N, K = w.shape
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    if out is None:
+        q = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
+        s = torch.empty((K // group, N), dtype=torch.bfloat16, device=w.device)
+        z = None if symmetric else torch.empty((K // group, N), dtype=torch.uint8, device=w.device)
+    else:
+        q = _out(out[0], "out[0]", torch.uint8, (N, K // 2), w)
+        s = _out(out[1], "out[1]", torch.bfloat16, (K // group, N), w)
+        z = None if symmetric else _out(out[2], "out[2]", torch.uint8, (K // group, N), w)
+    _check("fp8_quant_int4", L.fp8_quant_int4(_ptr(w), N, K, group, _ptr(q), _ptr(s),
+                                              _ptr(z) if z is not None else None, _stream(w)))
+    return q, s, z
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, workspace=None) -> torch.Tensor:
+    """Scales the tensors of `grads` (fp32, bf16 or fp16, contiguous, any mix)
+    by min(1, max_norm / (norm + 1e-6)), norm being the 2-norm over all of
+    them, and returns norm (0-dim fp32, on the device).  In place unless `out`
+    gives one tensor per gradient."""
+    L = load_library()
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if not grads:
+        raise ValueError("clip_grad_norm: no gradients")
+    if len(outs) != len(grads):
+        raise ValueError("clip_grad_norm: out must hold one tensor per gradient")
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        for t, name in ((g, f"grads[{i}]"), (o, f"out[{i}]")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype not in CLIP_TYPES:
+                raise TypeError(f"{name} must be fp32, bf16 or fp16, got {t.dtype}")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a GPU tensor (no CPU path exists)")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if o.shape != g.shape or o.dtype != g.dtype:
+            raise ValueError(f"out[{i}] must have the shape and type of grads[{i}]")
+    _same_device(*grads, *outs)
+    n = len(grads)
+    P = ctypes.c_void_p
+    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    types = (ctypes.c_int32 * n)(*[CLIP_TYPES[g.dtype] for g in grads])
+    gp, op = (P * n)(*[g.data_ptr() for g in grads]), (P * n)(*[o.data_ptr() for o in outs])
+    norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_clip_workspace_size(sizes, n)), grads[0])
+    _check("fp8_clip_grad_norm", L.fp8_clip_grad_norm(gp, op, sizes, types, n, float(max_norm), _ptr(norm), ws,
+                                                      ws_bytes, _stream(grads[0])))
+    return norm

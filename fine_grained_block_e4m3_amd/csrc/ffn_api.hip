@@ -1,0 +1,435 @@
+// ffn_api.hip -- host side of the feed-forward operators of libfp8gemm.so:
+// the gated block and its gradient, 4-bit matrix-vector products, and the
+// gradient norm with clipping (declared in include/fp8gemm.h).
+//
+// As in fp8gemm_api.hip every entry point validates on the host, enqueues
+// nothing on an error, launches on the caller's stream, and neither
+// allocates, frees nor synchronizes.
+#include "host_common.h"
+#include "kernels_clip.h"
+#include "kernels_decode.h"
+#include "kernels_exact.h"
+#include "kernels_gated_grad.h"
+#include "kernels_skinny.h"
+
+namespace {
+
+using namespace fp8h;
+
+constexpr int64_t kMaxSkinnyM = 16;
+constexpr int64_t kMaxDecodeM = 64;
+
+bool act_ok(int32_t act) { return act == FP8_ACT_SILU || act == FP8_ACT_GELU; }
+
+// ---------------------------------------------------------------------------
+// Gated block, forward.
+// ---------------------------------------------------------------------------
+enum GatedOutputs : int32_t { kOutH = 0, kOutSave = 1, kOutQuant = 2 };
+
+// Decode-sized M: workgroups along K per 96-column tile of either projection.
+constexpr int kDecodeTile = 96, kDecodeWaves = 3, kDecodeChunk = 4;
+constexpr int decode_kbmax(int64_t M) { return M <= 32 ? 24 : 12; }   // X-resident kernel: K blocks per workgroup
+int64_t gated_splits(int64_t N, int64_t K, int cus) {
+    const int64_t tiles = 2 * cdiv(N, kDecodeTile);
+    int64_t s = tiles < cus ? cus / tiles : 1;
+    if (s > K / 128) s = K / 128;
+    return s > 8 ? 8 : s;
+}
+bool gated_skinny(int64_t M, int32_t outputs) { return M <= kMaxSkinnyM && outputs == kOutH; }
+size_t gated_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t outputs, int cus) {
+    if (M > kMaxDecodeM || gated_skinny(M, outputs)) return 0;
+    return (size_t)(2 * gated_splits(N, K, cus) * M * N) * sizeof(float);
+}
+
+template <int BM, int BN, int WM, int WN, bool POW2, int STAGES, bool QOUT = false>
+fp8_status launch_gated_tile(fp8k::GemmParams p, int cus, hipStream_t stream) {
+    p.m_tiles = (int)cdiv(p.M, BM);
+    p.n_tiles = (int)cdiv(p.N, BN / 2);
+    p.group_m = 4;
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    const int grid = (int)(tiles < cus ? tiles : cus);
+    hipLaunchKernelGGL((fp8k::gemm_exact_kernel<BM, BN, WM, WN, fp8k::kDense, POW2, STAGES, QOUT, true>), dim3(grid),
+                       dim3(64 * WM * WN), 0, stream, p.xq, p.sa, p.wq, p.sb, p.y, p.m_indices, p.masked_m, p);
+    return launch_status();
+}
+
+// Largest tile that still gives every compute unit one.
+template <bool POW2>
+fp8_status run_gated_tiles(const fp8k::GemmParams& p, bool quant, int cus, hipStream_t stream) {
+    const bool big = cdiv(p.M, 256) * cdiv(p.N, 128) >= cus;
+    if (quant)
+        return big ? launch_gated_tile<256, 256, 4, 2, POW2, 2, true>(p, cus, stream)
+                   : launch_gated_tile<128, 256, 2, 4, POW2, 3, true>(p, cus, stream);
+    if (big) return launch_gated_tile<256, 256, 4, 2, POW2, 2>(p, cus, stream);
+    if (cdiv(p.M, 128) * cdiv(p.N, 128) >= cus) return launch_gated_tile<128, 256, 2, 4, POW2, 3>(p, cus, stream);
+    if (cdiv(p.M, 128) * cdiv(p.N, 64) >= cus) return launch_gated_tile<128, 128, 2, 2, POW2, 4>(p, cus, stream);
+    return launch_gated_tile<64, 128, 2, 2, POW2, 4>(p, cus, stream);
+}
+
+// Decode-sized M: partial sums of both projections, then the joining kernel.
+template <int MSUB>
+void launch_gated_decode(const fp8k::GemmParams& p, int64_t splits, hipStream_t stream) {
+    const dim3 grid((unsigned)cdiv(p.N, kDecodeTile), (unsigned)splits, 2), block(64 * kDecodeWaves);
+    if (cdiv(p.K / 128, splits) <= decode_kbmax(p.M))
+        hipLaunchKernelGGL((fp8k::decode_exact_x_kernel<MSUB, kDecodeWaves, 4, MSUB == 1 ? 24 : 12, true>), grid, block,
+                           0, stream, p.xq, p.sa, p.wq, p.sb, p.y, p);
+    else
+        hipLaunchKernelGGL((fp8k::decode_exact_kernel<MSUB, kDecodeWaves, 5, kDecodeChunk, true>), grid, block, 0,
+                           stream, p.xq, p.sa, p.wq, p.sb, p.y, p);
+}
+
+fp8_status run_gated_decode(const fp8k::GemmParams& p, bool quant, bool pow2, int64_t splits, hipStream_t stream) {
+    if (p.M <= 32) launch_gated_decode<1>(p, splits, stream);
+    else launch_gated_decode<2>(p, splits, stream);
+    const fp8_status st = launch_status();
+    if (st != FP8_OK) return st;
+    const dim3 grid((unsigned)cdiv(p.M * cdiv(p.N, 128), 4)), block(256);
+    const int s = (int)splits;
+    if (!quant) hipLaunchKernelGGL((fp8k::decode_gated_reduce<false, false>), grid, block, 0, stream, p, s);
+    else if (pow2) hipLaunchKernelGGL((fp8k::decode_gated_reduce<true, true>), grid, block, 0, stream, p, s);
+    else hipLaunchKernelGGL((fp8k::decode_gated_reduce<true, false>), grid, block, 0, stream, p, s);
+    return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Up to 16 tokens.
+// ---------------------------------------------------------------------------
+template <int FMT, bool GATED, int RT, int KW, int U, int GROUP, bool ZEROS>
+fp8_status launch_skinny(const fp8k::SkinnyParams& p, hipStream_t stream) {
+    const int64_t cols = GATED ? 8 * RT : 16 * RT;
+    hipLaunchKernelGGL((fp8k::skinny_kernel<FMT, GATED, RT, KW, U, GROUP, ZEROS>), dim3((unsigned)cdiv(p.N, cols)),
+                       dim3(64 * KW), 0, stream, p);
+    return launch_status();
+}
+
+template <int FMT, bool GATED, int GROUP, bool ZEROS>
+fp8_status run_skinny(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
+    // rows of weights per compute unit decide between one 16-row tile per
+    // workgroup and two
+    const int64_t tiles = cdiv(p.N * (GATED ? 2 : 1), 16);
+    if (tiles < 4 * cus) return launch_skinny<FMT, GATED, 1, 8, 2, GROUP, ZEROS>(p, stream);
+    return launch_skinny<FMT, GATED, 2, 8, 2, GROUP, ZEROS>(p, stream);
+}
+
+template <bool GATED>
+fp8_status run_gemv_w4(const fp8k::SkinnyParams& p, int32_t group, hipStream_t stream) {
+    int cus = 0;
+    const fp8_status st = current_device_cus(&cus);
+    if (st != FP8_OK) return st;
+    const bool z = p.z[0] != nullptr;
+    switch (group) {
+        case FP8_W4_MXFP4: return run_skinny<fp8k::kSkinnyMxfp4, GATED, 32, false>(p, cus, stream);
+        case 32:
+            return z ? run_skinny<fp8k::kSkinnyInt4, GATED, 32, true>(p, cus, stream)
+                     : run_skinny<fp8k::kSkinnyInt4, GATED, 32, false>(p, cus, stream);
+        case 64:
+            return z ? run_skinny<fp8k::kSkinnyInt4, GATED, 64, true>(p, cus, stream)
+                     : run_skinny<fp8k::kSkinnyInt4, GATED, 64, false>(p, cus, stream);
+        default:
+            return z ? run_skinny<fp8k::kSkinnyInt4, GATED, 128, true>(p, cus, stream)
+                     : run_skinny<fp8k::kSkinnyInt4, GATED, 128, false>(p, cus, stream);
+    }
+}
+
+fp8_status check_gemv(int64_t M, int64_t N, int64_t K, int32_t group) {
+    if (!dims_ok(M) || !dims_ok(N) || !dims_ok(K) ||
+        !(group == FP8_W4_MXFP4 || group == 32 || group == 64 || group == 128))
+        return FP8_ERR_INVALID_ARG;
+    if (K % 128 || K == 0 || M > kMaxSkinnyM) return FP8_ERR_SHAPE;
+    if (K > kMaxGemmK) return FP8_ERR_UNSUPPORTED;
+    return FP8_OK;
+}
+
+fp8_status check_gated(int64_t M, int64_t N, int64_t K, int32_t act, uint32_t flags) {
+    if (!dims_ok(M) || !dims_ok(N) || !dims_ok(K) || !act_ok(act) || (flags & ~FP8_FLAG_UE8M0))
+        return FP8_ERR_INVALID_ARG;
+    if (K % 128) return FP8_ERR_SHAPE;
+    if (K > kMaxGemmK) return FP8_ERR_UNSUPPORTED;
+    return FP8_OK;
+}
+
+fp8_status run_gated(fp8k::GemmParams& p, int32_t outputs, uint32_t flags, void* ws, size_t ws_bytes,
+                     hipStream_t stream) {
+    int cus = 0;
+    const fp8_status st = current_device_cus(&cus);
+    if (st != FP8_OK) return st;
+    if (gated_skinny(p.M, outputs)) {
+        fp8k::SkinnyParams q{};
+        q.x = p.xq; q.sa = p.sa; q.w[0] = p.wq; q.w[1] = p.wq2; q.s[0] = p.sb; q.s[1] = p.sb2;
+        q.y = p.y; q.M = p.M; q.N = p.N; q.K = p.K; q.act = p.act;
+        return run_skinny<fp8k::kSkinnyE4m3, true, 128, false>(q, cus, stream);
+    }
+    const bool quant = outputs == kOutQuant, pow2 = flags & FP8_FLAG_UE8M0;
+    const size_t need = gated_ws_bytes(p.M, p.N, p.K, outputs, cus);
+    if (need && ws_bytes >= need) {
+        p.part = static_cast<float*>(ws);
+        return run_gated_decode(p, quant, pow2, gated_splits(p.N, p.K, cus), stream);
+    }
+    return pow2 ? run_gated_tiles<true>(p, quant, cus, stream) : run_gated_tiles<false>(p, quant, cus, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the gated block.
+// ---------------------------------------------------------------------------
+int64_t grad_np(int64_t N) { return cdiv(N, 64) * 64; }
+
+template <int BM, int BN, int WM, int WN, int STAGES>
+fp8_status launch_grad(fp8k::GatedGradParams p, hipStream_t stream) {
+    const int64_t nt = cdiv(p.K, BN);
+    const int64_t dx = p.dx ? cdiv(p.M, BM) * nt : 0, dw = p.dw[0] ? 2 * cdiv(p.N, BM) * nt : 0;
+    if (dx + dw > 0x7FFFFFFF) return FP8_ERR_UNSUPPORTED;
+    if (dx + dw == 0) return FP8_OK;
+    p.dx_tiles = (int32_t)dx;
+    hipLaunchKernelGGL((fp8k::gated_grad_gemm_kernel<BM, BN, WM, WN, STAGES>), dim3((unsigned)(dx + dw)),
+                       dim3(64 * WM * WN), 0, stream, p);
+    return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Gradient clipping.
+// ---------------------------------------------------------------------------
+int64_t clip_chunks(int64_t n) { return cdiv(n, fp8k::kClipChunk); }
+int clip_grid(int64_t chunks) { return (int)(chunks < fp8k::kClipMaxGrid ? chunks : fp8k::kClipMaxGrid); }
+
+// Calls f(first tensor, tensors, chunks) for each batch of the call.
+template <typename F>
+fp8_status clip_batches(const int64_t* sizes, int32_t count, F&& f) {
+    for (int32_t i = 0; i < count;) {
+        int64_t chunks = 0;
+        int32_t k = 0;
+        for (; k < fp8k::kClipBatch && i + k < count; ++k) {
+            const int64_t c = clip_chunks(sizes[i + k]);
+            if (chunks + c > 0x7FFFFFFF) break;
+            chunks += c;
+        }
+        if (k == 0) return FP8_ERR_UNSUPPORTED;     // one tensor of over 2^44 elements
+        const fp8_status st = f(i, k, chunks);
+        if (st != FP8_OK) return st;
+        i += k;
+    }
+    return FP8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fp8_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t outputs) {
+    if (!dims_ok(M) || !dims_ok(N) || !dims_ok(K) || K % 128 || M == 0 || N == 0 || K == 0 || outputs < 0 ||
+        outputs > 2)
+        return 0;
+    int cus = 0;
+    if (current_device_cus(&cus) != FP8_OK) return 0;
+    return gated_ws_bytes(M, N, K, outputs, cus);
+}
+
+fp8_status fp8_gated_nt(const uint8_t* xq, const float* sa, const uint8_t* wgq, const float* sbg,
+                        const uint8_t* wuq, const float* sbu, uint16_t* h, uint16_t* g, uint16_t* u, int64_t M,
+                        int64_t N, int64_t K, int32_t act, uint32_t flags, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    const fp8_status st = check_gated(M, N, K, act, flags);
+    if (st != FP8_OK) return st;
+    if (M == 0 || N == 0) return FP8_OK;
+    if (K == 0) return FP8_ERR_SHAPE;
+    if (!xq || !sa || !wgq || !sbg || !wuq || !sbu || !h || (!g != !u) || (workspace_bytes && !workspace))
+        return FP8_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)xq, (const void*)sa, (const void*)wgq, (const void*)sbg, (const void*)wuq,
+                          (const void*)sbu, (const void*)h, (const void*)g, (const void*)u, (const void*)workspace})
+        if (!aligned16(p)) return FP8_ERR_ALIGNMENT;
+    fp8k::GemmParams p{};
+    p.xq = xq; p.sa = sa; p.wq = wgq; p.sb = sbg; p.wq2 = wuq; p.sb2 = sbu;
+    p.y = h; p.g_out = g; p.u_out = u; p.act = act;
+    p.M = M; p.N = N; p.K = K; p.E = 1;
+    return run_gated(p, g ? kOutSave : kOutH, flags, workspace, workspace ? workspace_bytes : 0, (hipStream_t)stream);
+}
+
+fp8_status fp8_gated_nt_qout(const uint8_t* xq, const float* sa, const uint8_t* wgq, const float* sbg,
+                             const uint8_t* wuq, const float* sbu, uint8_t* hq, float* sh, int64_t M, int64_t N,
+                             int64_t K, int32_t act, uint32_t flags, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    const fp8_status st = check_gated(M, N, K, act, flags);
+    if (st != FP8_OK) return st;
+    if (N % 128) return FP8_ERR_SHAPE;
+    if (M == 0 || N == 0) return FP8_OK;
+    if (K == 0) return FP8_ERR_SHAPE;
+    if (!xq || !sa || !wgq || !sbg || !wuq || !sbu || !hq || !sh || (workspace_bytes && !workspace))
+        return FP8_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)xq, (const void*)sa, (const void*)wgq, (const void*)sbg, (const void*)wuq,
+                          (const void*)sbu, (const void*)hq, (const void*)sh, (const void*)workspace})
+        if (!aligned16(p)) return FP8_ERR_ALIGNMENT;
+    fp8k::GemmParams p{};
+    p.xq = xq; p.sa = sa; p.wq = wgq; p.sb = sbg; p.wq2 = wuq; p.sb2 = sbu;
+    p.yq = hq; p.sy = sh; p.act = act;
+    p.M = M; p.N = N; p.K = K; p.E = 1;
+    return run_gated(p, kOutQuant, flags, workspace, workspace ? workspace_bytes : 0, (hipStream_t)stream);
+}
+
+size_t fp8_gated_grad_workspace_size(int64_t M, int64_t N) {
+    if (!dims_ok(M) || !dims_ok(N)) return 0;
+    return (size_t)(2 * M * grad_np(N)) * sizeof(uint16_t);
+}
+
+fp8_status fp8_gated_nt_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, const uint16_t* x,
+                             const uint16_t* wg, const uint16_t* wu, uint16_t* dx, uint16_t* dwg, uint16_t* dwu,
+                             int64_t M, int64_t N, int64_t K, int32_t act, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    if (!dims_ok(M) || !dims_ok(N) || !dims_ok(K) || !act_ok(act)) return FP8_ERR_INVALID_ARG;
+    if (K % 128) return FP8_ERR_SHAPE;
+    if (K > kMaxGemmK || N > kMaxGemmK - 64) return FP8_ERR_UNSUPPORTED;
+    if (K == 0 || (M == 0 && N == 0) || (!dx && !dwg && !dwu)) return FP8_OK;
+    if (!dwg != !dwu) return FP8_ERR_INVALID_ARG;
+    if (M && N && (!dh || !g || !u)) return FP8_ERR_INVALID_ARG;
+    if ((M && !x && dwg) || (N && (!wg || !wu) && dx)) return FP8_ERR_INVALID_ARG;
+    const size_t need = fp8_gated_grad_workspace_size(M, N);
+    if (need && !workspace) return FP8_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return FP8_ERR_SCRATCH;
+    for (const void* p : {(const void*)dh, (const void*)g, (const void*)u, (const void*)x, (const void*)wg,
+                          (const void*)wu, (const void*)dx, (const void*)dwg, (const void*)dwu, (const void*)workspace})
+        if (!aligned16(p)) return FP8_ERR_ALIGNMENT;
+    int cus = 0;
+    fp8_status st = current_device_cus(&cus);
+    if (st != FP8_OK) return st;
+    fp8k::GatedGradParams p{};
+    p.dh = dh; p.g = g; p.u = u; p.x = x; p.w[0] = wg; p.w[1] = wu;
+    p.d = static_cast<uint16_t*>(workspace);
+    p.dx = M ? dx : nullptr; p.dw[0] = N ? dwg : nullptr; p.dw[1] = N ? dwu : nullptr;
+    p.M = M; p.N = N; p.K = K; p.NP = grad_np(N); p.act = act;
+    hipStream_t s = (hipStream_t)stream;
+    if (M && N) {
+        const int64_t blocks = cdiv(M * (p.NP / 8), 256);
+        if (blocks > 0x7FFFFFFF) return FP8_ERR_UNSUPPORTED;
+        if (N % 8 == 0)
+            hipLaunchKernelGGL(fp8k::gated_grad_act_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, p);
+        else
+            hipLaunchKernelGGL(fp8k::gated_grad_act_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, p);
+        st = launch_status();
+        if (st != FP8_OK) return st;
+    }
+    return launch_grad<256, 256, 2, 2, 4>(p, s);
+}
+
+fp8_status fp8_gemv_w4(const uint16_t* x, const uint8_t* w, const void* s, const uint8_t* z, uint16_t* y, int64_t M,
+                       int64_t N, int64_t K, int32_t group, void* stream) {
+    const fp8_status st = check_gemv(M, N, K, group);
+    if (st != FP8_OK) return st;
+    if (M == 0 || N == 0) return FP8_OK;
+    if (!x || !w || !s || !y || (z && group == FP8_W4_MXFP4)) return FP8_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)x, (const void*)w, s, (const void*)z, (const void*)y})
+        if (!aligned16(p)) return FP8_ERR_ALIGNMENT;
+    fp8k::SkinnyParams p{};
+    p.x = x; p.w[0] = w; p.s[0] = s; p.z[0] = z; p.y = y;
+    p.M = M; p.N = N; p.K = K;
+    return run_gemv_w4<false>(p, group, (hipStream_t)stream);
+}
+
+fp8_status fp8_gated_gemv_w4(const uint16_t* x, const uint8_t* wg, const void* sg, const uint8_t* zg,
+                             const uint8_t* wu, const void* su, const uint8_t* zu, uint16_t* y, int64_t M, int64_t N,
+                             int64_t K, int32_t group, int32_t act, void* stream) {
+    const fp8_status st = check_gemv(M, N, K, group);
+    if (st != FP8_OK) return st;
+    if (!act_ok(act)) return FP8_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return FP8_OK;
+    if (!x || !wg || !sg || !wu || !su || !y || (zg && group == FP8_W4_MXFP4) || (!zg != !zu))
+        return FP8_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)x, (const void*)wg, sg, (const void*)zg, (const void*)wu, su, (const void*)zu,
+                          (const void*)y})
+        if (!aligned16(p)) return FP8_ERR_ALIGNMENT;
+    fp8k::SkinnyParams p{};
+    p.x = x; p.w[0] = wg; p.w[1] = wu; p.s[0] = sg; p.s[1] = su; p.z[0] = zg; p.z[1] = zu; p.y = y;
+    p.M = M; p.N = N; p.K = K; p.act = act;
+    return run_gemv_w4<true>(p, group, (hipStream_t)stream);
+}
+
+fp8_status fp8_quant_int4(const float* w, int64_t N, int64_t K, int32_t group, uint8_t* q, uint16_t* s, uint8_t* z,
+                          void* stream) {
+    if (!dims_ok(N) || !dims_ok(K) || !(group == 32 || group == 64 || group == 128)) return FP8_ERR_INVALID_ARG;
+    if (K % 128) return FP8_ERR_SHAPE;
+    if (N == 0 || K == 0) return FP8_OK;
+    if (!w || !q || !s) return FP8_ERR_INVALID_ARG;
+    if (!aligned16(w) || !aligned16(q) || !aligned16(s) || !aligned16(z)) return FP8_ERR_ALIGNMENT;
+    int cus = 0;
+    const fp8_status st = current_device_cus(&cus);
+    if (st != FP8_OK) return st;
+    const int64_t blocks = cdiv(N * (K / group), 256 / (group / 4));
+    if (blocks > 0x7FFFFFFF) return FP8_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)blocks), block(256);
+    hipStream_t t = (hipStream_t)stream;
+    if (group == 32) hipLaunchKernelGGL(fp8k::quant_int4_kernel<32>, grid, block, 0, t, w, q, s, z, N, K);
+    else if (group == 64) hipLaunchKernelGGL(fp8k::quant_int4_kernel<64>, grid, block, 0, t, w, q, s, z, N, K);
+    else hipLaunchKernelGGL(fp8k::quant_int4_kernel<128>, grid, block, 0, t, w, q, s, z, N, K);
+    return launch_status();
+}
+
+size_t fp8_clip_workspace_size(const int64_t* sizes, int32_t count) {
+    if (count < 0 || (count && !sizes)) return 0;
+    size_t slots = 0;
+    for (int32_t i = 0; i < count; ++i)
+        if (sizes[i] < 0) return 0;
+    (void)clip_batches(sizes, count, [&](int32_t, int32_t, int64_t chunks) {
+        slots += (size_t)clip_grid(chunks);
+        return FP8_OK;
+    });
+    return 8 * (slots ? slots : 1);
+}
+
+fp8_status fp8_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types,
+                              int32_t count, float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    if (count < 0 || !(max_norm >= 0.f) || !norm || (count && (!grads || !outs || !sizes || !types)))
+        return FP8_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < count; ++i) {
+        if (sizes[i] < 0 || types[i] < FP8_TYPE_F32 || types[i] > FP8_TYPE_F16) return FP8_ERR_INVALID_ARG;
+        if (sizes[i] && (!grads[i] || !outs[i])) return FP8_ERR_INVALID_ARG;
+        const uintptr_t mask = types[i] == FP8_TYPE_F32 ? 3 : 1;
+        if (((uintptr_t)grads[i] | (uintptr_t)outs[i]) & mask) return FP8_ERR_ALIGNMENT;
+    }
+    if (((uintptr_t)norm & 3) || ((uintptr_t)workspace & 7)) return FP8_ERR_ALIGNMENT;
+    if (!workspace) return FP8_ERR_INVALID_ARG;
+    if (workspace_bytes < fp8_clip_workspace_size(sizes, count)) return FP8_ERR_SCRATCH;
+    int cus = 0;
+    fp8_status st = current_device_cus(&cus);
+    if (st != FP8_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    double* slots = static_cast<double*>(workspace);
+    auto table = [&](int32_t i, int32_t k) {
+        fp8k::ClipTable t{};
+        int64_t chunks = 0;
+        for (int32_t j = 0; j < k; ++j) {
+            t.in[j] = grads[i + j];
+            t.out[j] = outs[i + j];
+            t.n_type[j] = 4 * sizes[i + j] + types[i + j];
+            t.first[j] = (int32_t)chunks;
+            chunks += clip_chunks(sizes[i + j]);
+        }
+        t.first[k] = (int32_t)chunks;
+        t.count = k;
+        return t;
+    };
+    int64_t used = 0;
+    st = clip_batches(sizes, count, [&](int32_t i, int32_t k, int64_t chunks) {
+        if (chunks == 0) return FP8_OK;
+        hipLaunchKernelGGL(fp8k::clip_norm_kernel, dim3(clip_grid(chunks)), dim3(256), 0, s, table(i, k), slots + used);
+        used += clip_grid(chunks);
+        return launch_status();
+    });
+    if (st != FP8_OK) return st;
+    if (used > fp8k::kClipMaxSlots) {
+        hipLaunchKernelGGL(fp8k::clip_join_kernel, dim3(1), dim3(256), 0, s, slots, (int)used);
+        st = launch_status();
+        if (st != FP8_OK) return st;
+        used = 1;
+    }
+    if (used == 0) {    // nothing to scale: the norm is 0
+        hipLaunchKernelGGL(fp8k::clip_scale_kernel, dim3(1), dim3(256), 0, s, fp8k::ClipTable{}, slots, 0, max_norm, norm);
+        return launch_status();
+    }
+    return clip_batches(sizes, count, [&](int32_t i, int32_t k, int64_t chunks) {
+        if (chunks == 0) return FP8_OK;
+        hipLaunchKernelGGL(fp8k::clip_scale_kernel, dim3(clip_grid(chunks)), dim3(256), 0, s, table(i, k), slots,
+                           (int)used, max_norm, norm);
+        norm = nullptr;     // written by the first launch
+        return launch_status();
+    });
+}
+
+}  // extern "C"

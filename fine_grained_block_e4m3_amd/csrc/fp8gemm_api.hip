@@ -8,10 +8,10 @@
 
 #include <stdint.h>
 
-#include <atomic>
 #include <mutex>
 
 #include "../../include/fp8gemm.h"
+#include "host_common.h"
 #include "kernels_decode.h"
 #include "kernels_exact.h"
 #include "kernels_gemm.h"
@@ -19,39 +19,9 @@
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;     // rows/cols fit int32 tile math
-constexpr int kMaxDevices = 64;
+using namespace fp8h;
+
 constexpr uint32_t kGemmFlags = FP8_FLAG_UE8M0 | FP8_FLAG_FAST_ACCUM;
-// Per-lane operand offsets inside a tile are 32-bit: 256 rows * K < 2^31.
-constexpr int64_t kMaxGemmK = (int64_t)1 << 22;
-
-// Per-device compute-unit count, filled once per device.
-std::atomic<int> g_cu_count[kMaxDevices];
-std::once_flag g_cu_once[kMaxDevices];
-
-fp8_status current_device_cus(int* cus) {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
-        (void)hipGetLastError();
-        return FP8_ERR_NO_DEVICE;
-    }
-    std::call_once(g_cu_once[dev], [dev]() {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
-            n = 0;
-        g_cu_count[dev].store(n);
-    });
-    const int n = g_cu_count[dev].load();
-    if (n <= 0) {
-        (void)hipGetLastError();
-        return FP8_ERR_NO_DEVICE;
-    }
-    *cus = n;
-    return FP8_OK;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 // Scratch of fp8_gemm_nt_noalloc: the split-K partial sums of the decode GEMM
 // in a fixed device array instead of a workspace the caller passes.  Every
 // GPU holds its own copy (from when the library is loaded on it until the
@@ -85,10 +55,6 @@ fp8_status current_device_scratch(void** ptr) {
     }
     *ptr = g_scratch_ptr[dev];
     return FP8_OK;
-}
-
-fp8_status launch_status() {
-    return hipGetLastError() == hipSuccess ? FP8_OK : FP8_ERR_LAUNCH;
 }
 
 // ---------------------------------------------------------------------------
@@ -141,8 +107,6 @@ fp8_status launch_exact(const fp8k::GemmParams& p, int cus, hipStream_t stream, 
 // count, so that fp8_gemm_plan can report it and tests can check it on the
 // host; the launches below follow the plan.
 // ---------------------------------------------------------------------------
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 enum Inst : int {
     // FP8-instruction kernel (FP8_FLAG_FAST_ACCUM, MX paths)
     kFastDecode, kFastDecodeKx, kFast64x96, kFast256x224, kFast256x256, kFast256x128, kFast128x128,
@@ -638,8 +602,6 @@ fp8_status run_gemm(const fp8k::GemmParams& p, uint32_t flags, void* ws, size_t 
                                     : run_plan<MODE, fp8k::kPathFp8>(pl, exact, p, ws, cus, stream, qout);
 }
 
-bool dims_ok(int64_t a) { return a >= 0 && a < kMaxDim; }
-
 // MXFP8 / MXFP4 weights: the dense FP8-instruction instances with the MX path
 // (scales as per-lane E8M0 operands, no promotion).
 template <int PATH>
@@ -664,7 +626,7 @@ const char* fp8_status_string(fp8_status s) {
         case FP8_ERR_UNSUPPORTED: return "unsupported configuration";
         case FP8_ERR_NO_DEVICE: return "no usable HIP device";
         case FP8_ERR_LAUNCH: return "kernel launch failed";
-        case FP8_ERR_SCRATCH: return "the problem needs more split-K scratch than fp8_gemm_nt_noalloc holds";
+        case FP8_ERR_SCRATCH: return "the workspace (fp8_gemm_nt_noalloc: the library's scratch) is too small";
     }
     return "unknown status";
 }

@@ -43,6 +43,11 @@ struct GemmParams {
     int32_t pair_cus;           // contiguous: > 0 when the tiles follow the pair schedule
                                 // built on the device (build_pair_sched), with this many
                                 // compute units in its full-round rule; 0: rows [m_lo, ...)
+    const uint8_t* wq2;         // gated: the up weight and its scales (wq, sb: the gate)
+    const float* sb2;
+    uint16_t* g_out;            // gated: BF16 g and u (M, N) for the gradient, or null
+    uint16_t* u_out;
+    int32_t act;                // gated: activation (FP8_ACT_*)
 };
 
 // Workgroup barrier without a memory fence.  Each wave has already waited on

@@ -59,13 +59,21 @@
 //     are walked largest expert first (gemm_common.h), so the dispatcher
 //     starts the longest ones first.  The tile body (kernels_exact_tile.inc)
 //     is instantiated once per number of valid subtiles.
+//   * Gated form (GATED: the gate and up projections of a feed-forward block,
+//     h = act(X Wg^T) * (X Wu^T)).  The tile's BN weight rows are BN/2 rows of
+//     each weight, alternating 32 gate rows and 32 up rows, so that the even
+//     and odd subtiles of a wave hold g and u of the same 32 output columns
+//     in the same registers of the same lanes: the activation and the product
+//     are lane-local in the epilogue, and one X tile feeds both projections.
 #pragma once
 
 #include "gemm_common.h"
+#include "gated_common.h"
 
 namespace fp8k {
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int MODE, bool POW2, int STAGES, bool QOUT = false>
+template <int BM, int BN, int WAVES_M, int WAVES_N, int MODE, bool POW2, int STAGES, bool QOUT = false,
+          bool GATED = false>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
     const uint8_t* __restrict__ xq_, const float* __restrict__ sa_, const uint8_t* __restrict__ wq_,
     const float* __restrict__ sb_, uint16_t* __restrict__ y_, const int32_t* __restrict__ m_indices_,
@@ -103,10 +111,16 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
     static_assert(BN / 128 + 2 <= 64, "one scale load covers the tile's weight blocks");
     static_assert(STAGES >= 2 && LDS_BYTES <= 160 * 1024, "LDS holds the stage ring");
     static_assert((STAGES - 2) * NPIECE <= 63 && PER <= 16, "vmcnt range");
-    static_assert(!QOUT || (MODE == kDense && TN == 128 && BN % 128 == 0),
-                  "quantized output: a 128-column group per wave");
+    static_assert(!QOUT || (MODE == kDense && (GATED ? BN == 256 : TN == 128 && BN % 128 == 0)),
+                  "quantized output: a 128-column group per wave (gated: per tile)");
+    static_assert(!GATED || (MODE == kDense && FJ % 2 == 0 && NXP % NWAVES == 0 && NWP % NWAVES == 0 &&
+                             (NWAVES == 4 || NWAVES == 8) && NWAVES >= NSA + 2),
+                  "gated: gate and up subtiles in pairs, whole pieces, a scale wave for each weight");
+    constexpr int ON = GATED ? BN / 2 : BN;   // output columns of a tile
 
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_BYTES];
+    // gated quantized output: each wave's row maxima, for the tile's 128-column group
+    __shared__ float gamax[GATED && QOUT ? WAVES_N * BM : 1];
 
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
@@ -148,6 +162,13 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
     const int rl = lane >> 3;
     const uint32_t voff0 = (uint32_t)((8 * wave + rl) * K) + (uint32_t)(((lane & 7) ^ rl ^ (wave & 1)) << 4);
     const uint32_t qstep = uniform((int)(8 * NWAVES * K));
+    // Gated: 8-row group f of the W tile lies in subtile f/4, an even subtile
+    // of gate rows or an odd one of up rows, at output columns
+    // 32*(f/8) + 8*(f%4).  With 8 waves piece q of wave w is in subtile
+    // 2q + w/4 (the weight depends on the wave, the columns advance by 32 per
+    // piece), with 4 waves in subtile q.
+    const uint32_t voffg = (uint32_t)((8 * (wave & 3) + rl) * K) + (uint32_t)(((lane & 7) ^ rl ^ (wave & 1)) << 4);
+    const uint32_t gstep = uniform((int)(32 * K));
     // fragment addresses within a stage: row r of a subtile, logical chunk
     // 4h + pr at slot (4h + pr) ^ lds_swz(r); subtile and stage offsets are
     // ds_read immediates (the swizzle depends on r mod 16 only)
@@ -187,7 +208,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
             }
         } else if (MODE == kContiguous && p.pair_cus > 0) {
             decode_tile_paired<BM, BN>(t, p, pair_ent, pair_sh, tc);
-        } else if (!decode_tile<MODE, BM, BN>(t, p, m_indices_, masked_m_, tc)) {
+        } else if (!decode_tile<MODE, BM, ON>(t, p, m_indices_, masked_m_, tc)) {
             continue;
         }
         const int64_t row0 = tc.row0, n0 = tc.n0;
@@ -199,11 +220,17 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
             sb += (int64_t)expert * (N / 128) * KB;
         }
         const int rows_valid = (int)min((int64_t)BM, tc.row_end - row0);
-        const int cols_valid = (int)min((int64_t)BN, N - n0);
+        const int cols_valid = (int)min((int64_t)ON, N - n0);
 
         // buffer resources: rows past the valid range read zeros
         const i32x4 xr = make_rsrc(xq_ + row0 * K, (uint32_t)(rows_valid * K));
-        const i32x4 wr = make_rsrc(wq + n0 * K, (uint32_t)(cols_valid * K));
+        // (gated, 8 waves: this wave's weight; 4 waves: wr gate, wr2 up)
+        const uint8_t* wq1 = GATED && NWAVES == 8 && wave >= 4 ? p.wq2 : wq;
+        const i32x4 wr = make_rsrc(wq1 + n0 * K, (uint32_t)(cols_valid * K));
+        i32x4 wr2 = wr;
+        if constexpr (GATED && NWAVES == 4) wr2 = make_rsrc(p.wq2 + n0 * K, (uint32_t)(cols_valid * K));
+        // gated: the scale waves load the gate's and the up weight's scales in turn
+        if constexpr (GATED) sb = (wave - NSA) & 1 ? p.sb2 : sb_;
         const int nb0 = (int)(n0 >> 7);
         const int nbl = (int)min((int64_t)(BN / 128 + 2), (N + 127) / 128 - nb0);
         // this wave's scale load: a base advancing adv bytes per K block, an
@@ -218,8 +245,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
         uint32_t sb_slot[FJ];
 #pragma unroll
         for (int b = 0; b < FJ; ++b) {
-            const int64_t n = n0 + wn * TN + 32 * b;
-            sb_slot[b] = (uint32_t)(SC_BASE + 256 * NSA + 4 * ((int)((n < N ? n : N - 1) >> 7) - nb0));
+            const int64_t n = GATED ? n0 + wn * (TN / 2) + 32 * (b / 2) : n0 + wn * TN + 32 * b;
+            sb_slot[b] = (uint32_t)(SC_BASE + 256 * (GATED ? NSA + b % 2 : NSA) +
+                                    4 * ((int)((n < N ? n : N - 1) >> 7) - nb0));
         }
 
         // Loads of K block kb into stage s: the ranges are cleared past the
@@ -235,7 +263,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
                 constexpr bool isx = P < XPER;
                 constexpr int q = isx ? P : P - XPER;
                 constexpr uint32_t stride = isx ? BM * 128 : BN * 128;
-                i32x4 r = isx ? xr : wr;
+                i32x4 r = isx ? xr : GATED && NWAVES == 4 && q % 2 ? wr2 : wr;
                 r[2] &= live;
                 uint32_t dst = ldsw + (uint32_t)((isx ? 0 : W_BASE) + q * NWAVES * 1024) + (uint32_t)L.s * stride;
                 if constexpr (q * NWAVES + NWAVES > (isx ? NXP : NWP)) {
@@ -245,7 +273,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
                         dst = lds0 + SPARE_BASE;
                     }
                 }
-                dma_lds16_one<0>(dst, voff0 + (uint32_t)q * qstep, r, L.kb * 128);
+                const uint32_t voff = GATED && !isx ? voffg + (uint32_t)(NWAVES == 8 ? q : q / 2) * gstep
+                                                    : voff0 + (uint32_t)q * qstep;
+                dma_lds16_one<0>(dst, voff, r, L.kb * 128);
             } else {
                 const uint64_t scb = sc_base + (uint64_t)(uint32_t)L.kb * sc_adv;
                 const i32x4 sr{(int)(uint32_t)scb, (int)(uint32_t)(scb >> 32) & 0xFFFF, (int)sc_rec & live, 0x00020000};

@@ -1,0 +1,314 @@
+// kernels_gated_grad.h -- gradient of the gated feed-forward block for gfx950.
+//
+// Forward: g = X Wg^T, u = X Wu^T, h = act(g) * u.  With dh given:
+//   dg = dh * u * act'(g),  du = dh * act(g)              (M, N)
+//   dX = dg Wg + du Wu                                    (M, K)
+//   dWg = dg^T X,  dWu = du^T X                           (N, K)
+// X, Wg, Wu, g, u, dh and the results are BF16; dg and du are formed in FP32
+// and rounded once to BF16, the type the matrix instruction takes (every
+// product is then exact in FP32 and the sums are FP32).
+//
+//   1. gated_grad_act_kernel writes dg and du, rows padded with zeros to a
+//      multiple of 64 columns (a stream: 6 bytes read, 4 written per element).
+//   2. gated_grad_gemm_kernel forms the products.  None of the operands is
+//      transposed in memory: an operand whose contraction runs along its rows'
+//      elements (dg, du in dX) is staged in LDS as 64-byte row pieces and read
+//      with ds_read_b128; one whose contraction runs over its rows (W in dX,
+//      dg, du and X in dW) is staged as it lies, 512 contiguous bytes of each
+//      of 32 rows, and read with ds_read_b64_tr_b16, which hands each lane
+//      four contraction steps of its column.
+#pragma once
+
+#include "gated_common.h"
+#include "gemm_common.h"
+
+namespace fp8k {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+struct GatedGradParams {
+    const uint16_t* dh;         // (M, N)
+    const uint16_t* g;
+    const uint16_t* u;
+    const uint16_t* x;          // (M, K)
+    const uint16_t* w[2];       // gate, up (N, K)
+    uint16_t* d;                // workspace: dg then du, each (M, NP)
+    uint16_t* dx;               // (M, K) or null
+    uint16_t* dw[2];            // (N, K) or null
+    int64_t M, N, K, NP;        // NP: N rounded up to a multiple of 64
+    int32_t act;
+    int32_t dx_tiles;           // workgroups of dX; those of dWg and dWu follow
+};
+
+// Eight elements of a row per thread.
+template <bool VEC>
+__global__ __launch_bounds__(256) void gated_grad_act_kernel(GatedGradParams p) {
+    const int64_t per_row = p.NP / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.M * per_row) return;
+    const int64_t m = i / per_row, n = (i - m * per_row) * 8;
+    const int64_t at = m * p.N + n;
+    i32x4 h{}, g{}, u{};
+    if (VEC ? n < p.N : n + 8 <= p.N) {
+        // VEC: N % 8 == 0, every row 16-byte aligned
+        __builtin_memcpy(&h, VEC ? __builtin_assume_aligned(p.dh + at, 16) : p.dh + at, 16);
+        __builtin_memcpy(&g, VEC ? __builtin_assume_aligned(p.g + at, 16) : p.g + at, 16);
+        __builtin_memcpy(&u, VEC ? __builtin_assume_aligned(p.u + at, 16) : p.u + at, 16);
+    } else if (!VEC) {
+        // the row's last elements; the padding stays zero
+        for (int j = 0; j < 8 && n + j < p.N; ++j) {
+            reinterpret_cast<uint16_t*>(&h)[j] = p.dh[at + j];
+            reinterpret_cast<uint16_t*>(&g)[j] = p.g[at + j];
+            reinterpret_cast<uint16_t*>(&u)[j] = p.u[at + j];
+        }
+    }
+    i32x4 dg, du;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a[2], b[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t sh = e ? 0 : 16;
+            const float hv = __uint_as_float(((uint32_t)h[j] << sh) & 0xFFFF0000u);
+            const float gv = __uint_as_float(((uint32_t)g[j] << sh) & 0xFFFF0000u);
+            const float uv = __uint_as_float(((uint32_t)u[j] << sh) & 0xFFFF0000u);
+            a[e] = hv * uv * gated_act_grad(p.act, gv);
+            b[e] = hv * gated_act(p.act, gv);
+        }
+        dg[j] = (int)pack_bf16x2(a[0], a[1]);
+        du[j] = (int)pack_bf16x2(b[0], b[1]);
+    }
+    i32x4* out = reinterpret_cast<i32x4*>(p.d + m * p.NP + n);
+    out[0] = dg;
+    out[p.M * p.NP / 8] = du;
+}
+
+// One operand of a product in LDS: a stage of 32 contraction steps of BX rows
+// of the result (or columns).  SLOW: the contraction runs over the operand's
+// memory rows.
+//   fast: LDS row of 64 bytes per result row, its four 16-byte chunks at slot
+//         chunk ^ (row / 4) % 4 (16 rows at one chunk cover all banks)
+//   slow: LDS row of 2 BX bytes per contraction step k, its 32-byte chunks at
+//         slot chunk ^ 2 (k % 4) (the 2 x 4 chunks that 32 lanes read cover all banks)
+template <int BX, int NWAVES, bool SLOW>
+struct GradOperand {
+    static constexpr int BYTES = BX * 64;
+    static constexpr int PIECES = BYTES / 1024;         // 1 KB wave loads
+    static constexpr int PER = PIECES / NWAVES;
+    static constexpr int ROWB = 2 * BX;                 // slow: bytes of an LDS row
+    static constexpr int KPP = 1024 / ROWB;             // slow: contraction steps per piece
+    static_assert(PIECES % NWAVES == 0 && BX >= 128 && BX <= 512, "whole pieces per wave");
+
+    // Byte offset of lane's 16 bytes of piece f from the stage's corner in memory.
+    static __device__ __forceinline__ uint32_t source(int f, int lane, uint32_t ld_bytes) {
+        if constexpr (SLOW) {
+            constexpr int LPK = 64 / KPP;               // lanes per contraction step
+            const int k = f * KPP + lane / LPK, pos = lane % LPK;
+            const int chunk = (pos >> 1) ^ (2 * (k & 3));
+            return (uint32_t)k * ld_bytes + 32 * chunk + 16 * (pos & 1);
+        } else {
+            const int row = 16 * f + (lane >> 2);
+            return (uint32_t)row * ld_bytes + 16 * ((lane & 3) ^ ((lane >> 4) & 3));
+        }
+    }
+    // Per-lane LDS offset of the 32-wide subtile at result row x0 + 32 a.
+    static __device__ __forceinline__ uint32_t fragment(int x0, int lane) {
+        if constexpr (SLOW) {
+            const int t = lane & 15, j = t >> 2, g = lane >> 4;
+            const int chunk = (x0 / 16 + (g & 1)) ^ (2 * j);
+            return (uint32_t)((8 * (g >> 1) + j) * ROWB + 32 * chunk + 8 * (t & 3));
+        } else {
+            return (uint32_t)((x0 + (lane & 31)) * 64);
+        }
+    }
+    // Operand of contraction steps 16 s .. 16 s + 15 (s = 0, 1) of a subtile:
+    // lane l holds steps 8 (l/32) .. + 7 of result row l%32.
+    static __device__ __forceinline__ bf16x8 read(FP8K_LDS const uint8_t* base, uint32_t frag, int s, int lane) {
+        if constexpr (SLOW) {
+            FP8K_LDS const uint8_t* at = base + frag + s * 16 * ROWB;
+            s16x4 v[2];
+            v[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP8K_LDS s16x4*)(at));
+            v[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP8K_LDS s16x4*)(at + 4 * ROWB));
+            return __builtin_bit_cast(bf16x8, v);
+        } else {
+            const uint32_t slot = (uint32_t)((2 * s + (lane >> 5)) ^ ((lane >> 2) & 3)) << 4;
+            return __builtin_bit_cast(bf16x8, *(FP8K_LDS const i32x4*)(base + frag + slot));
+        }
+    }
+};
+
+// One BM x BN tile of out (R, S) = sum over segments z of P_z Q_z, P the
+// operand of the result's rows and Q of its columns.  Per segment the
+// contraction has `len` steps; memory past an operand's end reads as zeros.
+struct GradTile {
+    const uint16_t* pb[2];      // corner of P and Q at contraction step 0
+    const uint16_t* qb[2];
+    int64_t p_elems, q_elems;   // elements from the corners to the operands' ends
+    int64_t p_ld, q_ld;         // elements between memory rows
+    int64_t p_step, q_step;     // elements per contraction step
+    int segs;
+    int64_t len;
+    uint16_t* out;              // result element (0, 0) of the tile
+    int64_t out_ld;
+    int rows, cols;             // valid part
+};
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, bool PSLOW>
+__device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
+    constexpr int NWAVES = WAVES_M * WAVES_N;
+    constexpr int TM = BM / WAVES_M, TN = BN / WAVES_N, FI = TM / 32, FJ = TN / 32;
+    using P = GradOperand<BM, NWAVES, PSLOW>;
+    using Q = GradOperand<BN, NWAVES, true>;
+    constexpr int STAGE = P::BYTES + Q::BYTES, NL = P::PER + Q::PER;
+    static_assert((STAGES - 2) * NL <= 63, "vmcnt range");
+
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int wm = wave % WAVES_M, wn = wave / WAVES_M;
+    const uint32_t lds0 = uniform((int)lds_addr(smem));
+    FP8K_LDS const uint8_t* lds = (FP8K_LDS const uint8_t*)smem;
+
+    uint32_t psrc[P::PER], qsrc[Q::PER];
+#pragma unroll
+    for (int i = 0; i < P::PER; ++i) psrc[i] = P::source(wave + i * NWAVES, lane, (uint32_t)(2 * t.p_ld));
+#pragma unroll
+    for (int i = 0; i < Q::PER; ++i) qsrc[i] = Q::source(wave + i * NWAVES, lane, (uint32_t)(2 * t.q_ld));
+    uint32_t pf[FI], qf[FJ];
+#pragma unroll
+    for (int a = 0; a < FI; ++a) pf[a] = P::fragment(wm * TM + 32 * a, lane);
+#pragma unroll
+    for (int b = 0; b < FJ; ++b) qf[b] = Q::fragment(wn * TN + 32 * b, lane);
+
+    const int per_seg = (int)((t.len + 31) / 32);
+    const int nblocks = per_seg * t.segs;
+    // The operands' corners advance block by block; a range that has run out
+    // (past the operand, or past the last block) reads zeros.
+    auto range = [](int64_t elems) FP8K_INLINE {
+        return (uint32_t)(elems <= 0 ? 0 : elems >= (1ll << 30) ? (1ll << 31) : 2 * elems);
+    };
+    auto issue = [&](int kb, int stage) FP8K_INLINE {
+        const int z = t.segs > 1 && kb >= per_seg ? 1 : 0;
+        const int64_t k0 = (int64_t)(kb - z * per_seg) * 32;
+        const bool live = kb < nblocks;
+        const i32x4 pr = make_rsrc(t.pb[z] + k0 * t.p_step, live ? range(t.p_elems - k0 * t.p_step) : 0u);
+        const i32x4 qr = make_rsrc(t.qb[z] + k0 * t.q_step, live ? range(t.q_elems - k0 * t.q_step) : 0u);
+        const uint32_t dst = lds0 + (uint32_t)(stage * STAGE + wave * 1024);
+#pragma unroll
+        for (int i = 0; i < P::PER; ++i) dma_lds16_one<0>(dst + i * NWAVES * 1024, psrc[i], pr, 0);
+#pragma unroll
+        for (int i = 0; i < Q::PER; ++i) dma_lds16_one<0>(dst + P::BYTES + i * NWAVES * 1024, qsrc[i], qr, 0);
+    };
+
+    f32x16 acc[FI][FJ];
+#pragma unroll
+    for (int a = 0; a < FI; ++a)
+#pragma unroll
+        for (int b = 0; b < FJ; ++b)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.f;
+
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
+
+    int stage = 0;
+    for (int kb = 0; kb < nblocks; ++kb) {
+        // this wave's loads of block kb have landed; every wave's have after
+        // the barrier, and every wave is past its reads of the stage that the
+        // next loads overwrite
+        wait_vmcnt<(STAGES - 2) * NL>();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        lds_barrier();
+        issue(kb + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+        FP8K_LDS const uint8_t* base = lds + stage * STAGE;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            bf16x8 pv[FI], qv[FJ];
+#pragma unroll
+            for (int a = 0; a < FI; ++a) pv[a] = P::read(base, pf[a], s, lane);
+#pragma unroll
+            for (int b = 0; b < FJ; ++b) qv[b] = Q::read(base + P::BYTES, qf[b], s, lane);
+#pragma unroll
+            for (int a = 0; a < FI; ++a)
+#pragma unroll
+                for (int b = 0; b < FJ; ++b)
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qv[b], pv[a], acc[a][b], 0, 0, 0);
+        }
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    wait_vmcnt<0>();
+
+    // lane l, value v of subtile (a, b): row 32a + l%32, column 32b + 8(v/4) + 4(l/32) + v%4
+    const int h = lane >> 5;
+#pragma unroll
+    for (int a = 0; a < FI; ++a) {
+        const int m = wm * TM + 32 * a + (lane & 31);
+        if (m >= t.rows) continue;
+#pragma unroll
+        for (int b = 0; b < FJ; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = wn * TN + 32 * b + 8 * q + 4 * h;
+                // K % 128 == 0: whole groups of 4 columns, 8-byte aligned
+                if (n < t.cols)
+                    *reinterpret_cast<uint2*>(t.out + (int64_t)m * t.out_ld + n) =
+                        make_uint2(pack_bf16x2(acc[a][b][4 * q], acc[a][b][4 * q + 1]),
+                                   pack_bf16x2(acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]));
+            }
+    }
+}
+
+// Workgroups [0, dx_tiles): tiles of dX; the rest: tiles of dWg, then of dWu.
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gated_grad_gemm_kernel(GatedGradParams p) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * (BM + BN) * 64];
+    const int nt = (int)((p.K + BN - 1) / BN);
+    // workgroup b of a dispatch wave lands on XCD b % 8: each XCD takes a run
+    // of consecutive tiles (and shares their operands in its L2)
+    auto run_of = [](int b, int count) FP8K_INLINE {
+        const int per = count / 8, rest = count % 8, xcd = b % 8;
+        return xcd * per + min(xcd, rest) + b / 8;
+    };
+    int mt, ntile;
+    GradTile t;
+    t.q_ld = t.q_step = p.K;
+    if ((int)blockIdx.x < p.dx_tiles) {
+        const int tile = run_of(blockIdx.x, p.dx_tiles);
+        raster(tile, (int)((p.M + BM - 1) / BM), nt, 4, mt, ntile);
+        const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)ntile * BN;
+        for (int z = 0; z < 2; ++z) {
+            t.pb[z] = p.d + (z * p.M + m0) * p.NP;
+            t.qb[z] = p.w[z] + n0;
+        }
+        t.p_elems = (p.M - m0) * p.NP;
+        t.q_elems = p.N * p.K - n0;
+        t.p_ld = p.NP;
+        t.p_step = 1;
+        t.segs = 2;
+        t.len = p.NP;
+        t.out = p.dx + m0 * p.K + n0;
+        t.out_ld = p.K;
+        t.rows = (int)min((int64_t)BM, p.M - m0);
+        t.cols = (int)min((int64_t)BN, p.K - n0);
+        grad_tile<BM, BN, WAVES_M, WAVES_N, STAGES, false>(t, smem);
+    } else {
+        const int rt = (int)((p.N + BM - 1) / BM);
+        const int tile = run_of(blockIdx.x - p.dx_tiles, 2 * rt * nt);
+        const int z = tile >= rt * nt;
+        raster(tile - z * rt * nt, rt, nt, 4, mt, ntile);
+        const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)ntile * BN;
+        t.pb[0] = t.pb[1] = p.d + z * p.M * p.NP + m0;
+        t.qb[0] = t.qb[1] = p.x + n0;
+        t.p_elems = p.M * p.NP - m0;
+        t.q_elems = p.M * p.K - n0;
+        t.p_ld = t.p_step = p.NP;
+        t.segs = 1;
+        t.len = p.M;
+        t.out = p.dw[z] + m0 * p.K + n0;
+        t.out_ld = p.K;
+        t.rows = (int)min((int64_t)BM, p.N - m0);
+        t.cols = (int)min((int64_t)BN, p.K - n0);
+        grad_tile<BM, BN, WAVES_M, WAVES_N, STAGES, true>(t, smem);
+    }
+}
+
+}  // namespace fp8k

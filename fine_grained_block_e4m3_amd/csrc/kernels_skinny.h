@@ -1,0 +1,351 @@
+// kernels_skinny.h -- products of up to 16 tokens with a weight matrix for
+// gfx950: matrix-vector products with 4-bit weights and group scales, and the
+// gated feed-forward block on up to 16 tokens (4-bit or E4M3 weights).
+//
+//   y[m][n] = sum_k x[m][k] w[n][k],  m < M <= 16
+//   gated:  y = act(x Wg^T) * (x Wu^T)
+// Weight formats (K % 128 == 0, codes row-major, two 4-bit codes per byte, the
+// even element low):
+//   kSkinnyMxfp4  w = E2M1 * 2^(e-127) per 32 along K, e packed [K/128][N]
+//                 (fp8_quant_mxfp4's layout); x BF16
+//   kSkinnyInt4   w = s * (q - z), q = 0..15, per group of 32, 64 or 128:
+//                 s BF16 [K/group][N], z u8 [K/group][N] or 8; x BF16
+//   kSkinnyE4m3   x and w E4M3 with 1x128 and 128x128 scales
+//
+// What bounds it: every weight is read once and used M times, so the weight
+// stream from HBM.  The kernel is therefore built around that stream:
+//   * Weights go from memory straight into the registers in which the matrix
+//     instruction takes them: lane (r, q) = (l%16, l/16) of a wave reads the
+//     16 bytes q of row r's 64-byte K block (128 4-bit weights), which are
+//     the four MFMA steps' operands.  No LDS, no barrier in the K loop.
+//   * v_mfma_f32_16x16x32 with the 16 weight rows as A and the tokens as B:
+//     tokens past M repeat the last one (their loads coalesce with it) and
+//     are not stored.  A vector-FMA form would spend M operations per weight;
+//     this one spends the decoding only, whatever M.
+//   * The KW waves of a workgroup share its rows and take every KW-th K
+//     block; one LDS exchange at the end adds their FP32 sums in wave order.
+//     With few rows this keeps every compute unit reading; no workspace and
+//     no second launch.
+//   * The loads of the next U blocks are issued before the U blocks at hand
+//     are multiplied.
+// Exactness: E2M1 times a power of two is a BF16 value (products exact, FP32
+// sums).  4-bit integers enter as the BF16 values 128 + q (an OR into the
+// mantissa: exact); the group's sum of x comes from the same instruction with
+// a matrix of ones, and s * (sum x (128 + q) - (128 + z) * sum x) is formed in
+// FP32 per group.  E4M3 is widened exactly to FP16.
+#pragma once
+
+#include "gated_common.h"
+#include "gemm_common.h"
+
+namespace fp8k {
+
+
+enum SkinnyFormat : int { kSkinnyMxfp4 = 0, kSkinnyInt4 = 1, kSkinnyE4m3 = 2 };
+
+struct SkinnyParams {
+    const void* x;          // BF16 (M, K), or E4M3 codes (M, K)
+    const float* sa;        // E4M3: activation scales [K/128][M]
+    const uint8_t* w[2];    // weight codes; gated: gate, up
+    const void* s[2];       // scales
+    const uint8_t* z[2];    // 4-bit integers: zero points, or null (8)
+    uint16_t* y;            // BF16 (M, N)
+    int64_t M, N, K;
+    int32_t act;
+};
+
+// Transposes a 4x4 block of dwords over the four lanes (r, 0..3): afterwards
+// v[s] of lane (r, q) is what v[q] of lane (r, s) was.
+__device__ __forceinline__ i32x4 transpose_quads(i32x4 v) {
+    const auto a = __builtin_amdgcn_permlane32_swap((unsigned)v[0], (unsigned)v[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap((unsigned)v[1], (unsigned)v[3], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return i32x4{(int)c[0], (int)c[1], (int)d[0], (int)d[1]};
+}
+
+// Eight 4-bit codes of a dword as the BF16 values 128 + q, in the order
+// 0, 4, 1, 5, 2, 6, 3, 7 (pairs four codes apart: one shift, one and-or each).
+__device__ __forceinline__ bf16x8 u4x8_to_bf16(int v) {
+    i32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = (int)((((uint32_t)v >> (4 * j)) & 0x000F000Fu) | 0x43004300u);
+    return __builtin_bit_cast(bf16x8, r);
+}
+// Eight BF16 values in that order.
+__device__ __forceinline__ bf16x8 bf16x8_u4_order(i32x4 x) {
+    // pairs (0,4) (1,5) (2,6) (3,7) of the halves of dwords 0,1 and 2,3
+    i32x4 r;
+    r[0] = (int)__builtin_amdgcn_perm((unsigned)x[2], (unsigned)x[0], 0x05040100u);
+    r[1] = (int)__builtin_amdgcn_perm((unsigned)x[2], (unsigned)x[0], 0x07060302u);
+    r[2] = (int)__builtin_amdgcn_perm((unsigned)x[3], (unsigned)x[1], 0x05040100u);
+    r[3] = (int)__builtin_amdgcn_perm((unsigned)x[3], (unsigned)x[1], 0x07060302u);
+    return __builtin_bit_cast(bf16x8, r);
+}
+// Eight E2M1 codes of a dword times the power of two `scale`, as BF16.
+__device__ __forceinline__ bf16x8 e2m1x8_to_bf16(int v, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((unsigned)v, scale, 0);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((unsigned)v, scale, 1);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((unsigned)v, scale, 2);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((unsigned)v, scale, 3);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
+
+// RT: 16-row weight tiles per workgroup; gated: even tiles hold gate rows, odd
+// ones the up rows of the same columns, and RT == 1 one tile of 8 gate and 8
+// up rows (more workgroups for narrow weights).  KW: waves along K.  U: K
+// blocks in flight per wave.  GROUP: group size of 4-bit integers.
+template <int FMT, bool GATED, int RT, int KW, int U, int GROUP, bool ZEROS>
+__global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
+    constexpr bool kMixed = GATED && RT == 1;
+    constexpr int COLS = GATED ? 8 * RT : 16 * RT;      // output columns of a workgroup
+    constexpr int WL = FMT == kSkinnyE4m3 ? 2 : 1;      // 16-byte weight loads per lane and block
+    constexpr int XL = FMT == kSkinnyE4m3 ? 2 : 4;      // 16-byte x loads per lane and block
+    constexpr bool kTranspose = FMT == kSkinnyInt4 && GROUP < 128;
+    constexpr int NG = FMT == kSkinnyInt4 ? 128 / GROUP : 1;   // groups per block
+    static_assert(!GATED || RT == 1 || RT % 2 == 0, "gate and up tiles in pairs");
+    __shared__ f32x4 sums[KW][RT][64];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    const int64_t N = p.N;
+    const int KB = (int)(p.K / 128);
+    const int64_t n0 = (int64_t)blockIdx.x * COLS;
+    const bool edge = n0 + COLS > N;
+
+    // operand row of this lane in each tile, and the first of the 4 result
+    // rows it holds (rows past N repeat the last one; they are not stored)
+    const uint8_t* wrow[RT];
+    const uint32_t* erow[RT];       // MXFP4: this lane's scale dwords
+    int wsel[RT];                   // result rows: which weight
+    int64_t nres[RT];
+    const int64_t row_bytes = FMT == kSkinnyE4m3 ? p.K : p.K / 2;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int wi = kMixed ? r >> 3 : GATED ? t & 1 : 0;
+        const int64_t n = min(n0 + (kMixed ? r & 7 : 16 * (GATED ? t >> 1 : t) + r), N - 1);
+        wrow[t] = p.w[wi] + n * row_bytes + 16 * WL * q;
+        erow[t] = reinterpret_cast<const uint32_t*>(p.s[wi]) + n;
+        wsel[t] = kMixed ? q >> 1 : GATED ? t & 1 : 0;
+        nres[t] = n0 + (kMixed ? 4 * (q & 1) : 16 * (GATED ? t >> 1 : t) + 4 * q);
+    }
+    const int64_t m = min((int64_t)r, p.M - 1);
+    // x of this lane's token: 4-bit with whole-block groups and E4M3: the 32
+    // elements 32q ..; transposed: elements 32 s + 8 q of step s
+    const uint8_t* xrow = static_cast<const uint8_t*>(p.x) + m * p.K * (FMT == kSkinnyE4m3 ? 1 : 2) +
+                          (FMT == kSkinnyE4m3 ? 32 * q : kTranspose ? 16 * q : 64 * q);
+
+    struct Block {
+        i32x4 w[RT][WL];
+        i32x4 x[XL];
+        uint32_t e[RT];             // MXFP4: scale dword of the operand row
+        uint32_t sl[RT][NG], sh[RT][NG];   // int4: 4 BF16 scales of the result rows
+        uint32_t zz[RT][NG];        // int4: 4 zero points
+        float sab[RT];              // E4M3: sa * sb of the result rows
+    };
+    auto load = [&](Block& b, int kb0) FP8K_INLINE {
+        const int kb = min(kb0, KB - 1);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+#pragma unroll
+            for (int i = 0; i < WL; ++i)
+                b.w[t][i] = __builtin_nontemporal_load(
+                    reinterpret_cast<const i32x4*>(wrow[t] + (int64_t)kb * 64 * WL + 16 * i));
+            if constexpr (FMT == kSkinnyMxfp4) b.e[t] = erow[t][(int64_t)kb * N];
+            if constexpr (FMT == kSkinnyE4m3) {
+                const int64_t nb = min(nres[t], N - 1) >> 7;
+                b.sab[t] = p.sa[(int64_t)kb * p.M + m] * static_cast<const float*>(p.s[wsel[t]])[nb * KB + kb];
+            }
+            if constexpr (FMT == kSkinnyInt4) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int64_t at = ((int64_t)kb * NG + g) * N;
+                    const uint16_t* sp = static_cast<const uint16_t*>(p.s[wsel[t]]) + at;
+                    const uint8_t* zp = ZEROS ? p.z[wsel[t]] + at : nullptr;
+                    if (!edge) {
+                        // 8 and 4 bytes, aligned to an element only when N is odd
+                        uint32_t v[2];
+                        __builtin_memcpy(v, sp + nres[t], 8);
+                        b.sl[t][g] = v[0];
+                        b.sh[t][g] = v[1];
+                        if constexpr (ZEROS) __builtin_memcpy(&b.zz[t][g], zp + nres[t], 4);
+                    } else {
+                        int64_t c[4];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) c[v] = min(nres[t] + v, N - 1);
+                        b.sl[t][g] = sp[c[0]] | (uint32_t)sp[c[1]] << 16;
+                        b.sh[t][g] = sp[c[2]] | (uint32_t)sp[c[3]] << 16;
+                        if constexpr (ZEROS)
+                            b.zz[t][g] = zp[c[0]] | (uint32_t)zp[c[1]] << 8 | (uint32_t)zp[c[2]] << 16 |
+                                         (uint32_t)zp[c[3]] << 24;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < XL; ++i)
+            b.x[i] = *reinterpret_cast<const i32x4*>(xrow + (int64_t)kb * (FMT == kSkinnyE4m3 ? 128 : 256) +
+                                                     (kTranspose ? 64 : 16) * i);
+    };
+
+    f32x4 acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    auto multiply = [&](const Block& b) FP8K_INLINE {
+        if constexpr (FMT == kSkinnyE4m3) {
+            f32x4 part[RT];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const f16x8 xv = e4m3x8_to_f16(b.x[s >> 1][2 * (s & 1)], b.x[s >> 1][2 * (s & 1) + 1]);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const f16x8 wv = e4m3x8_to_f16(b.w[t][s >> 1][2 * (s & 1)], b.w[t][s >> 1][2 * (s & 1) + 1]);
+                    part[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, xv, s ? part[t] : f32x4{}, 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(b.sab[t], part[t][v], acc[t][v]);
+        } else if constexpr (FMT == kSkinnyMxfp4) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const bf16x8 xv = __builtin_bit_cast(bf16x8, b.x[s]);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    // the lane's 32 weights are group q: its scale byte as an FP32 exponent
+                    const float sc = __uint_as_float((b.e[t] >> (8 * q) & 0xFFu) << 23);
+                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e2m1x8_to_bf16(b.w[t][0][s], sc), xv, acc[t],
+                                                                     0, 0, 0);
+                }
+            }
+        } else {
+            const bf16x8 ones = __builtin_bit_cast(bf16x8, i32x4{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80});
+            i32x4 wt[RT];
+#pragma unroll
+            for (int t = 0; t < RT; ++t) wt[t] = kTranspose ? transpose_quads(b.w[t][0]) : b.w[t][0];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                f32x4 part[RT], sx{};
+#pragma unroll
+                for (int t = 0; t < RT; ++t) part[t] = f32x4{};
+#pragma unroll
+                for (int i = 0; i < 4 / NG; ++i) {
+                    const int s = g * (4 / NG) + i;
+                    const bf16x8 xv = bf16x8_u4_order(b.x[s]);
+                    sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xv, sx, 0, 0, 0);
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u4x8_to_bf16(wt[t][s]), xv, part[t], 0, 0, 0);
+                }
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const uint32_t sw = v < 2 ? b.sl[t][g] : b.sh[t][g];
+                        const float sc = v & 1 ? __uint_as_float(sw & 0xFFFF0000u) : bf16_bits_to_f32(sw);
+                        const float off = ZEROS ? 128.f + (float)(b.zz[t][g] >> (8 * v) & 0xFFu) : 136.f;
+                        acc[t][v] = __builtin_fmaf(sc, __builtin_fmaf(-off, sx[0], part[t][v]), acc[t][v]);
+                    }
+            }
+        }
+    };
+
+    Block cur[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (wave + u * KW < KB) load(cur[u], wave + u * KW);
+    for (int kb = wave; kb < KB; kb += U * KW) {
+        Block next[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (kb + (U + u) * KW < KB) load(next[u], kb + (U + u) * KW);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (kb + u * KW < KB) multiply(cur[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) cur[u] = next[u];
+    }
+
+    // ---- join the waves' sums, in wave order; tile t by wave t % KW ----
+#pragma unroll
+    for (int t = 0; t < RT; ++t) sums[wave][t][lane] = acc[t];
+    __syncthreads();
+    auto total = [&](int t, int l) FP8K_INLINE {
+        f32x4 v = sums[0][t][l];
+        for (int w = 1; w < KW; ++w) v += sums[w][t][l];
+        return v;
+    };
+    constexpr int OT = GATED ? (RT + 1) / 2 : RT;       // result tiles
+    for (int t = wave; t < OT; t += KW) {
+        f32x4 v;
+        if constexpr (GATED) {
+            if (kMixed && q >= 2) continue;             // the up rows' lanes
+            const f32x4 g = total(kMixed ? 0 : 2 * t, lane), u = total(kMixed ? 0 : 2 * t + 1, kMixed ? lane + 32 : lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = gated_act(p.act, g[i]) * u[i];
+        } else {
+            v = total(t, lane);
+        }
+        if (r >= p.M) continue;
+        const int64_t n = n0 + 16 * t + 4 * q;
+        uint16_t* out = p.y + (int64_t)r * N + n;
+        const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
+        if ((N & 3) == 0 && n + 3 < N) {
+            *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+        } else {
+            if (n < N) out[0] = (uint16_t)(lo & 0xFFFF);
+            if (n + 1 < N) out[1] = (uint16_t)(lo >> 16);
+            if (n + 2 < N) out[2] = (uint16_t)(hi & 0xFFFF);
+            if (n + 3 < N) out[3] = (uint16_t)(hi >> 16);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit integer weights with group scales.  Asymmetric: lo = min(w, 0),
+// hi = max(w, 0), s = BF16((hi - lo) / 15), z = round(-lo / s) in [0, 15];
+// symmetric: s = BF16(amax / 7), z = 8; q = clamp(round(w / s) + z, 0, 15).
+// All roundings to nearest, ties to even, quotients correctly rounded; the
+// scale is at least BF16(1e-8), so a group of zeros is z everywhere.
+// One group per 8 lanes of 4 elements (group 32), 16 or 32 lanes; a stream.
+// ---------------------------------------------------------------------------
+template <int GROUP>
+__global__ __launch_bounds__(256) void quant_int4_kernel(const float* __restrict__ w, uint8_t* __restrict__ qd,
+                                                         uint16_t* __restrict__ s, uint8_t* __restrict__ z,
+                                                         int64_t N, int64_t K) {
+    constexpr int L = GROUP / 4;                        // lanes per group
+    const int64_t groups = K / GROUP;
+    const int64_t id = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const int64_t total = N * groups;
+    const int64_t at = min(id, total - 1);              // whole sub-waves stay active for the shuffles
+    const int64_t n = at / groups, g = at - n * groups;
+    const int i = (int)(threadIdx.x % L);
+    const f32x4 v = *reinterpret_cast<const f32x4*>(w + n * K + g * GROUP + 4 * i);
+    float lo = fminf(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), 0.f);
+    float hi = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), 0.f);
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) {
+        lo = fminf(lo, __shfl_xor(lo, o, L));
+        hi = fmaxf(hi, __shfl_xor(hi, o, L));
+    }
+    const float wide = z ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
+    const uint32_t sb = pack_bf16x2(fmaxf(wide, 1e-8f), 0.f) & 0xFFFFu;
+    const float sc = bf16_bits_to_f32(sb);
+    const float zp = z ? fminf(fmaxf(rintf(-lo / sc), 0.f), 15.f) : 8.f;
+    uint32_t c = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        c |= (uint32_t)fminf(fmaxf(rintf(v[j] / sc) + zp, 0.f), 15.f) << (4 * j);
+    if (id >= total) return;
+    *reinterpret_cast<uint16_t*>(qd + (n * K + g * GROUP) / 2 + 2 * i) = (uint16_t)c;
+    if (i == 0) {
+        s[g * N + n] = (uint16_t)sb;
+        if (z) z[g * N + n] = (uint8_t)zp;
+    }
+}
+
+}  // namespace fp8k

@@ -30,8 +30,9 @@
  *       FP8_ERR_ALIGNMENT    a pointer not 16-byte aligned
  *       FP8_ERR_NO_DEVICE    no HIP device is usable
  *       FP8_ERR_LAUNCH       the kernel launch reported an error
- *       FP8_ERR_SCRATCH      (fp8_gemm_nt_noalloc) the problem needs more
- *                            split-K scratch than its fixed array holds
+ *       FP8_ERR_SCRATCH      the workspace is smaller than the call needs
+ *                            (fp8_gemm_nt_noalloc: the problem needs more
+ *                            split-K scratch than its fixed array holds)
  *     A call with an empty problem (M == 0, E == 0, N == 0 ...) returns FP8_OK
  *     and enqueues nothing.  Device-side data (expert indices, valid counts)
  *     is never reported as an error: its handling is defined per call.
@@ -340,6 +341,134 @@ typedef struct {
 fp8_status fp8_gemm_plan(int32_t layout, int64_t M, int64_t N, int64_t K,
                          uint32_t flags, int32_t compute_units,
                          size_t workspace_bytes, fp8_gemm_plan_t* plan);
+
+/* ---------------------------------------------------------------------------
+ * Gated feed-forward block: both projections, the activation and the product.
+ *   g = X Wg^T,  u = X Wu^T,  h = act(g) * u
+ * ------------------------------------------------------------------------- */
+
+/* Activations.  SILU: act(g) = g / (1 + e^-g).  GELU (the tanh form):
+ * act(g) = g / (1 + e^-t), t = 2 sqrt(2/pi) (g + 0.044715 g^3). */
+#define FP8_ACT_SILU 0
+#define FP8_ACT_GELU 1
+
+/*
+ * Forward on block-scaled E4M3 operands.
+ *   xq u8 (M,K), sa fp32 [K/128][M], wgq and wuq u8 (N,K), sbg and sbu fp32
+ *   [ceil(N/128)][K/128] as for fp8_gemm_nt; any M and N, K % 128 == 0.
+ *   h bf16 bits (M,N); g and u bf16 bits (M,N), both or neither: the
+ *   projections, which the gradient needs.
+ * g and u are formed with exact block partials as on fp8_gemm_nt's default
+ * path; the activation and the product are FP32, and each output is rounded
+ * once.  flags: FP8_FLAG_UE8M0 (the scales are powers of two).
+ * workspace: up to 64 rows (M <= 16: only where g and u, or quantized
+ * outputs, are asked for) a workspace of fp8_gated_workspace_size() bytes lets
+ * K be split over workgroups; without it, or with a smaller one, the call runs
+ * unsplit.  outputs (of the size query): 0 h, 1 h with g and u, 2 quantized.
+ */
+fp8_status fp8_gated_nt(const uint8_t* xq, const float* sa, const uint8_t* wgq,
+                        const float* sbg, const uint8_t* wuq, const float* sbu,
+                        uint16_t* h, uint16_t* g, uint16_t* u, int64_t M,
+                        int64_t N, int64_t K, int32_t act, uint32_t flags,
+                        void* workspace, size_t workspace_bytes, void* stream);
+size_t fp8_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t outputs);
+
+/*
+ * fp8_gated_nt with h quantized for the next GEMM (the down projection), from
+ * the FP32 values, as fp8_gemm_nt_qout does:
+ *   hq u8 (M,N) E4M3 codes, sh fp32 [N/128][M] 1x128 scales; N % 128 == 0.
+ */
+fp8_status fp8_gated_nt_qout(const uint8_t* xq, const float* sa, const uint8_t* wgq,
+                             const float* sbg, const uint8_t* wuq, const float* sbu,
+                             uint8_t* hq, float* sh, int64_t M, int64_t N,
+                             int64_t K, int32_t act, uint32_t flags,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the gated block, BF16 operands (the activations and weights
+ * before quantization; quantization is taken as the identity):
+ *   dg = dh * u * act'(g),  du = dh * act(g)
+ *   dX = dg Wg + du Wu,  dWg = dg^T X,  dWu = du^T X
+ *   dh, g, u (M,N), x (M,K), wg, wu (N,K), dx (M,K), dwg, dwu (N,K): bf16
+ *   bits; any M and N, K % 128 == 0.  dx may be NULL, and dwg and dwu may
+ *   both be NULL (not computed).  With M == 0 dwg and dwu are zeros, with
+ *   N == 0 dx is.
+ * dg and du are formed in FP32 and rounded to BF16, the matrix instruction's
+ * type; sums are FP32, and each result is rounded once.  The workspace (dg
+ * and du) is required: fp8_gated_grad_workspace_size() bytes, else
+ * FP8_ERR_SCRATCH.
+ */
+fp8_status fp8_gated_nt_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
+                             const uint16_t* x, const uint16_t* wg, const uint16_t* wu,
+                             uint16_t* dx, uint16_t* dwg, uint16_t* dwu, int64_t M,
+                             int64_t N, int64_t K, int32_t act, void* workspace,
+                             size_t workspace_bytes, void* stream);
+size_t fp8_gated_grad_workspace_size(int64_t M, int64_t N);
+
+/* ---------------------------------------------------------------------------
+ * Matrix-vector products with 4-bit weights and group scales, for up to 16
+ * tokens (M <= 16, else FP8_ERR_SHAPE).
+ * ------------------------------------------------------------------------- */
+
+/* Value of `group` for MXFP4 weights (E2M1 with one E8M0 scale per 32). */
+#define FP8_W4_MXFP4 0
+
+/*
+ * y[m][n] = sum_k x[m][k] w[n][k]
+ *   x bf16 bits (M,K), y bf16 bits (M,N); any N, K % 128 == 0.
+ *   w u8 (N,K/2): two codes per byte, the even element in the low nibble.
+ *   group == FP8_W4_MXFP4: w = E2M1 * 2^(e-127), s = u32 [K/128][N] packed
+ *     scale bytes, both as fp8_quant_mxfp4 writes them; z NULL.
+ *   group 32, 64 or 128: w = s * (q - z), q = 0..15; s bf16 bits [K/group][N];
+ *     z u8 [K/group][N] (values 0..15), or NULL for 8 everywhere.
+ * Every product is exact, the sums are FP32, y is rounded once.
+ */
+fp8_status fp8_gemv_w4(const uint16_t* x, const uint8_t* w, const void* s,
+                       const uint8_t* z, uint16_t* y, int64_t M, int64_t N,
+                       int64_t K, int32_t group, void* stream);
+
+/* The gated block on such weights: y = act(x Wg^T) * (x Wu^T), one kernel.
+ * zg and zu: both or neither. */
+fp8_status fp8_gated_gemv_w4(const uint16_t* x, const uint8_t* wg, const void* sg,
+                             const uint8_t* zg, const uint8_t* wu, const void* su,
+                             const uint8_t* zu, uint16_t* y, int64_t M, int64_t N,
+                             int64_t K, int32_t group, int32_t act, void* stream);
+
+/*
+ * 4-bit integer weight quantizer, one scale per `group` (32, 64, 128) along K:
+ *   z given:  lo = min(w, 0), hi = max(w, 0) over the group, s =
+ *             bf16((hi - lo) / 15), z = clamp(round(-lo / s), 0, 15)
+ *   z NULL:   s = bf16(max|w| / 7), z = 8
+ *   q = clamp(round(w / s) + z, 0, 15);  s is at least bf16(1e-8)
+ * Roundings to nearest, ties to even; quotients correctly rounded FP32.
+ *   w fp32 (N,K) -> q u8 (N,K/2), s bf16 bits [K/group][N], z u8 [K/group][N]
+ */
+fp8_status fp8_quant_int4(const float* w, int64_t N, int64_t K, int32_t group,
+                          uint8_t* q, uint16_t* s, uint8_t* z, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Global gradient norm over many tensors, and clipping.
+ *   norm = sqrt(sum over all tensors and elements of g^2)
+ *   out  = g * min(1, max_norm / (norm + 1e-6))
+ * ------------------------------------------------------------------------- */
+#define FP8_TYPE_F32 0
+#define FP8_TYPE_BF16 1
+#define FP8_TYPE_F16 2
+
+/*
+ * grads, outs, sizes, types: HOST arrays of `count` device pointers, element
+ * counts and FP8_TYPE_*, read during the call only.  Tensors need no more
+ * alignment than their elements; outs[i] may be grads[i] (in place), and
+ * overlaps nothing else.  norm: one FP32 on the device.  Squares are summed
+ * in FP64 in a fixed order.  A NaN among the gradients makes the norm and all
+ * outputs NaN; an infinity makes the factor 0.  The workspace is required:
+ * fp8_clip_workspace_size() bytes, 8-byte aligned, else FP8_ERR_SCRATCH.
+ */
+fp8_status fp8_clip_grad_norm(const void* const* grads, void* const* outs,
+                              const int64_t* sizes, const int32_t* types,
+                              int32_t count, float max_norm, float* norm,
+                              void* workspace, size_t workspace_bytes, void* stream);
+size_t fp8_clip_workspace_size(const int64_t* sizes, int32_t count);
 
 /* M alignment every expert segment of the contiguous layout must have
  * ([DG] "分组 GEMM 的两种布局": the alignment query).  Returns 128. */
