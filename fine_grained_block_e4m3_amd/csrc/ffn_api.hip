@@ -10,13 +10,12 @@
 #include "kernels_decode.h"
 #include "kernels_exact.h"
 #include "kernels_gated_grad.h"
-#include "kernels_skinny.h"
+#include "skinny.h"
 
 namespace {
 
 using namespace fp8h;
 
-constexpr int64_t kMaxSkinnyM = 16;
 constexpr int64_t kMaxDecodeM = 64;
 
 bool act_ok(int32_t act) { return act == FP8_ACT_SILU || act == FP8_ACT_GELU; }
@@ -91,51 +90,12 @@ fp8_status run_gated_decode(const fp8k::GemmParams& p, bool quant, bool pow2, in
     return launch_status();
 }
 
-// ---------------------------------------------------------------------------
-// Up to 16 tokens.
-// ---------------------------------------------------------------------------
-template <int FMT, bool GATED, int RT, int KW, int U, int GROUP, bool ZEROS>
-fp8_status launch_skinny(const fp8k::SkinnyParams& p, hipStream_t stream) {
-    const int64_t cols = GATED ? 8 * RT : 16 * RT;
-    hipLaunchKernelGGL((fp8k::skinny_kernel<FMT, GATED, RT, KW, U, GROUP, ZEROS>), dim3((unsigned)cdiv(p.N, cols)),
-                       dim3(64 * KW), 0, stream, p);
-    return launch_status();
-}
-
-template <int FMT, bool GATED, int GROUP, bool ZEROS>
-fp8_status run_skinny(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
-    // rows of weights per compute unit decide between one 16-row tile per
-    // workgroup and two
-    const int64_t tiles = cdiv(p.N * (GATED ? 2 : 1), 16);
-    if (tiles < 4 * cus) return launch_skinny<FMT, GATED, 1, 8, 2, GROUP, ZEROS>(p, stream);
-    return launch_skinny<FMT, GATED, 2, 8, 2, GROUP, ZEROS>(p, stream);
-}
-
-template <bool GATED>
-fp8_status run_gemv_w4(const fp8k::SkinnyParams& p, int32_t group, hipStream_t stream) {
-    int cus = 0;
-    const fp8_status st = current_device_cus(&cus);
-    if (st != FP8_OK) return st;
-    const bool z = p.z[0] != nullptr;
-    switch (group) {
-        case FP8_W4_MXFP4: return run_skinny<fp8k::kSkinnyMxfp4, GATED, 32, false>(p, cus, stream);
-        case 32:
-            return z ? run_skinny<fp8k::kSkinnyInt4, GATED, 32, true>(p, cus, stream)
-                     : run_skinny<fp8k::kSkinnyInt4, GATED, 32, false>(p, cus, stream);
-        case 64:
-            return z ? run_skinny<fp8k::kSkinnyInt4, GATED, 64, true>(p, cus, stream)
-                     : run_skinny<fp8k::kSkinnyInt4, GATED, 64, false>(p, cus, stream);
-        default:
-            return z ? run_skinny<fp8k::kSkinnyInt4, GATED, 128, true>(p, cus, stream)
-                     : run_skinny<fp8k::kSkinnyInt4, GATED, 128, false>(p, cus, stream);
-    }
-}
-
 fp8_status check_gemv(int64_t M, int64_t N, int64_t K, int32_t group) {
     if (!dims_ok(M) || !dims_ok(N) || !dims_ok(K) ||
         !(group == FP8_W4_MXFP4 || group == 32 || group == 64 || group == 128))
         return FP8_ERR_INVALID_ARG;
     if (K % 128 || K == 0 || M > kMaxSkinnyM) return FP8_ERR_SHAPE;
+    if (group != FP8_W4_MXFP4 && N && N < 4) return FP8_ERR_SHAPE;   // the kernel reads 4 scales at once
     if (K > kMaxGemmK) return FP8_ERR_UNSUPPORTED;
     return FP8_OK;
 }
@@ -157,7 +117,7 @@ fp8_status run_gated(fp8k::GemmParams& p, int32_t outputs, uint32_t flags, void*
         fp8k::SkinnyParams q{};
         q.x = p.xq; q.sa = p.sa; q.w[0] = p.wq; q.w[1] = p.wq2; q.s[0] = p.sb; q.s[1] = p.sb2;
         q.y = p.y; q.M = p.M; q.N = p.N; q.K = p.K; q.act = p.act;
-        return run_skinny<fp8k::kSkinnyE4m3, true, 128, false>(q, cus, stream);
+        return run_skinny_gated_e4m3(q, cus, stream);
     }
     const bool quant = outputs == kOutQuant, pow2 = flags & FP8_FLAG_UE8M0;
     const size_t need = gated_ws_bytes(p.M, p.N, p.K, outputs, cus);
@@ -319,7 +279,7 @@ fp8_status fp8_gemv_w4(const uint16_t* x, const uint8_t* w, const void* s, const
     fp8k::SkinnyParams p{};
     p.x = x; p.w[0] = w; p.s[0] = s; p.z[0] = z; p.y = y;
     p.M = M; p.N = N; p.K = K;
-    return run_gemv_w4<false>(p, group, (hipStream_t)stream);
+    return run_gemv_w4(p, false, group, (hipStream_t)stream);
 }
 
 fp8_status fp8_gated_gemv_w4(const uint16_t* x, const uint8_t* wg, const void* sg, const uint8_t* zg,
@@ -337,7 +297,7 @@ fp8_status fp8_gated_gemv_w4(const uint16_t* x, const uint8_t* wg, const void* s
     fp8k::SkinnyParams p{};
     p.x = x; p.w[0] = wg; p.w[1] = wu; p.s[0] = sg; p.s[1] = su; p.z[0] = zg; p.z[1] = zu; p.y = y;
     p.M = M; p.N = N; p.K = K; p.act = act;
-    return run_gemv_w4<true>(p, group, (hipStream_t)stream);
+    return run_gemv_w4(p, true, group, (hipStream_t)stream);
 }
 
 fp8_status fp8_quant_int4(const float* w, int64_t N, int64_t K, int32_t group, uint8_t* q, uint16_t* s, uint8_t* z,
@@ -350,14 +310,7 @@ fp8_status fp8_quant_int4(const float* w, int64_t N, int64_t K, int32_t group, u
     int cus = 0;
     const fp8_status st = current_device_cus(&cus);
     if (st != FP8_OK) return st;
-    const int64_t blocks = cdiv(N * (K / group), 256 / (group / 4));
-    if (blocks > 0x7FFFFFFF) return FP8_ERR_INVALID_ARG;
-    const dim3 grid((unsigned)blocks), block(256);
-    hipStream_t t = (hipStream_t)stream;
-    if (group == 32) hipLaunchKernelGGL(fp8k::quant_int4_kernel<32>, grid, block, 0, t, w, q, s, z, N, K);
-    else if (group == 64) hipLaunchKernelGGL(fp8k::quant_int4_kernel<64>, grid, block, 0, t, w, q, s, z, N, K);
-    else hipLaunchKernelGGL(fp8k::quant_int4_kernel<128>, grid, block, 0, t, w, q, s, z, N, K);
-    return launch_status();
+    return run_quant_int4(w, N, K, group, q, s, z, (hipStream_t)stream);
 }
 
 size_t fp8_clip_workspace_size(const int64_t* sizes, int32_t count) {

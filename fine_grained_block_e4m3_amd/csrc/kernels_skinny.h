@@ -22,37 +22,26 @@
 //     tokens past M repeat the last one (their loads coalesce with it) and
 //     are not stored.  A vector-FMA form would spend M operations per weight;
 //     this one spends the decoding only, whatever M.
-//   * The KW waves of a workgroup share its rows and take every KW-th K
-//     block; one LDS exchange at the end adds their FP32 sums in wave order.
-//     With few rows this keeps every compute unit reading; no workspace and
-//     no second launch.
-//   * The loads of the next U blocks are issued before the U blocks at hand
-//     are multiplied.
+//   * The KW waves of a workgroup share its rows and split K; one LDS exchange
+//     at the end adds their FP32 sums in wave order.  With few rows this keeps
+//     every compute unit reading; no workspace and no second launch.
+//   * Every workgroup reads all of x, from its L2: RT 16-row tiles per
+//     workgroup share each x operand (the launch picks RT, skinny_launch.hip).
+//   * The loads of the D - 1 blocks that follow are in flight while a block is
+//     multiplied.
 // Exactness: E2M1 times a power of two is a BF16 value (products exact, FP32
-// sums).  4-bit integers enter as the BF16 values 128 + q (an OR into the
-// mantissa: exact); the group's sum of x comes from the same instruction with
-// a matrix of ones, and s * (sum x (128 + q) - (128 + z) * sum x) is formed in
-// FP32 per group.  E4M3 is widened exactly to FP16.
+// sums).  4-bit integers enter as the BF16 integers q; the group's sum of x
+// comes from the same instruction with a matrix of ones, and
+// s * (sum x q - z * sum x) is formed in FP32 per group.  E4M3 is widened exactly to FP16.
 #pragma once
 
 #include "gated_common.h"
-#include "gemm_common.h"
+#include "skinny.h"
 
 namespace fp8k {
 
 
 enum SkinnyFormat : int { kSkinnyMxfp4 = 0, kSkinnyInt4 = 1, kSkinnyE4m3 = 2 };
-
-struct SkinnyParams {
-    const void* x;          // BF16 (M, K), or E4M3 codes (M, K)
-    const float* sa;        // E4M3: activation scales [K/128][M]
-    const uint8_t* w[2];    // weight codes; gated: gate, up
-    const void* s[2];       // scales
-    const uint8_t* z[2];    // 4-bit integers: zero points, or null (8)
-    uint16_t* y;            // BF16 (M, N)
-    int64_t M, N, K;
-    int32_t act;
-};
 
 // Transposes a 4x4 block of dwords over the four lanes (r, 0..3): afterwards
 // v[s] of lane (r, q) is what v[q] of lane (r, s) was.
@@ -64,22 +53,24 @@ __device__ __forceinline__ i32x4 transpose_quads(i32x4 v) {
     return i32x4{(int)c[0], (int)c[1], (int)d[0], (int)d[1]};
 }
 
-// Eight 4-bit codes of a dword as the BF16 values 128 + q, in the order
-// 0, 4, 1, 5, 2, 6, 3, 7 (pairs four codes apart: one shift, one and-or each).
+// Eight 4-bit codes of a dword as BF16 integers, in the order 0, 2, 4, 6, 1, 3,
+// 5, 7.  A byte of value q < 16 is the E4M3 value q * 2^-9 (subnormal below 8,
+// exponent 1 above), so the hardware converter widens them at scale 2^9.
 __device__ __forceinline__ bf16x8 u4x8_to_bf16(int v) {
-    i32x4 r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = (int)((((uint32_t)v >> (4 * j)) & 0x000F000Fu) | 0x43004300u);
-    return __builtin_bit_cast(bf16x8, r);
+    const unsigned lo = (unsigned)v & 0x0F0F0F0Fu, hi = ((unsigned)v >> 4) & 0x0F0F0F0Fu;
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 // Eight BF16 values in that order.
 __device__ __forceinline__ bf16x8 bf16x8_u4_order(i32x4 x) {
-    // pairs (0,4) (1,5) (2,6) (3,7) of the halves of dwords 0,1 and 2,3
     i32x4 r;
-    r[0] = (int)__builtin_amdgcn_perm((unsigned)x[2], (unsigned)x[0], 0x05040100u);
-    r[1] = (int)__builtin_amdgcn_perm((unsigned)x[2], (unsigned)x[0], 0x07060302u);
-    r[2] = (int)__builtin_amdgcn_perm((unsigned)x[3], (unsigned)x[1], 0x05040100u);
-    r[3] = (int)__builtin_amdgcn_perm((unsigned)x[3], (unsigned)x[1], 0x07060302u);
+    r[0] = (int)__builtin_amdgcn_perm((unsigned)x[1], (unsigned)x[0], 0x05040100u);
+    r[1] = (int)__builtin_amdgcn_perm((unsigned)x[3], (unsigned)x[2], 0x05040100u);
+    r[2] = (int)__builtin_amdgcn_perm((unsigned)x[1], (unsigned)x[0], 0x07060302u);
+    r[3] = (int)__builtin_amdgcn_perm((unsigned)x[3], (unsigned)x[2], 0x07060302u);
     return __builtin_bit_cast(bf16x8, r);
 }
 // Eight E2M1 codes of a dword times the power of two `scale`, as BF16.
@@ -94,9 +85,9 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as
 
 // RT: 16-row weight tiles per workgroup; gated: even tiles hold gate rows, odd
 // ones the up rows of the same columns, and RT == 1 one tile of 8 gate and 8
-// up rows (more workgroups for narrow weights).  KW: waves along K.  U: K
-// blocks in flight per wave.  GROUP: group size of 4-bit integers.
-template <int FMT, bool GATED, int RT, int KW, int U, int GROUP, bool ZEROS>
+// up rows (more workgroups for narrow weights).  KW: waves along K.  D: K
+// blocks of a wave in registers.  GROUP: group size of 4-bit integers.
+template <int FMT, bool GATED, int RT, int KW, int D, int GROUP, bool ZEROS>
 __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     constexpr bool kMixed = GATED && RT == 1;
     constexpr int COLS = GATED ? 8 * RT : 16 * RT;      // output columns of a workgroup
@@ -112,15 +103,24 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     const int r = lane & 15, q = lane >> 4;
     const int64_t N = p.N;
     const int KB = (int)(p.K / 128);
-    const int64_t n0 = (int64_t)blockIdx.x * COLS;
+    // workgroup b of a dispatch wave lands on XCD b % 8: each XCD takes a run of
+    // consecutive rows, so that the lines of the scale tables (16 rows take a
+    // part of one) are fetched into one L2 only
+    const int G = gridDim.x, per = G / 8, rest = G % 8, xcd = blockIdx.x % 8;
+    const int64_t n0 = (int64_t)(xcd * per + min(xcd, rest) + (int)(blockIdx.x / 8)) * COLS;
+
     const bool edge = n0 + COLS > N;
 
     // operand row of this lane in each tile, and the first of the 4 result
     // rows it holds (rows past N repeat the last one; they are not stored)
     const uint8_t* wrow[RT];
     const uint32_t* erow[RT];       // MXFP4: this lane's scale dwords
-    int wsel[RT];                   // result rows: which weight
-    int64_t nres[RT];
+    // 4-bit integers: the 4 scales and zero points of the lane's result rows
+    // (N >= 4; rows that end past N are read up to N and shifted down)
+    const uint16_t* srow[RT];
+    const uint8_t* zrow[RT];
+    int sshift[RT];
+    const float* brow[RT];          // E4M3: the block scales of the result rows
     const int64_t row_bytes = FMT == kSkinnyE4m3 ? p.K : p.K / 2;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -128,59 +128,44 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
         const int64_t n = min(n0 + (kMixed ? r & 7 : 16 * (GATED ? t >> 1 : t) + r), N - 1);
         wrow[t] = p.w[wi] + n * row_bytes + 16 * WL * q;
         erow[t] = reinterpret_cast<const uint32_t*>(p.s[wi]) + n;
-        wsel[t] = kMixed ? q >> 1 : GATED ? t & 1 : 0;
-        nres[t] = n0 + (kMixed ? 4 * (q & 1) : 16 * (GATED ? t >> 1 : t) + 4 * q);
+        const int ri = kMixed ? q >> 1 : GATED ? t & 1 : 0;
+        const int64_t nr = n0 + (kMixed ? 4 * (q & 1) : 16 * (GATED ? t >> 1 : t) + 4 * q);
+        const int64_t from = min(nr, N - 4);
+        srow[t] = static_cast<const uint16_t*>(p.s[ri]) + from;
+        zrow[t] = ZEROS ? p.z[ri] + from : nullptr;
+        sshift[t] = (int)min(nr - from, (int64_t)3);
+        brow[t] = static_cast<const float*>(p.s[ri]) + (min(nr, N - 1) >> 7) * KB;
     }
     const int64_t m = min((int64_t)r, p.M - 1);
     // x of this lane's token: 4-bit with whole-block groups and E4M3: the 32
     // elements 32q ..; transposed: elements 32 s + 8 q of step s
     const uint8_t* xrow = static_cast<const uint8_t*>(p.x) + m * p.K * (FMT == kSkinnyE4m3 ? 1 : 2) +
                           (FMT == kSkinnyE4m3 ? 32 * q : kTranspose ? 16 * q : 64 * q);
+    const float* sarow = p.sa + m;
 
     struct Block {
         i32x4 w[RT][WL];
         i32x4 x[XL];
         uint32_t e[RT];             // MXFP4: scale dword of the operand row
-        uint32_t sl[RT][NG], sh[RT][NG];   // int4: 4 BF16 scales of the result rows
-        uint32_t zz[RT][NG];        // int4: 4 zero points
+        uint64_t s[RT][NG];         // int4: 4 BF16 scales of the result rows
+        uint32_t z[RT][NG];         // ... and 4 zero points
         float sab[RT];              // E4M3: sa * sb of the result rows
     };
-    auto load = [&](Block& b, int kb0) FP8K_INLINE {
-        const int kb = min(kb0, KB - 1);
+    auto load = [&](Block& b, int kb) FP8K_INLINE {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
 #pragma unroll
             for (int i = 0; i < WL; ++i)
-                b.w[t][i] = __builtin_nontemporal_load(
-                    reinterpret_cast<const i32x4*>(wrow[t] + (int64_t)kb * 64 * WL + 16 * i));
+                b.w[t][i] = *reinterpret_cast<const i32x4*>(wrow[t] + (int64_t)kb * 64 * WL + 16 * i);
             if constexpr (FMT == kSkinnyMxfp4) b.e[t] = erow[t][(int64_t)kb * N];
-            if constexpr (FMT == kSkinnyE4m3) {
-                const int64_t nb = min(nres[t], N - 1) >> 7;
-                b.sab[t] = p.sa[(int64_t)kb * p.M + m] * static_cast<const float*>(p.s[wsel[t]])[nb * KB + kb];
-            }
+            if constexpr (FMT == kSkinnyE4m3) b.sab[t] = sarow[(int64_t)kb * p.M] * brow[t][kb];
             if constexpr (FMT == kSkinnyInt4) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
+                    // 8 and 4 bytes, aligned to their elements
                     const int64_t at = ((int64_t)kb * NG + g) * N;
-                    const uint16_t* sp = static_cast<const uint16_t*>(p.s[wsel[t]]) + at;
-                    const uint8_t* zp = ZEROS ? p.z[wsel[t]] + at : nullptr;
-                    if (!edge) {
-                        // 8 and 4 bytes, aligned to an element only when N is odd
-                        uint32_t v[2];
-                        __builtin_memcpy(v, sp + nres[t], 8);
-                        b.sl[t][g] = v[0];
-                        b.sh[t][g] = v[1];
-                        if constexpr (ZEROS) __builtin_memcpy(&b.zz[t][g], zp + nres[t], 4);
-                    } else {
-                        int64_t c[4];
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) c[v] = min(nres[t] + v, N - 1);
-                        b.sl[t][g] = sp[c[0]] | (uint32_t)sp[c[1]] << 16;
-                        b.sh[t][g] = sp[c[2]] | (uint32_t)sp[c[3]] << 16;
-                        if constexpr (ZEROS)
-                            b.zz[t][g] = zp[c[0]] | (uint32_t)zp[c[1]] << 8 | (uint32_t)zp[c[2]] << 16 |
-                                         (uint32_t)zp[c[3]] << 24;
-                    }
+                    __builtin_memcpy(&b.s[t][g], srow[t] + at, 8);
+                    if constexpr (ZEROS) __builtin_memcpy(&b.z[t][g], zrow[t] + at, 4);
                 }
             }
         }
@@ -242,32 +227,53 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
                         part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u4x8_to_bf16(wt[t][s]), xv, part[t], 0, 0, 0);
                 }
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
+                for (int t = 0; t < RT; ++t) {
+                    uint64_t s4 = b.s[t][g];
+                    uint32_t z4 = ZEROS ? b.z[t][g] : 0u;
+                    if (edge) {
+                        s4 >>= 16 * sshift[t];
+                        z4 >>= 8 * sshift[t];
+                    }
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
-                        const uint32_t sw = v < 2 ? b.sl[t][g] : b.sh[t][g];
+                        const uint32_t sw = (uint32_t)(v < 2 ? s4 : s4 >> 32);
                         const float sc = v & 1 ? __uint_as_float(sw & 0xFFFF0000u) : bf16_bits_to_f32(sw);
-                        const float off = ZEROS ? 128.f + (float)(b.zz[t][g] >> (8 * v) & 0xFFu) : 136.f;
+                        const float off = ZEROS ? (float)(z4 >> (8 * v) & 0xFFu) : 8.f;
                         acc[t][v] = __builtin_fmaf(sc, __builtin_fmaf(-off, sx[0], part[t][v]), acc[t][v]);
                     }
+                }
             }
         }
     };
 
-    Block cur[U];
+    // This wave's blocks, D - 1 of them in flight ahead of the one multiplied:
+    // every KW-th pair of blocks (the two 64-byte halves of a row's 128-byte
+    // line, one right after the other), counted from a start that differs from
+    // workgroup to workgroup, so that the workgroups, which all read the same
+    // x, do not ask for the same lines at the same time.
+    const int rot = (int)((unsigned)blockIdx.x * 6u % (unsigned)KB);
+    const int pairs = (KB + 1) / 2, mine = pairs > wave ? (pairs - wave + KW - 1) / KW : 0;
+    const int nb = 2 * mine - (mine && (KB & 1) && wave + (mine - 1) * KW == pairs - 1);
+    auto block_of = [&](int j) FP8K_INLINE {
+        const int kb = 2 * (wave + (j >> 1) * KW) + (j & 1) + rot;
+        return kb < KB ? kb : kb - KB;
+    };
+    Block b[D];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (wave + u * KW < KB) load(cur[u], wave + u * KW);
-    for (int kb = wave; kb < KB; kb += U * KW) {
-        Block next[U];
+    for (int j = 0; j < D - 1; ++j)
+        if (j < nb) load(b[j], block_of(j));
+    int at = 0;
+    for (; at + 2 * D - 2 < nb; at += D) {      // every load of the round is one of a block
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (kb + (U + u) * KW < KB) load(next[u], kb + (U + u) * KW);
+        for (int j = 0; j < D; ++j) {
+            load(b[(j + D - 1) % D], block_of(at + j + D - 1));
+            multiply(b[j]);
+        }
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (kb + u * KW < KB) multiply(cur[u]);
-#pragma unroll
-        for (int u = 0; u < U; ++u) cur[u] = next[u];
+    for (int j = 0; j < 2 * D - 2; ++j) {
+        if (at + j + D - 1 < nb) load(b[(j + D - 1) % D], block_of(at + j + D - 1));
+        if (at + j < nb) multiply(b[j % D]);
     }
 
     // ---- join the waves' sums, in wave order; tile t by wave t % KW ----

@@ -1,0 +1,108 @@
+// skinny_launch.hip -- instances and launches of the kernels for up to 16
+// tokens (kernels_skinny.h).
+#include "kernels_skinny.h"
+
+namespace {
+
+using namespace fp8h;
+
+// 16-row weight tiles per workgroup: the number that leaves the fullest compute
+// unit the fewest tiles, and of those the largest, whose tiles share the x
+// operands.  One MI355X, int4 weights with groups of 128, 16 x 24576 x 7168
+// (1536 tiles): 6 per workgroup 27-29 us, 3 34, 2 38, 1 56; gated MXFP4
+// 1 x 2048 x 7168 (256 tiles): 1 per workgroup 6.4 us, 2 7.7; 3 x 2112 x 7168
+// (264): 1 10.9, 2 8.5.
+int pick_tiles(int64_t tiles, int cus, std::initializer_list<int> allowed) {
+    int best = 1;
+    int64_t cost = INT64_MAX;
+    for (int rt : allowed) {
+        const int64_t c = cdiv(cdiv(tiles, rt), cus) * rt;
+        if (c <= cost) {
+            cost = c;
+            best = rt;
+        }
+    }
+    return best;
+}
+
+constexpr int kWaves = 8, kDepth = 2;
+
+template <int FMT, bool GATED, int RT, int GROUP, bool ZEROS>
+fp8_status launch_skinny(const fp8k::SkinnyParams& p, hipStream_t stream) {
+    const int64_t cols = GATED ? 8 * RT : 16 * RT;
+    hipLaunchKernelGGL((fp8k::skinny_kernel<FMT, GATED, RT, kWaves, kDepth, GROUP, ZEROS>),
+                       dim3((unsigned)cdiv(p.N, cols)), dim3(64 * kWaves), 0, stream, p);
+    return launch_status();
+}
+
+template <int FMT, bool GATED, int GROUP, bool ZEROS>
+fp8_status run_skinny(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
+    const int64_t tiles = cdiv(p.N * (GATED ? 2 : 1), 16);
+    if constexpr (FMT == fp8k::kSkinnyInt4 && GROUP < 128) {
+        // scales and zero points of several groups per block: more tiles than
+        // two do not fit the registers
+        return pick_tiles(tiles, cus, {1, 2}) == 1 ? launch_skinny<FMT, GATED, 1, GROUP, ZEROS>(p, stream)
+                                                   : launch_skinny<FMT, GATED, 2, GROUP, ZEROS>(p, stream);
+    } else {
+        int rt;
+        if constexpr (GATED) rt = pick_tiles(tiles, cus, {1, 2, 4, 6});
+        else if constexpr (ZEROS) rt = pick_tiles(tiles, cus, {1, 2, 3, 4});   // 6 spill
+        else rt = pick_tiles(tiles, cus, {1, 2, 3, 4, 6});
+        switch (rt) {
+            case 1: return launch_skinny<FMT, GATED, 1, GROUP, ZEROS>(p, stream);
+            case 2: return launch_skinny<FMT, GATED, 2, GROUP, ZEROS>(p, stream);
+            case 3:
+                if constexpr (!GATED) return launch_skinny<FMT, GATED, 3, GROUP, ZEROS>(p, stream);
+                else return FP8_ERR_UNSUPPORTED;
+            case 4: return launch_skinny<FMT, GATED, 4, GROUP, ZEROS>(p, stream);
+            default:
+                if constexpr (GATED || !ZEROS) return launch_skinny<FMT, GATED, 6, GROUP, ZEROS>(p, stream);
+                else return FP8_ERR_UNSUPPORTED;
+        }
+    }
+}
+
+template <bool GATED>
+fp8_status run_w4(const fp8k::SkinnyParams& p, int32_t group, int cus, hipStream_t stream) {
+    const bool z = p.z[0] != nullptr;
+    switch (group) {
+        case FP8_W4_MXFP4: return run_skinny<fp8k::kSkinnyMxfp4, GATED, 32, false>(p, cus, stream);
+        case 32:
+            return z ? run_skinny<fp8k::kSkinnyInt4, GATED, 32, true>(p, cus, stream)
+                     : run_skinny<fp8k::kSkinnyInt4, GATED, 32, false>(p, cus, stream);
+        case 64:
+            return z ? run_skinny<fp8k::kSkinnyInt4, GATED, 64, true>(p, cus, stream)
+                     : run_skinny<fp8k::kSkinnyInt4, GATED, 64, false>(p, cus, stream);
+        default:
+            return z ? run_skinny<fp8k::kSkinnyInt4, GATED, 128, true>(p, cus, stream)
+                     : run_skinny<fp8k::kSkinnyInt4, GATED, 128, false>(p, cus, stream);
+    }
+}
+
+}  // namespace
+
+namespace fp8h {
+
+fp8_status run_skinny_gated_e4m3(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
+    return run_skinny<fp8k::kSkinnyE4m3, true, 128, false>(p, cus, stream);
+}
+
+fp8_status run_gemv_w4(const fp8k::SkinnyParams& p, bool gated, int32_t group, hipStream_t stream) {
+    int cus = 0;
+    const fp8_status st = current_device_cus(&cus);
+    if (st != FP8_OK) return st;
+    return gated ? run_w4<true>(p, group, cus, stream) : run_w4<false>(p, group, cus, stream);
+}
+
+fp8_status run_quant_int4(const float* w, int64_t N, int64_t K, int32_t group, uint8_t* q, uint16_t* s, uint8_t* z,
+                          hipStream_t stream) {
+    const int64_t blocks = cdiv(N * (K / group), 256 / (group / 4));
+    if (blocks > 0x7FFFFFFF) return FP8_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)blocks), block(256);
+    if (group == 32) hipLaunchKernelGGL(fp8k::quant_int4_kernel<32>, grid, block, 0, stream, w, q, s, z, N, K);
+    else if (group == 64) hipLaunchKernelGGL(fp8k::quant_int4_kernel<64>, grid, block, 0, stream, w, q, s, z, N, K);
+    else hipLaunchKernelGGL(fp8k::quant_int4_kernel<128>, grid, block, 0, stream, w, q, s, z, N, K);
+    return launch_status();
+}
+
+}  // namespace fp8h
