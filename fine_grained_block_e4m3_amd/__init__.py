@@ -158,11 +158,19 @@ def _check(fn: str, status: int) -> None:
         raise Fp8GemmError(fn, status, msg)
 
 
-def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+# The raw handle of a device's current stream, without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(t: torch.Tensor) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> None:
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -187,14 +195,14 @@ def _out(t, name: str, dtype: torch.dtype, shape, like: torch.Tensor) -> torch.T
 
 
 def _same_device(*ts: torch.Tensor) -> None:
-    d = ts[0].device
+    d = ts[0].get_device()
     for t in ts[1:]:
-        if t.device != d:
-            raise ValueError(f"operands on different devices: {d} and {t.device}")
+        if t.get_device() != d:
+            raise ValueError(f"operands on different devices: {ts[0].device} and {t.device}")
 
 
-def _ptr(t: torch.Tensor):
-    return ctypes.c_void_p(t.data_ptr())
+def _ptr(t: torch.Tensor) -> int:
+    return t.data_ptr()
 
 
 def _flags(ue8m0: bool, fast_accum: bool = False) -> int:
@@ -462,6 +470,11 @@ def _gated_operands(xq, sa, wgq, sbg, wuq, sbu, fn: str):
     return M, N, K
 
 
+def _gated_workspace_size(M: int, N: int, K: int, outputs: int) -> int:
+    # only decode-sized M uses a workspace
+    return int(load_library().fp8_gated_workspace_size(M, N, K, outputs)) if M <= 64 else 0
+
+
 def gated_nt(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = False, save: bool = False, out=None,
              workspace=None):
     """Gated feed-forward block on block-scaled E4M3 operands: h (M, N) bf16 =
@@ -479,7 +492,7 @@ def gated_nt(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = False,
         if len(ys) != count:
             raise ValueError("gated_nt: out must be (h, g, u) with save")
         ys = [_out(t, f"out[{i}]", torch.bfloat16, (M, N), xq) for i, t in enumerate(ys)]
-    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_gated_workspace_size(M, N, K, 1 if save else 0)), xq)
+    ws, ws_bytes, keep = _workspace(workspace, _gated_workspace_size(M, N, K, 1 if save else 0), xq)
     _check("fp8_gated_nt", L.fp8_gated_nt(
         _ptr(xq), _ptr(sa), _ptr(wgq), _ptr(sbg), _ptr(wuq), _ptr(sbu), _ptr(ys[0]),
         _ptr(ys[1]) if save else None, _ptr(ys[2]) if save else None, M, N, K, a, _flags(ue8m0), ws, ws_bytes,
@@ -499,7 +512,7 @@ def gated_nt_qout(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = F
     else:
         hq = _out(out[0], "out[0]", torch.uint8, (M, N), xq)
         sh = _out(out[1], "out[1]", torch.float32, (N // 128, M), xq)
-    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_gated_workspace_size(M, N, K, 2)), xq)
+    ws, ws_bytes, keep = _workspace(workspace, _gated_workspace_size(M, N, K, 2), xq)
     _check("fp8_gated_nt_qout", L.fp8_gated_nt_qout(
         _ptr(xq), _ptr(sa), _ptr(wgq), _ptr(sbg), _ptr(wuq), _ptr(sbu), _ptr(hq), _ptr(sh), M, N, K, a,
         _flags(ue8m0), ws, ws_bytes, _stream(xq)))
@@ -620,34 +633,36 @@ def clip_grad_norm(grads, max_norm: float, out=None, workspace=None) -> torch.Te
     """Scales the tensors of `grads` (fp32, bf16 or fp16, contiguous, any mix)
     by min(1, max_norm / (norm + 1e-6)), norm being the 2-norm over all of
     them, and returns norm (0-dim fp32, on the device).  In place unless `out`
-    gives one tensor per gradient."""
+    gives one tensor of the same type and size per gradient."""
     L = load_library()
     grads = list(grads)
     outs = grads if out is None else list(out)
-    if not grads:
-        raise ValueError("clip_grad_norm: no gradients")
-    if len(outs) != len(grads):
-        raise ValueError("clip_grad_norm: out must hold one tensor per gradient")
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        for t, name in ((g, f"grads[{i}]"), (o, f"out[{i}]")):
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"{name} must be a torch.Tensor")
-            if t.dtype not in CLIP_TYPES:
-                raise TypeError(f"{name} must be fp32, bf16 or fp16, got {t.dtype}")
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a GPU tensor (no CPU path exists)")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-        if o.shape != g.shape or o.dtype != g.dtype:
-            raise ValueError(f"out[{i}] must have the shape and type of grads[{i}]")
-    _same_device(*grads, *outs)
     n = len(grads)
+    if not n:
+        raise ValueError("clip_grad_norm: no gradients")
+    if len(outs) != n:
+        raise ValueError("clip_grad_norm: out must hold one tensor per gradient")
+    T = torch.Tensor
+    both = grads if outs is grads else grads + outs
+    # one pass per property: the calls that matter here hold hundreds of tensors
+    dtypes, counts, devices = [t.dtype for t in both], list(map(T.numel, both)), set(map(T.get_device, both))
+    try:
+        types = [CLIP_TYPES[d] for d in dtypes]
+    except KeyError as e:
+        raise TypeError(f"clip_grad_norm: gradients must be fp32, bf16 or fp16, got {e.args[0]}") from None
+    if len(devices) != 1 or -1 in devices:
+        raise ValueError("clip_grad_norm: gradients must be GPU tensors of one device (no CPU path exists)")
+    if not all(map(T.is_contiguous, both)):
+        raise ValueError("clip_grad_norm: gradients must be contiguous")
+    if outs is not grads and (dtypes[:n] != dtypes[n:] or counts[:n] != counts[n:]):
+        raise ValueError("clip_grad_norm: out[i] must have the type and size of grads[i]")
+    ptrs = list(map(T.data_ptr, both))
     P = ctypes.c_void_p
-    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    types = (ctypes.c_int32 * n)(*[CLIP_TYPES[g.dtype] for g in grads])
-    gp, op = (P * n)(*[g.data_ptr() for g in grads]), (P * n)(*[o.data_ptr() for o in outs])
+    sizes, kinds = (ctypes.c_int64 * n)(*counts[:n]), (ctypes.c_int32 * n)(*types[:n])
+    gp = (P * n)(*ptrs[:n])
+    op = gp if outs is grads else (P * n)(*ptrs[n:])
     norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
     ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_clip_workspace_size(sizes, n)), grads[0])
-    _check("fp8_clip_grad_norm", L.fp8_clip_grad_norm(gp, op, sizes, types, n, float(max_norm), _ptr(norm), ws,
+    _check("fp8_clip_grad_norm", L.fp8_clip_grad_norm(gp, op, sizes, kinds, n, float(max_norm), _ptr(norm), ws,
                                                       ws_bytes, _stream(grads[0])))
     return norm
