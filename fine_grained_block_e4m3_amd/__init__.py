@@ -128,7 +128,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fp8_gated_workspace_size.argtypes = [I64, I64, I64, I32]
     L.fp8_gated_workspace_size.restype = ctypes.c_size_t
     L.fp8_gated_nt_grad.argtypes = [P] * 9 + [I64, I64, I64, I32, P, ctypes.c_size_t, P]
-    L.fp8_gated_grad_workspace_size.argtypes = [I64, I64]
+    L.fp8_gated_grad_workspace_size.argtypes = [I64, I64, I64]
     L.fp8_gated_grad_workspace_size.restype = ctypes.c_size_t
     L.fp8_gemv_w4.argtypes = [P] * 5 + [I64, I64, I64, I32, P]
     L.fp8_gated_gemv_w4.argtypes = [P] * 8 + [I64, I64, I64, I32, I32, P]
@@ -540,7 +540,7 @@ def gated_nt_grad(dh, g, u, x, wg, wu, act: str = "silu", need_dx: bool = True, 
     else:
         ys = [_out(t, f"out[{i}]", torch.bfloat16, shape, dh) if w else None
               for i, (t, shape, w) in enumerate(zip(out, shapes, wanted))]
-    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_gated_grad_workspace_size(M, N)), dh)
+    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_gated_grad_workspace_size(M, N, K)), dh)
     _check("fp8_gated_nt_grad", L.fp8_gated_nt_grad(
         _ptr(dh), _ptr(g), _ptr(u), _ptr(x), _ptr(wg), _ptr(wu), *[_ptr(t) if t is not None else None for t in ys],
         M, N, K, a, ws, ws_bytes, _stream(dh)))

@@ -133,16 +133,89 @@ fp8_status run_gated(fp8k::GemmParams& p, int32_t outputs, uint32_t flags, void*
 // ---------------------------------------------------------------------------
 int64_t grad_np(int64_t N) { return cdiv(N, 64) * 64; }
 
-template <int BM, int BN, int WM, int WN, int STAGES>
-fp8_status launch_grad(fp8k::GatedGradParams p, hipStream_t stream) {
-    const int64_t nt = cdiv(p.K, BN);
-    const int64_t dx = p.dx ? cdiv(p.M, BM) * nt : 0, dw = p.dw[0] ? 2 * cdiv(p.N, BM) * nt : 0;
-    if (dx + dw > 0x7FFFFFFF) return FP8_ERR_UNSUPPORTED;
-    if (dx + dw == 0) return FP8_OK;
-    p.dx_tiles = (int32_t)dx;
-    hipLaunchKernelGGL((fp8k::gated_grad_gemm_kernel<BM, BN, WM, WN, STAGES>), dim3((unsigned)(dx + dw)),
-                       dim3(64 * WM * WN), 0, stream, p);
+// Tiles and splits of the two products.
+struct GradPlan {
+    bool big;                   // 128x256 tiles, else 128x128
+    bool dw_first;
+    int64_t dx_tiles, dw_tiles, dx_splits, dw_splits;
+    size_t d_bytes, dx_part, dw_part;   // workspace: dg and du, then FP32 sums
+    size_t bytes() const { return d_bytes + dx_part + dw_part; }
+};
+
+// Two 128x256 workgroups of four waves fit a compute unit, or three of 128x128
+// (64x128 and 64x64 per wave); a second and third workgroup multiply while one
+// waits at a barrier, fills its stages or stores.  128x256 reads a quarter
+// less from LDS per product and is faster once the work of a slot is several
+// times the longest tile; below that the finer tiles balance better (one
+// MI355X, 128x256 against 128x128: 4096x2048x7168 408 and 458 us,
+// 3000x2048x7168 371 and 369, 8192x7168x640 384 and 329, 500x2112x7168 87 and
+// 75).  One 256x256 workgroup of eight waves per unit: 437 us on the first.
+GradPlan grad_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int cus) {
+    GradPlan pl{};
+    const int64_t dx_blocks = 2 * grad_np(N) / 32, dw_blocks = cdiv(M, 32);
+    auto tiles = [&](int bn) {
+        pl.dx_tiles = dx ? cdiv(M, 128) * cdiv(K, bn) : 0;
+        pl.dw_tiles = dw ? 2 * cdiv(N, 128) * cdiv(K, bn) : 0;
+        return pl.dx_tiles * dx_blocks + pl.dw_tiles * dw_blocks;   // 32-step blocks
+    };
+    const int64_t longest = dx && (!dw || dx_blocks > dw_blocks) ? dx_blocks : dw_blocks;
+    pl.big = tiles(256) >= 2 * cus * 3 * longest;
+    const int64_t share = tiles(pl.big ? 256 : 128) / (3 * cus);    // blocks per slot
+    pl.dw_first = dw_blocks > dx_blocks;
+    pl.d_bytes = (size_t)(2 * M * grad_np(N)) * sizeof(uint16_t);
+    // A product whose few tiles have contractions several times the share of a
+    // slot would run alone at the end: split it.
+    auto splits = [&](int64_t n_tiles, int64_t blocks) {
+        const int64_t s = n_tiles ? blocks / (share > 16 ? share : 16) : 1;
+        return pl.big || s < 3 ? (int64_t)1 : s > 8 ? (int64_t)8 : s;
+    };
+    pl.dx_splits = splits(pl.dx_tiles, dx_blocks);
+    pl.dw_splits = splits(pl.dw_tiles, dw_blocks);
+    if (pl.dx_splits > 1) pl.dx_part = (size_t)(pl.dx_splits * M * K) * sizeof(float);
+    if (pl.dw_splits > 1) pl.dw_part = (size_t)(pl.dw_splits * 2 * N * K) * sizeof(float);
+    return pl;
+}
+
+template <int BN, int OCC>
+fp8_status launch_grad(const fp8k::GatedGradParams& p, bool dw_first, hipStream_t stream) {
+    const int64_t wgs = (int64_t)p.dx_tiles * p.dx_splits + (int64_t)p.dw_tiles * p.dw_splits;
+    hipLaunchKernelGGL((fp8k::gated_grad_gemm_kernel<128, BN, 2, 2, 3, OCC>), dim3((unsigned)wgs), dim3(256), 0, stream,
+                       p, dw_first);
     return launch_status();
+}
+
+fp8_status launch_grad_join(const float* part, int64_t splits, int64_t half, int64_t total, uint16_t* out0,
+                            uint16_t* out1, hipStream_t stream) {
+    hipLaunchKernelGGL(fp8k::gated_grad_join_kernel, dim3((unsigned)cdiv(total, 1024)), dim3(256), 0, stream, part,
+                       (int)splits, half, total, out0, out1);
+    return launch_status();
+}
+
+fp8_status run_grad(fp8k::GatedGradParams& p, const GradPlan& pl, uint8_t* ws, hipStream_t s) {
+    if (pl.dx_tiles * pl.dx_splits + pl.dw_tiles * pl.dw_splits > 0x7FFFFFFF ||
+        cdiv(p.M * (p.NP / 8), 256) > 0x7FFFFFFF)
+        return FP8_ERR_UNSUPPORTED;
+    p.d = reinterpret_cast<uint16_t*>(ws);
+    p.dx_part = reinterpret_cast<float*>(ws + pl.d_bytes);
+    p.dw_part = reinterpret_cast<float*>(ws + pl.d_bytes + pl.dx_part);
+    p.dx_tiles = (int32_t)pl.dx_tiles;
+    p.dw_tiles = (int32_t)pl.dw_tiles;
+    p.dx_splits = (int32_t)pl.dx_splits;
+    p.dw_splits = (int32_t)pl.dw_splits;
+    if (pl.dx_tiles + pl.dw_tiles == 0) return FP8_OK;
+    fp8_status st = FP8_OK;
+    if (p.M && p.N) {
+        const dim3 grid((unsigned)cdiv(p.M * (p.NP / 8), 256)), block(256);
+        if (p.N % 8 == 0) hipLaunchKernelGGL(fp8k::gated_grad_act_kernel<true>, grid, block, 0, s, p);
+        else hipLaunchKernelGGL(fp8k::gated_grad_act_kernel<false>, grid, block, 0, s, p);
+        st = launch_status();
+    }
+    if (st == FP8_OK) st = pl.big ? launch_grad<256, 2>(p, pl.dw_first, s) : launch_grad<128, 3>(p, pl.dw_first, s);
+    if (st == FP8_OK && pl.dx_splits > 1)
+        st = launch_grad_join(p.dx_part, pl.dx_splits, p.M * p.K, p.M * p.K, p.dx, nullptr, s);
+    if (st == FP8_OK && pl.dw_splits > 1)
+        st = launch_grad_join(p.dw_part, pl.dw_splits, p.N * p.K, 2 * p.N * p.K, p.dw[0], p.dw[1], s);
+    return st;
 }
 
 // ---------------------------------------------------------------------------
@@ -224,9 +297,17 @@ fp8_status fp8_gated_nt_qout(const uint8_t* xq, const float* sa, const uint8_t* 
     return run_gated(p, kOutQuant, flags, workspace, workspace ? workspace_bytes : 0, (hipStream_t)stream);
 }
 
-size_t fp8_gated_grad_workspace_size(int64_t M, int64_t N) {
-    if (!dims_ok(M) || !dims_ok(N)) return 0;
-    return (size_t)(2 * M * grad_np(N)) * sizeof(uint16_t);
+size_t fp8_gated_grad_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (!dims_ok(M) || !dims_ok(N) || !dims_ok(K) || K % 128 || K > kMaxGemmK || N > kMaxGemmK - 64) return 0;
+    int cus = 0;
+    if (current_device_cus(&cus) != FP8_OK) return 0;
+    // of a call for all gradients, or for some of them
+    size_t most = 0;
+    for (int which = 1; which <= 3; ++which) {
+        const size_t b = grad_plan(M, N, K, which & 1 && M, which & 2 && N, cus).bytes();
+        if (b > most) most = b;
+    }
+    return most;
 }
 
 fp8_status fp8_gated_nt_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, const uint16_t* x,
@@ -240,32 +321,20 @@ fp8_status fp8_gated_nt_grad(const uint16_t* dh, const uint16_t* g, const uint16
     if (!dwg != !dwu) return FP8_ERR_INVALID_ARG;
     if (M && N && (!dh || !g || !u)) return FP8_ERR_INVALID_ARG;
     if ((M && !x && dwg) || (N && (!wg || !wu) && dx)) return FP8_ERR_INVALID_ARG;
-    const size_t need = fp8_gated_grad_workspace_size(M, N);
-    if (need && !workspace) return FP8_ERR_INVALID_ARG;
-    if (workspace_bytes < need) return FP8_ERR_SCRATCH;
     for (const void* p : {(const void*)dh, (const void*)g, (const void*)u, (const void*)x, (const void*)wg,
                           (const void*)wu, (const void*)dx, (const void*)dwg, (const void*)dwu, (const void*)workspace})
         if (!aligned16(p)) return FP8_ERR_ALIGNMENT;
+    if (workspace_bytes && !workspace) return FP8_ERR_INVALID_ARG;
     int cus = 0;
-    fp8_status st = current_device_cus(&cus);
+    const fp8_status st = current_device_cus(&cus);
     if (st != FP8_OK) return st;
+    const GradPlan pl = grad_plan(M, N, K, dx && M, dwg && N, cus);
+    if (workspace_bytes < pl.bytes()) return FP8_ERR_SCRATCH;
     fp8k::GatedGradParams p{};
     p.dh = dh; p.g = g; p.u = u; p.x = x; p.w[0] = wg; p.w[1] = wu;
-    p.d = static_cast<uint16_t*>(workspace);
-    p.dx = M ? dx : nullptr; p.dw[0] = N ? dwg : nullptr; p.dw[1] = N ? dwu : nullptr;
+    p.dx = dx; p.dw[0] = dwg; p.dw[1] = dwu;
     p.M = M; p.N = N; p.K = K; p.NP = grad_np(N); p.act = act;
-    hipStream_t s = (hipStream_t)stream;
-    if (M && N) {
-        const int64_t blocks = cdiv(M * (p.NP / 8), 256);
-        if (blocks > 0x7FFFFFFF) return FP8_ERR_UNSUPPORTED;
-        if (N % 8 == 0)
-            hipLaunchKernelGGL(fp8k::gated_grad_act_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, p);
-        else
-            hipLaunchKernelGGL(fp8k::gated_grad_act_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, p);
-        st = launch_status();
-        if (st != FP8_OK) return st;
-    }
-    return launch_grad<256, 256, 2, 2, 4>(p, s);
+    return run_grad(p, pl, static_cast<uint8_t*>(workspace), (hipStream_t)stream);
 }
 
 fp8_status fp8_gemv_w4(const uint16_t* x, const uint8_t* w, const void* s, const uint8_t* z, uint16_t* y, int64_t M,

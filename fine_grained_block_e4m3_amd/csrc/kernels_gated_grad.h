@@ -37,7 +37,10 @@ struct GatedGradParams {
     uint16_t* dw[2];            // (N, K) or null
     int64_t M, N, K, NP;        // NP: N rounded up to a multiple of 64
     int32_t act;
-    int32_t dx_tiles;           // workgroups of dX; those of dWg and dWu follow
+    int32_t dx_tiles, dw_tiles; // tiles of dX, and of dWg and dWu together
+    int32_t dx_splits, dw_splits;   // workgroups per tile along the contraction
+    float* dx_part;             // dx_splits > 1: FP32 sums [split][M][K]
+    float* dw_part;             // dw_splits > 1: FP32 sums [split][2][N][K]
 };
 
 // Eight elements of a row per thread.
@@ -148,7 +151,9 @@ struct GradTile {
     int64_t p_step, q_step;     // elements per contraction step
     int segs;
     int64_t len;
+    int split, splits;          // this workgroup's share of the contraction
     uint16_t* out;              // result element (0, 0) of the tile
+    float* part;                // ... of this split's FP32 sums (splits > 1)
     int64_t out_ld;
     int rows, cols;             // valid part
 };
@@ -160,7 +165,7 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
     using P = GradOperand<BM, NWAVES, PSLOW>;
     using Q = GradOperand<BN, NWAVES, true>;
     constexpr int STAGE = P::BYTES + Q::BYTES, NL = P::PER + Q::PER;
-    static_assert((STAGES - 2) * NL <= 63, "vmcnt range");
+    static_assert(STAGES >= 2 && (STAGES - 1) * NL <= 63, "vmcnt range");
 
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
@@ -180,16 +185,19 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
     for (int b = 0; b < FJ; ++b) qf[b] = Q::fragment(wn * TN + 32 * b, lane);
 
     const int per_seg = (int)((t.len + 31) / 32);
-    const int nblocks = per_seg * t.segs;
+    const int all = per_seg * t.segs;
+    const int first = (int)((int64_t)all * t.split / t.splits);
+    const int nblocks = (int)((int64_t)all * (t.split + 1) / t.splits) - first;
     // The operands' corners advance block by block; a range that has run out
     // (past the operand, or past the last block) reads zeros.
     auto range = [](int64_t elems) FP8K_INLINE {
         return (uint32_t)(elems <= 0 ? 0 : elems >= (1ll << 30) ? (1ll << 31) : 2 * elems);
     };
-    auto issue = [&](int kb, int stage) FP8K_INLINE {
+    auto issue = [&](int i, int stage) FP8K_INLINE {
+        const bool live = i < nblocks;
+        const int kb = first + i;
         const int z = t.segs > 1 && kb >= per_seg ? 1 : 0;
         const int64_t k0 = (int64_t)(kb - z * per_seg) * 32;
-        const bool live = kb < nblocks;
         const i32x4 pr = make_rsrc(t.pb[z] + k0 * t.p_step, live ? range(t.p_elems - k0 * t.p_step) : 0u);
         const i32x4 qr = make_rsrc(t.qb[z] + k0 * t.q_step, live ? range(t.q_elems - k0 * t.q_step) : 0u);
         const uint32_t dst = lds0 + (uint32_t)(stage * STAGE + wave * 1024);
@@ -207,33 +215,49 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.f;
 
+    // Operands are read one half block (16 steps) ahead of the products.  A
+    // block's barrier sits in the middle of the block before it: there every
+    // wave has read all of its current block, whose stage the loads of the
+    // block STAGES further then overwrite, and its own loads of the next
+    // block have landed.
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
-
-    int stage = 0;
-    for (int kb = 0; kb < nblocks; ++kb) {
-        // this wave's loads of block kb have landed; every wave's have after
-        // the barrier, and every wave is past its reads of the stage that the
-        // next loads overwrite
-        wait_vmcnt<(STAGES - 2) * NL>();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        lds_barrier();
-        issue(kb + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+    for (int s = 0; s < STAGES; ++s) issue(s, s);
+    wait_vmcnt<(STAGES - 1) * NL>();
+    lds_barrier();
+    struct Operands {
+        bf16x8 p[FI], q[FJ];
+    };
+    auto read = [&](Operands& o, int stage, int s) FP8K_INLINE {
         FP8K_LDS const uint8_t* base = lds + stage * STAGE;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            bf16x8 pv[FI], qv[FJ];
+        for (int a = 0; a < FI; ++a) o.p[a] = P::read(base, pf[a], s, lane);
 #pragma unroll
-            for (int a = 0; a < FI; ++a) pv[a] = P::read(base, pf[a], s, lane);
+        for (int b = 0; b < FJ; ++b) o.q[b] = Q::read(base + P::BYTES, qf[b], s, lane);
+    };
+    auto multiply = [&](const Operands& o) FP8K_INLINE {
 #pragma unroll
-            for (int b = 0; b < FJ; ++b) qv[b] = Q::read(base + P::BYTES, qf[b], s, lane);
+        for (int a = 0; a < FI; ++a)
 #pragma unroll
-            for (int a = 0; a < FI; ++a)
-#pragma unroll
-                for (int b = 0; b < FJ; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qv[b], pv[a], acc[a][b], 0, 0, 0);
-        }
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
+            for (int b = 0; b < FJ; ++b)
+                acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.q[b], o.p[a], acc[a][b], 0, 0, 0);
+    };
+    Operands o0, o1;
+    read(o0, 0, 0);
+    int stage = 0;
+    for (int kb = 0; kb < nblocks; ++kb) {
+        const int next = stage + 1 == STAGES ? 0 : stage + 1;
+        __builtin_amdgcn_sched_barrier(0);
+        read(o1, stage, 1);
+        multiply(o0);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_vmcnt<(STAGES - 2) * NL>();
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        read(o0, next, 0);
+        issue(kb + STAGES, stage);
+        multiply(o1);
+        stage = next;
     }
     wait_vmcnt<0>();
 
@@ -249,7 +273,11 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
             for (int q = 0; q < 4; ++q) {
                 const int n = wn * TN + 32 * b + 8 * q + 4 * h;
                 // K % 128 == 0: whole groups of 4 columns, 8-byte aligned
-                if (n < t.cols)
+                if (n >= t.cols) continue;
+                if (t.splits > 1)
+                    *reinterpret_cast<f32x4*>(t.part + (int64_t)m * t.out_ld + n) =
+                        f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+                else
                     *reinterpret_cast<uint2*>(t.out + (int64_t)m * t.out_ld + n) =
                         make_uint2(pack_bf16x2(acc[a][b][4 * q], acc[a][b][4 * q + 1]),
                                    pack_bf16x2(acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]));
@@ -257,9 +285,11 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
     }
 }
 
-// Workgroups [0, dx_tiles): tiles of dX; the rest: tiles of dWg, then of dWu.
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gated_grad_gemm_kernel(GatedGradParams p) {
+// Workgroups: the tiles of dX, then those of dWg and dWu (dw_first: the other
+// way round, the product with the longer contraction first), each tile's
+// splits side by side.
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int OCC>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void gated_grad_gemm_kernel(GatedGradParams p, bool dw_first) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * (BM + BN) * 64];
     const int nt = (int)((p.K + BN - 1) / BN);
     // workgroup b of a dispatch wave lands on XCD b % 8: each XCD takes a run
@@ -268,12 +298,18 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gated_grad_gemm_ker
         const int per = count / 8, rest = count % 8, xcd = b % 8;
         return xcd * per + min(xcd, rest) + b / 8;
     };
+    const int dx_wgs = p.dx_tiles * p.dx_splits, dw_wgs = p.dw_tiles * p.dw_splits;
+    const bool is_dx = dw_first ? (int)blockIdx.x >= dw_wgs : (int)blockIdx.x < dx_wgs;
+    const int id = (int)blockIdx.x - (is_dx == dw_first ? (dw_first ? dw_wgs : dx_wgs) : 0);
     int mt, ntile;
     GradTile t;
     t.q_ld = t.q_step = p.K;
-    if ((int)blockIdx.x < p.dx_tiles) {
-        const int tile = run_of(blockIdx.x, p.dx_tiles);
-        raster(tile, (int)((p.M + BM - 1) / BM), nt, 4, mt, ntile);
+    t.out_ld = p.K;
+    if (is_dx) {
+        const int at = run_of(id, dx_wgs);
+        t.splits = p.dx_splits;
+        t.split = at % t.splits;
+        raster(at / t.splits, (int)((p.M + BM - 1) / BM), nt, 4, mt, ntile);
         const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)ntile * BN;
         for (int z = 0; z < 2; ++z) {
             t.pb[z] = p.d + (z * p.M + m0) * p.NP;
@@ -286,13 +322,16 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gated_grad_gemm_ker
         t.segs = 2;
         t.len = p.NP;
         t.out = p.dx + m0 * p.K + n0;
-        t.out_ld = p.K;
+        t.part = p.dx_part + (t.split * p.M + m0) * p.K + n0;
         t.rows = (int)min((int64_t)BM, p.M - m0);
         t.cols = (int)min((int64_t)BN, p.K - n0);
         grad_tile<BM, BN, WAVES_M, WAVES_N, STAGES, false>(t, smem);
     } else {
         const int rt = (int)((p.N + BM - 1) / BM);
-        const int tile = run_of(blockIdx.x - p.dx_tiles, 2 * rt * nt);
+        const int at = run_of(id, dw_wgs);
+        t.splits = p.dw_splits;
+        t.split = at % t.splits;
+        const int tile = at / t.splits;
         const int z = tile >= rt * nt;
         raster(tile - z * rt * nt, rt, nt, 4, mt, ntile);
         const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)ntile * BN;
@@ -304,11 +343,23 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gated_grad_gemm_ker
         t.segs = 1;
         t.len = p.M;
         t.out = p.dw[z] + m0 * p.K + n0;
-        t.out_ld = p.K;
+        t.part = p.dw_part + ((2 * t.split + z) * p.N + m0) * p.K + n0;
         t.rows = (int)min((int64_t)BM, p.N - m0);
         t.cols = (int)min((int64_t)BN, p.K - n0);
         grad_tile<BM, BN, WAVES_M, WAVES_N, STAGES, true>(t, smem);
     }
+}
+
+// out = the splits' FP32 sums in split order, rounded; four elements per
+// thread of `half` to out0 and the next `half` to out1 (K % 128 == 0).
+__global__ __launch_bounds__(256) void gated_grad_join_kernel(const float* __restrict__ part, int splits, int64_t half,
+                                                              int64_t total, uint16_t* out0, uint16_t* out1) {
+    const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (i >= total) return;
+    f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
+    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(part + s * total + i);
+    uint16_t* out = i < half ? out0 + i : out1 + (i - half);
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
 }  // namespace fp8k

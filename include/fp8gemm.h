@@ -395,7 +395,7 @@ fp8_status fp8_gated_nt_qout(const uint8_t* xq, const float* sa, const uint8_t* 
  *   N == 0 dx is.
  * dg and du are formed in FP32 and rounded to BF16, the matrix instruction's
  * type; sums are FP32, and each result is rounded once.  The workspace (dg
- * and du) is required: fp8_gated_grad_workspace_size() bytes, else
+ * and du, and FP32 sums where a contraction is split) is required: fp8_gated_grad_workspace_size() bytes, else
  * FP8_ERR_SCRATCH.
  */
 fp8_status fp8_gated_nt_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
@@ -403,7 +403,7 @@ fp8_status fp8_gated_nt_grad(const uint16_t* dh, const uint16_t* g, const uint16
                              uint16_t* dx, uint16_t* dwg, uint16_t* dwu, int64_t M,
                              int64_t N, int64_t K, int32_t act, void* workspace,
                              size_t workspace_bytes, void* stream);
-size_t fp8_gated_grad_workspace_size(int64_t M, int64_t N);
+size_t fp8_gated_grad_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /* ---------------------------------------------------------------------------
  * Matrix-vector products with 4-bit weights and group scales, for up to 16
