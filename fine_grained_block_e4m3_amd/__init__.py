@@ -471,8 +471,9 @@ def _gated_operands(xq, sa, wgq, sbg, wuq, sbu, fn: str):
 
 
 def _gated_workspace_size(M: int, N: int, K: int, outputs: int) -> int:
-    # only decode-sized M uses a workspace
-    return int(load_library().fp8_gated_workspace_size(M, N, K, outputs)) if M <= 64 else 0
+    if M <= 64 and outputs == 0:
+        return 0            # one kernel, K split inside its workgroups
+    return int(load_library().fp8_gated_workspace_size(M, N, K, outputs))
 
 
 def gated_nt(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = False, save: bool = False, out=None,
@@ -480,13 +481,14 @@ def gated_nt(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = False,
     """Gated feed-forward block on block-scaled E4M3 operands: h (M, N) bf16 =
     act(X Wg^T) * (X Wu^T), act "silu" or "gelu" (tanh form).  With save the
     projections are returned too: (h, g, u), which gated_nt_grad takes.  out:
-    h, or (h, g, u).  workspace: for decode-sized M, as for gemm_nt."""
+    h, or (h, g, u).  workspace: as for gemm_nt, where the output has too few
+    tiles to fill the device."""
     L = load_library()
     a = _act(act)
     M, N, K = _gated_operands(xq, sa, wgq, sbg, wuq, sbu, "gated_nt")
     count = 3 if save else 1
     if out is None:
-        ys = [torch.empty((M, N), dtype=torch.bfloat16, device=xq.device) for _ in range(count)]
+        ys = [xq.new_empty((M, N), dtype=torch.bfloat16) for _ in range(count)]
     else:
         ys = list(out) if save else [out]
         if len(ys) != count:
@@ -581,7 +583,7 @@ def gemv_w4(x, w, scales, zeros=None, out=None) -> torch.Tensor:
     group = _w4(w, scales, zeros, N, K, "w")
     _same_device(x, w, scales)
     y = _out(out, "out", torch.bfloat16, (M, N), x) if out is not None \
-        else torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        else x.new_empty((M, N))
     _check("fp8_gemv_w4", L.fp8_gemv_w4(_ptr(x), _ptr(w), _ptr(scales), _ptr(zeros) if zeros is not None else None,
                                         _ptr(y), M, N, K, group, _stream(x)))
     return y
@@ -601,7 +603,7 @@ def gated_gemv_w4(x, wg, scales_g, wu, scales_u, zeros_g=None, zeros_u=None, act
         raise ValueError("gated_gemv_w4: both weights must have one format")
     _same_device(x, wg, scales_g, wu, scales_u)
     y = _out(out, "out", torch.bfloat16, (M, N), x) if out is not None \
-        else torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        else x.new_empty((M, N))
     _check("fp8_gated_gemv_w4", L.fp8_gated_gemv_w4(
         _ptr(x), _ptr(wg), _ptr(scales_g), _ptr(zeros_g) if zeros_g is not None else None, _ptr(wu), _ptr(scales_u),
         _ptr(zeros_u) if zeros_u is not None else None, _ptr(y), M, N, K, group, a, _stream(x)))

@@ -7,16 +7,15 @@
 // allocates, frees nor synchronizes.
 #include "host_common.h"
 #include "kernels_clip.h"
-#include "kernels_decode.h"
 #include "kernels_exact.h"
 #include "kernels_gated_grad.h"
+#include "kernels_gated_join.h"
 #include "skinny.h"
 
 namespace {
 
 using namespace fp8h;
 
-constexpr int64_t kMaxDecodeM = 64;
 
 bool act_ok(int32_t act) { return act == FP8_ACT_SILU || act == FP8_ACT_GELU; }
 
@@ -25,69 +24,100 @@ bool act_ok(int32_t act) { return act == FP8_ACT_SILU || act == FP8_ACT_GELU; }
 // ---------------------------------------------------------------------------
 enum GatedOutputs : int32_t { kOutH = 0, kOutSave = 1, kOutQuant = 2 };
 
-// Decode-sized M: workgroups along K per 96-column tile of either projection.
-constexpr int kDecodeTile = 96, kDecodeWaves = 3, kDecodeChunk = 4;
-constexpr int decode_kbmax(int64_t M) { return M <= 32 ? 24 : 12; }   // X-resident kernel: K blocks per workgroup
-int64_t gated_splits(int64_t N, int64_t K, int cus) {
-    const int64_t tiles = 2 * cdiv(N, kDecodeTile);
-    int64_t s = tiles < cus ? cus / tiles : 1;
-    if (s > K / 128) s = K / 128;
-    return s > 8 ? 8 : s;
+// Up to 64 tokens, and only h wanted: one kernel built around the weights'
+// stream (kernels_skinny.h), K split inside its workgroups.
+bool gated_skinny(int64_t M, int32_t outputs) { return M <= kMaxSkinnyGatedM && outputs == kOutH; }
+
+// Tiles of the rest: rows x output columns, and the time of one K block when
+// every compute unit has one (one MI355X, K 7168, us).
+enum GatedTile : int { kGated256x128, kGated128x128, kGated128x64, kGated64x128, kGated64x64, kGatedTiles };
+struct GatedTileInfo {
+    int bm, cols;
+    double us;
+    bool quant;                 // has a quantized-output form (its 128 columns are one group)
+};
+constexpr GatedTileInfo kGatedTile[kGatedTiles] = {
+    {256, 128, 3.54, true}, {128, 128, 1.88, true}, {128, 64, 1.14, false}, {64, 128, 1.12, true}, {64, 64, 0.85, false}};
+
+// The tile, and the workgroups along K per tile (only where the tiles leave
+// compute units idle, all in one round), with the least estimated time: the
+// rounds' K blocks, 3 us to start and end a round, and for a split a second
+// launch (4 us) and its FP32 sums written and read at 4 TB/s.
+struct GatedPlan {
+    GatedTile tile;
+    int64_t splits;
+};
+GatedPlan gated_plan(int64_t M, int64_t N, int64_t K, bool quant, bool may_split, int cus) {
+    GatedPlan best{kGated256x128, 1};
+    double least = 1e30;
+    const int64_t kb = K / 128;
+    for (int t = 0; t < kGatedTiles; ++t) {
+        const GatedTileInfo& i = kGatedTile[t];
+        const int64_t tiles = cdiv(M, i.bm) * cdiv(N, i.cols);
+        for (int64_t s = 1; s <= 8; ++s) {
+            if (s > 1 && (!may_split || tiles * s > cus || kb < 4 * s)) break;
+            if (s == 1 && quant && !i.quant) continue;
+            double us = (double)cdiv(tiles, cus) * (i.us * (double)cdiv(kb, s) + 3.0);
+            if (s > 1) us += 4.0 + 16.0 * (double)(s * M * N) / 4e6;
+            if (us < least) {
+                least = us;
+                best = {(GatedTile)t, s};
+            }
+        }
+    }
+    return best;
 }
-bool gated_skinny(int64_t M, int32_t outputs) { return M <= kMaxSkinnyM && outputs == kOutH; }
+
 size_t gated_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t outputs, int cus) {
-    if (M > kMaxDecodeM || gated_skinny(M, outputs)) return 0;
-    return (size_t)(2 * gated_splits(N, K, cus) * M * N) * sizeof(float);
+    if (gated_skinny(M, outputs)) return 0;
+    const int64_t s = gated_plan(M, N, K, outputs == kOutQuant, true, cus).splits;
+    return s > 1 ? (size_t)(2 * s * M * N) * sizeof(float) : 0;
 }
 
 template <int BM, int BN, int WM, int WN, bool POW2, int STAGES, bool QOUT = false>
-fp8_status launch_gated_tile(fp8k::GemmParams p, int cus, hipStream_t stream) {
+fp8_status launch_gated_tile(fp8k::GemmParams p, int64_t splits, int cus, hipStream_t stream) {
     p.m_tiles = (int)cdiv(p.M, BM);
     p.n_tiles = (int)cdiv(p.N, BN / 2);
     p.group_m = 4;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-    const int grid = (int)(tiles < cus ? tiles : cus);
-    hipLaunchKernelGGL((fp8k::gemm_exact_kernel<BM, BN, WM, WN, fp8k::kDense, POW2, STAGES, QOUT, true>), dim3(grid),
+    const dim3 grid((unsigned)(tiles < cus ? tiles : cus), (unsigned)splits);
+    hipLaunchKernelGGL((fp8k::gemm_exact_kernel<BM, BN, WM, WN, fp8k::kDense, POW2, STAGES, QOUT, true>), grid,
                        dim3(64 * WM * WN), 0, stream, p.xq, p.sa, p.wq, p.sb, p.y, p.m_indices, p.masked_m, p);
     return launch_status();
 }
 
-// Largest tile that still gives every compute unit one.
-template <bool POW2>
-fp8_status run_gated_tiles(const fp8k::GemmParams& p, bool quant, int cus, hipStream_t stream) {
-    const bool big = cdiv(p.M, 256) * cdiv(p.N, 128) >= cus;
-    if (quant)
-        return big ? launch_gated_tile<256, 256, 4, 2, POW2, 2, true>(p, cus, stream)
-                   : launch_gated_tile<128, 256, 2, 4, POW2, 3, true>(p, cus, stream);
-    if (big) return launch_gated_tile<256, 256, 4, 2, POW2, 2>(p, cus, stream);
-    if (cdiv(p.M, 128) * cdiv(p.N, 128) >= cus) return launch_gated_tile<128, 256, 2, 4, POW2, 3>(p, cus, stream);
-    if (cdiv(p.M, 128) * cdiv(p.N, 64) >= cus) return launch_gated_tile<128, 128, 2, 2, POW2, 4>(p, cus, stream);
-    return launch_gated_tile<64, 128, 2, 2, POW2, 4>(p, cus, stream);
-}
-
-// Decode-sized M: partial sums of both projections, then the joining kernel.
-template <int MSUB>
-void launch_gated_decode(const fp8k::GemmParams& p, int64_t splits, hipStream_t stream) {
-    const dim3 grid((unsigned)cdiv(p.N, kDecodeTile), (unsigned)splits, 2), block(64 * kDecodeWaves);
-    if (cdiv(p.K / 128, splits) <= decode_kbmax(p.M))
-        hipLaunchKernelGGL((fp8k::decode_exact_x_kernel<MSUB, kDecodeWaves, 4, MSUB == 1 ? 24 : 12, true>), grid, block,
-                           0, stream, p.xq, p.sa, p.wq, p.sb, p.y, p);
-    else
-        hipLaunchKernelGGL((fp8k::decode_exact_kernel<MSUB, kDecodeWaves, 5, kDecodeChunk, true>), grid, block, 0,
-                           stream, p.xq, p.sa, p.wq, p.sb, p.y, p);
-}
-
-fp8_status run_gated_decode(const fp8k::GemmParams& p, bool quant, bool pow2, int64_t splits, hipStream_t stream) {
-    if (p.M <= 32) launch_gated_decode<1>(p, splits, stream);
-    else launch_gated_decode<2>(p, splits, stream);
-    const fp8_status st = launch_status();
-    if (st != FP8_OK) return st;
-    const dim3 grid((unsigned)cdiv(p.M * cdiv(p.N, 128), 4)), block(256);
+// The joining kernel: K splits' sums to the outputs.
+fp8_status launch_gated_join(const fp8k::GemmParams& p, bool quant, bool pow2, int64_t splits, hipStream_t stream) {
+    const int64_t blocks = cdiv(p.M * cdiv(p.N, 128), 4);
+    if (blocks > 0x7FFFFFFF) return FP8_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks), block(256);
     const int s = (int)splits;
-    if (!quant) hipLaunchKernelGGL((fp8k::decode_gated_reduce<false, false>), grid, block, 0, stream, p, s);
-    else if (pow2) hipLaunchKernelGGL((fp8k::decode_gated_reduce<true, true>), grid, block, 0, stream, p, s);
-    else hipLaunchKernelGGL((fp8k::decode_gated_reduce<true, false>), grid, block, 0, stream, p, s);
+    if (!quant) hipLaunchKernelGGL((fp8k::gated_join_kernel<false, false>), grid, block, 0, stream, p, s);
+    else if (pow2) hipLaunchKernelGGL((fp8k::gated_join_kernel<true, true>), grid, block, 0, stream, p, s);
+    else hipLaunchKernelGGL((fp8k::gated_join_kernel<true, false>), grid, block, 0, stream, p, s);
     return launch_status();
+}
+
+template <bool POW2>
+fp8_status run_gated_tiles(const fp8k::GemmParams& p, bool quant, bool may_split, int cus, hipStream_t stream) {
+    const GatedPlan pl = gated_plan(p.M, p.N, p.K, quant, may_split, cus);
+    const int64_t s = pl.splits;
+    if (s == 1 && quant) {
+        switch (pl.tile) {
+            case kGated256x128: return launch_gated_tile<256, 256, 4, 2, POW2, 2, true>(p, 1, cus, stream);
+            case kGated128x128: return launch_gated_tile<128, 256, 2, 4, POW2, 3, true>(p, 1, cus, stream);
+            default: return launch_gated_tile<64, 256, 2, 4, POW2, 3, true>(p, 1, cus, stream);
+        }
+    }
+    fp8_status st;
+    switch (pl.tile) {
+        case kGated256x128: st = launch_gated_tile<256, 256, 4, 2, POW2, 2>(p, s, cus, stream); break;
+        case kGated128x128: st = launch_gated_tile<128, 256, 2, 4, POW2, 3>(p, s, cus, stream); break;
+        case kGated128x64: st = launch_gated_tile<128, 128, 4, 2, POW2, 4>(p, s, cus, stream); break;
+        case kGated64x128: st = launch_gated_tile<64, 256, 2, 4, POW2, 3>(p, s, cus, stream); break;
+        default: st = launch_gated_tile<64, 128, 2, 2, POW2, 4>(p, s, cus, stream); break;
+    }
+    return st == FP8_OK && s > 1 ? launch_gated_join(p, quant, POW2, s, stream) : st;
 }
 
 fp8_status check_gemv(int64_t M, int64_t N, int64_t K, int32_t group) {
@@ -121,11 +151,10 @@ fp8_status run_gated(fp8k::GemmParams& p, int32_t outputs, uint32_t flags, void*
     }
     const bool quant = outputs == kOutQuant, pow2 = flags & FP8_FLAG_UE8M0;
     const size_t need = gated_ws_bytes(p.M, p.N, p.K, outputs, cus);
-    if (need && ws_bytes >= need) {
-        p.part = static_cast<float*>(ws);
-        return run_gated_decode(p, quant, pow2, gated_splits(p.N, p.K, cus), stream);
-    }
-    return pow2 ? run_gated_tiles<true>(p, quant, cus, stream) : run_gated_tiles<false>(p, quant, cus, stream);
+    const bool split = need && ws_bytes >= need;
+    if (split) p.part = static_cast<float*>(ws);
+    return pow2 ? run_gated_tiles<true>(p, quant, split, cus, stream)
+                : run_gated_tiles<false>(p, quant, split, cus, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -224,21 +253,19 @@ fp8_status run_grad(fp8k::GatedGradParams& p, const GradPlan& pl, uint8_t* ws, h
 int64_t clip_chunks(int64_t n) { return cdiv(n, fp8k::kClipChunk); }
 int clip_grid(int64_t chunks) { return (int)(chunks < fp8k::kClipMaxGrid ? chunks : fp8k::kClipMaxGrid); }
 
-// Calls f(first tensor, tensors, chunks) for each batch of the call.
+// Calls f(first tensor, tensors, chunks) for each batch of the call, or from
+// the last batch to the first.
 template <typename F>
-fp8_status clip_batches(const int64_t* sizes, int32_t count, F&& f) {
-    for (int32_t i = 0; i < count;) {
+fp8_status clip_batches(const int64_t* sizes, int32_t count, bool backwards, F&& f) {
+    const int32_t batches = (int32_t)cdiv(count, fp8k::kClipBatch);
+    for (int32_t b = 0; b < batches; ++b) {
+        const int32_t i = (backwards ? batches - 1 - b : b) * fp8k::kClipBatch;
+        const int32_t k = count - i < fp8k::kClipBatch ? count - i : fp8k::kClipBatch;
         int64_t chunks = 0;
-        int32_t k = 0;
-        for (; k < fp8k::kClipBatch && i + k < count; ++k) {
-            const int64_t c = clip_chunks(sizes[i + k]);
-            if (chunks + c > 0x7FFFFFFF) break;
-            chunks += c;
-        }
-        if (k == 0) return FP8_ERR_UNSUPPORTED;     // one tensor of over 2^44 elements
+        for (int32_t j = 0; j < k; ++j) chunks += clip_chunks(sizes[i + j]);
+        if (chunks > 0x7FFFFFFF) return FP8_ERR_UNSUPPORTED;
         const fp8_status st = f(i, k, chunks);
         if (st != FP8_OK) return st;
-        i += k;
     }
     return FP8_OK;
 }
@@ -387,7 +414,7 @@ size_t fp8_clip_workspace_size(const int64_t* sizes, int32_t count) {
     size_t slots = 0;
     for (int32_t i = 0; i < count; ++i)
         if (sizes[i] < 0) return 0;
-    (void)clip_batches(sizes, count, [&](int32_t, int32_t, int64_t chunks) {
+    (void)clip_batches(sizes, count, false, [&](int32_t, int32_t, int64_t chunks) {
         slots += (size_t)clip_grid(chunks);
         return FP8_OK;
     });
@@ -428,7 +455,7 @@ fp8_status fp8_clip_grad_norm(const void* const* grads, void* const* outs, const
         return t;
     };
     int64_t used = 0;
-    st = clip_batches(sizes, count, [&](int32_t i, int32_t k, int64_t chunks) {
+    st = clip_batches(sizes, count, false, [&](int32_t i, int32_t k, int64_t chunks) {
         if (chunks == 0) return FP8_OK;
         hipLaunchKernelGGL(fp8k::clip_norm_kernel, dim3(clip_grid(chunks)), dim3(256), 0, s, table(i, k), slots + used);
         used += clip_grid(chunks);
@@ -445,7 +472,8 @@ fp8_status fp8_clip_grad_norm(const void* const* grads, void* const* outs, const
         hipLaunchKernelGGL(fp8k::clip_scale_kernel, dim3(1), dim3(256), 0, s, fp8k::ClipTable{}, slots, 0, max_norm, norm);
         return launch_status();
     }
-    return clip_batches(sizes, count, [&](int32_t i, int32_t k, int64_t chunks) {
+    // backwards: what the first pass read last may still be in the last cache
+    return clip_batches(sizes, count, true, [&](int32_t i, int32_t k, int64_t chunks) {
         if (chunks == 0) return FP8_OK;
         hipLaunchKernelGGL(fp8k::clip_scale_kernel, dim3(clip_grid(chunks)), dim3(256), 0, s, table(i, k), slots,
                            (int)used, max_norm, norm);

@@ -52,4 +52,18 @@ __device__ __forceinline__ void store_bf16_subtile(uint16_t* row, int64_t n, int
     }
 }
 
+// The same values in FP32 (16-byte stores where every row keeps the alignment).
+__device__ __forceinline__ void store_f32_subtile(float* row, int64_t n, int64_t N, f32x16 v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q, n += 8) {
+        if ((N & 3) == 0 && n + 3 < N) {
+            *reinterpret_cast<f32x4*>(row + n) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < N) row[n + j] = v[4 * q + j];
+        }
+    }
+}
+
 }  // namespace fp8k

@@ -13,6 +13,8 @@
 //     or underflow for any finite FP32 gradient.  Every workgroup writes its
 //     sum to its own slot and the slots are added in a fixed order, so equal
 //     inputs give equal results.
+//   * The second pass runs backwards, over what the first read last, of which
+//     the 256 MB last-level cache still holds a part.
 //   * Vector loads of 16 bytes at any element alignment (gradients are often
 //     views of a flat buffer).
 #pragma once
@@ -173,7 +175,8 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(ClipTable t, const doub
     // a NaN norm stays a NaN factor; an infinite norm gives 0
     const double r = (double)max_norm / (norm + 1e-6);
     const float c = r > 1.0 ? 1.0f : (float)r;
-    for (int k = blockIdx.x; k < t.first[t.count]; k += gridDim.x) {
+    for (int b = blockIdx.x; b < t.first[t.count]; b += gridDim.x) {
+        const int k = t.first[t.count] - 1 - b;
         const int i = clip_tensor_of(t, k);
         if (c == 1.0f && t.in[i] == t.out[i]) continue;   // in place, nothing to clip
         const int64_t nt = t.n_type[i], at = (int64_t)(k - t.first[i]) * kClipChunk;

@@ -49,7 +49,6 @@
 #pragma once
 
 #include "device_common.h"
-#include "gated_common.h"
 #include "kernels_gemm.h"
 
 namespace fp8k {
@@ -279,7 +278,7 @@ namespace fp8k {
 
 // Split-K reduction of the decode GEMM: Y = BF16(sum over the splits, in
 // split order, of the FP32 partial sums [S][M][N]).
-static __global__ __launch_bounds__(256) void decode_split_reduce(const float* __restrict__ part, int S, int64_t MN,
+__global__ __launch_bounds__(256) void decode_split_reduce(const float* __restrict__ part, int S, int64_t MN,
                                                            uint16_t* __restrict__ y) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= MN) return;
@@ -560,15 +559,11 @@ __host__ __device__ constexpr int chunks_between(int pos, int D, int KBC) {
     return D > pos ? (D - pos + KBC - 1) / KBC : 0;
 }
 
-template <int MSUB, int NW, int NS, int KBC, bool GATED = false>
+template <int MSUB, int NW, int NS, int KBC>
 __global__ __launch_bounds__(64 * NW, 1) void decode_exact_kernel(
     const uint8_t* __restrict__ xq_, const float* __restrict__ sa_, const uint8_t* __restrict__ wq_,
     const float* __restrict__ sb_, uint16_t* __restrict__ y_, GemmParams p) {
     using L = DecodeExactLayout<MSUB, NW, NS, KBC>;
-    if constexpr (GATED) {
-        // the gate (grid.z 0) and the up projection (1) of a feed-forward block
-        if (blockIdx.z) wq_ = p.wq2, sb_ = p.sb2;
-    }
     constexpr int D = NS - 1, NPW = L::NPW;
     constexpr int CW = (D + KBC - 1) / KBC;             // chunks before the steady-state waits apply
     static_assert(MSUB >= 1 && MSUB <= 2 && NW >= 1 && NS >= 2, "decode tile");
@@ -732,7 +727,7 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_exact_kernel(
     wait_vmcnt<0>();
 
     // ---- stores: lane holds m = 32 ms + r32, n = nw + 8k + 4h + (0..3), k = 0..3 ----
-    float* part_base = p.part ? p.part + (int64_t)(GATED ? blockIdx.z * gridDim.y + blockIdx.y : blockIdx.y) * M * N : nullptr;
+    float* part_base = p.part ? p.part + (int64_t)blockIdx.y * M * N : nullptr;
 #pragma unroll
     for (int ms = 0; ms < MSUB; ++ms) {
         const int64_t m = 32 * ms + r32;
@@ -804,15 +799,11 @@ struct DecodeExactXLayout {
     static_assert(BYTES <= 160 * 1024, "LDS");
 };
 
-template <int MSUB, int NW, int NS, int KBMAX, bool GATED = false>
+template <int MSUB, int NW, int NS, int KBMAX>
 __global__ __launch_bounds__(64 * NW, 1) void decode_exact_x_kernel(
     const uint8_t* __restrict__ xq_, const float* __restrict__ sa_, const uint8_t* __restrict__ wq_,
     const float* __restrict__ sb_, uint16_t* __restrict__ y_, GemmParams p) {
     using L = DecodeExactXLayout<MSUB, NW, NS, KBMAX>;
-    if constexpr (GATED) {
-        // the gate (grid.z 0) and the up projection (1) of a feed-forward block
-        if (blockIdx.z) wq_ = p.wq2, sb_ = p.sb2;
-    }
     constexpr int D = NS - 1;
     static_assert(MSUB >= 1 && MSUB <= 2 && NW >= 1 && NS >= 2 && 4 * D <= 63, "decode tile");
     constexpr int TN = 32 * NW;
@@ -943,7 +934,7 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_exact_x_kernel(
     wait_vmcnt<0>();
 
     // ---- stores: lane holds m = 32 ms + r32, n = nw + 8k + 4h + (0..3), k = 0..3 ----
-    float* part_base = p.part ? p.part + (int64_t)(GATED ? blockIdx.z * gridDim.y + blockIdx.y : blockIdx.y) * M * N : nullptr;
+    float* part_base = p.part ? p.part + (int64_t)blockIdx.y * M * N : nullptr;
 #pragma unroll
     for (int ms = 0; ms < MSUB; ++ms) {
         const int64_t m = 32 * ms + r32;
@@ -976,51 +967,6 @@ __global__ __launch_bounds__(64 * NW, 1) void decode_exact_x_kernel(
                 if (n + 3 < N) yrow[n + 3] = (uint16_t)(hi >> 16);
             }
         }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Gated feed-forward block on decode-sized M: joins the FP32 partial sums of
-// the gate (part[0][s]) and up (part[1][s]) projections, s in order, and
-// forms h = act(g) * u.  A wave takes 128 columns of one row (two per lane),
-// the group of the quantized form.
-// ---------------------------------------------------------------------------
-template <bool QOUT, bool POW2>
-__global__ __launch_bounds__(256) void decode_gated_reduce(GemmParams p, int S) {
-    const int64_t groups = (p.N + 127) / 128;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (id >= p.M * groups) return;
-    const int lane = threadIdx.x & 63;
-    const int64_t m = id / groups, n = (id - m * groups) * 128 + 2 * lane;
-    const int64_t mn = p.M * p.N, at = m * p.N + n;
-    float g[2] = {0.f, 0.f}, u[2] = {0.f, 0.f}, h[2];
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (n + j < p.N) {
-                g[j] += p.part[s * mn + at + j];
-                u[j] += p.part[(S + s) * mn + at + j];
-            }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) h[j] = gated_act(p.act, g[j]) * u[j];
-    if constexpr (QOUT) {   // N % 128 == 0
-        float amax = fmaxf(fabsf(h[0]), fabsf(h[1]));
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-        const float sc = group_scale(amax, POW2);
-        *reinterpret_cast<uint16_t*>(p.yq + at) = (uint16_t)cvt_e4m3x2(h[0] / sc, h[1] / sc, 0, false);
-        if (lane == 0) p.sy[(n >> 7) * p.M + m] = sc;
-    } else {
-        const uint32_t hb = pack_bf16x2(h[0], h[1]), gb = pack_bf16x2(g[0], g[1]), ub = pack_bf16x2(u[0], u[1]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (n + j < p.N) {
-                p.y[at + j] = (uint16_t)(hb >> (16 * j));
-                if (p.g_out) {
-                    p.g_out[at + j] = (uint16_t)(gb >> (16 * j));
-                    p.u_out[at + j] = (uint16_t)(ub >> (16 * j));
-                }
-            }
     }
 }
 

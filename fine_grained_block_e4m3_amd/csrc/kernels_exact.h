@@ -131,7 +131,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
     const int wm = MODE == kMasked ? wave / WAVES_N : wave % WAVES_M;
     const int wn = MODE == kMasked ? wave % WAVES_N : wave / WAVES_M;
     const int64_t K = p.K;
-    const int KB = (int)(K / 128);
+    const int KBA = (int)(K / 128);     // K blocks of the operands
+    // this workgroup's K blocks (gated: K may be split over grid.y)
+    const int kb_lo = GATED ? (int)((int64_t)blockIdx.y * KBA / gridDim.y) : 0;
+    const int KB = GATED ? (int)((blockIdx.y + 1) * (int64_t)KBA / gridDim.y) - kb_lo : KBA;
+    const int64_t k_lo = 128 * (int64_t)kb_lo;
     const int64_t N = p.N;
     const int h = lane >> 5;            // K half of the block this lane covers
     const int r32 = lane & 31;          // row of a 32-row subtile
@@ -217,29 +221,31 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void gemm_exact_kernel(
         const float* sb = sb_;
         if constexpr (MODE != kDense) {
             wq += (int64_t)expert * N * K;
-            sb += (int64_t)expert * (N / 128) * KB;
+            sb += (int64_t)expert * (N / 128) * KBA;
         }
         const int rows_valid = (int)min((int64_t)BM, tc.row_end - row0);
         const int cols_valid = (int)min((int64_t)ON, N - n0);
 
         // buffer resources: rows past the valid range read zeros
-        const i32x4 xr = make_rsrc(xq_ + row0 * K, (uint32_t)(rows_valid * K));
+        const i32x4 xr = make_rsrc(xq_ + row0 * K + k_lo, (uint32_t)(rows_valid * K - k_lo));
         // (gated, 8 waves: this wave's weight; 4 waves: wr gate, wr2 up)
         const uint8_t* wq1 = GATED && NWAVES == 8 && wave >= 4 ? p.wq2 : wq;
-        const i32x4 wr = make_rsrc(wq1 + n0 * K, (uint32_t)(cols_valid * K));
+        const i32x4 wr = make_rsrc(wq1 + n0 * K + k_lo, (uint32_t)(cols_valid * K - k_lo));
         i32x4 wr2 = wr;
-        if constexpr (GATED && NWAVES == 4) wr2 = make_rsrc(p.wq2 + n0 * K, (uint32_t)(cols_valid * K));
+        if constexpr (GATED && NWAVES == 4) 
+            wr2 = make_rsrc(p.wq2 + n0 * K + k_lo, (uint32_t)(cols_valid * K - k_lo));
         // gated: the scale waves load the gate's and the up weight's scales in turn
         if constexpr (GATED) sb = (wave - NSA) & 1 ? p.sb2 : sb_;
         const int nb0 = (int)(n0 >> 7);
         const int nbl = (int)min((int64_t)(BN / 128 + 2), (N + 127) / 128 - nb0);
         // this wave's scale load: a base advancing adv bytes per K block, an
         // soffset of sstep bytes per K block and a byte range
-        const uint64_t sc_base = uniform_u64(sa_wave ? (uint64_t)(sa_ + row0) : (uint64_t)(sb + (int64_t)nb0 * KB));
+        const uint64_t sc_base = uniform_u64(sa_wave ? (uint64_t)(sa_ + row0 + kb_lo * p.M)
+                                                     : (uint64_t)(sb + (int64_t)nb0 * KBA + kb_lo));
         const uint32_t sc_adv = sa_wave ? (uint32_t)(4 * p.M) : 0u;
         const int sc_step = sa_wave ? 0 : 4;
-        const uint32_t sc_rec = uniform(sa_wave ? (int)(4 * rows_valid) : (int)(4 * nbl * KB));
-        const uint32_t sc_voff = sa_wave ? (uint32_t)(4 * (64 * wave + lane)) : (uint32_t)(4 * lane * KB);
+        const uint32_t sc_rec = uniform(sa_wave ? (int)(4 * rows_valid) : (int)(4 * nbl * KBA - 4 * kb_lo));
+        const uint32_t sc_voff = sa_wave ? (uint32_t)(4 * (64 * wave + lane)) : (uint32_t)(4 * lane * KBA);
         // LDS slot of each W subtile's weight-block scale (the last block for
         // subtiles past N, whose columns are never stored)
         uint32_t sb_slot[FJ];

@@ -1,8 +1,8 @@
-// kernels_skinny.h -- products of up to 16 tokens with a weight matrix for
-// gfx950: matrix-vector products with 4-bit weights and group scales, and the
-// gated feed-forward block on up to 16 tokens (4-bit or E4M3 weights).
+// kernels_skinny.h -- products of few tokens with a weight matrix for gfx950:
+// matrix-vector products with 4-bit weights and group scales, and the gated
+// feed-forward block (4-bit weights: up to 16 tokens; E4M3: up to 64).
 //
-//   y[m][n] = sum_k x[m][k] w[n][k],  m < M <= 16
+//   y[m][n] = sum_k x[m][k] w[n][k]
 //   gated:  y = act(x Wg^T) * (x Wu^T)
 // Weight formats (K % 128 == 0, codes row-major, two 4-bit codes per byte, the
 // even element low):
@@ -86,8 +86,9 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as
 // RT: 16-row weight tiles per workgroup; gated: even tiles hold gate rows, odd
 // ones the up rows of the same columns, and RT == 1 one tile of 8 gate and 8
 // up rows (more workgroups for narrow weights).  KW: waves along K.  D: K
-// blocks of a wave in registers.  GROUP: group size of 4-bit integers.
-template <int FMT, bool GATED, int RT, int KW, int D, int GROUP, bool ZEROS>
+// blocks of a wave in registers.  GROUP: group size of 4-bit integers.  MB:
+// blocks of 16 tokens (E4M3).
+template <int FMT, bool GATED, int RT, int KW, int D, int GROUP, bool ZEROS, int MB = 1>
 __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     constexpr bool kMixed = GATED && RT == 1;
     constexpr int COLS = GATED ? 8 * RT : 16 * RT;      // output columns of a workgroup
@@ -96,7 +97,8 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     constexpr bool kTranspose = FMT == kSkinnyInt4 && GROUP < 128;
     constexpr int NG = FMT == kSkinnyInt4 ? 128 / GROUP : 1;   // groups per block
     static_assert(!GATED || RT == 1 || RT % 2 == 0, "gate and up tiles in pairs");
-    __shared__ f32x4 sums[KW][RT][64];
+    static_assert(MB == 1 || FMT == kSkinnyE4m3, "token blocks");
+    __shared__ f32x4 sums[KW][RT * MB][64];
 
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
@@ -136,20 +138,25 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
         sshift[t] = (int)min(nr - from, (int64_t)3);
         brow[t] = static_cast<const float*>(p.s[ri]) + (min(nr, N - 1) >> 7) * KB;
     }
-    const int64_t m = min((int64_t)r, p.M - 1);
     // x of this lane's token: 4-bit with whole-block groups and E4M3: the 32
     // elements 32q ..; transposed: elements 32 s + 8 q of step s
-    const uint8_t* xrow = static_cast<const uint8_t*>(p.x) + m * p.K * (FMT == kSkinnyE4m3 ? 1 : 2) +
-                          (FMT == kSkinnyE4m3 ? 32 * q : kTranspose ? 16 * q : 64 * q);
-    const float* sarow = p.sa + m;
+    const uint8_t* xrow[MB];
+    const float* sarow[MB];
+#pragma unroll
+    for (int c = 0; c < MB; ++c) {
+        const int64_t m = min((int64_t)(16 * c + r), p.M - 1);
+        xrow[c] = static_cast<const uint8_t*>(p.x) + m * p.K * (FMT == kSkinnyE4m3 ? 1 : 2) +
+                  (FMT == kSkinnyE4m3 ? 32 * q : kTranspose ? 16 * q : 64 * q);
+        sarow[c] = p.sa + m;
+    }
 
     struct Block {
         i32x4 w[RT][WL];
-        i32x4 x[XL];
+        i32x4 x[MB][XL];
         uint32_t e[RT];             // MXFP4: scale dword of the operand row
         uint64_t s[RT][NG];         // int4: 4 BF16 scales of the result rows
         uint32_t z[RT][NG];         // ... and 4 zero points
-        float sab[RT];              // E4M3: sa * sb of the result rows
+        float sa[MB], sb[RT];       // E4M3: scales of the token and of the result rows
     };
     auto load = [&](Block& b, int kb) FP8K_INLINE {
 #pragma unroll
@@ -158,7 +165,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
             for (int i = 0; i < WL; ++i)
                 b.w[t][i] = *reinterpret_cast<const i32x4*>(wrow[t] + (int64_t)kb * 64 * WL + 16 * i);
             if constexpr (FMT == kSkinnyMxfp4) b.e[t] = erow[t][(int64_t)kb * N];
-            if constexpr (FMT == kSkinnyE4m3) b.sab[t] = sarow[(int64_t)kb * p.M] * brow[t][kb];
+            if constexpr (FMT == kSkinnyE4m3) b.sb[t] = brow[t][kb];
             if constexpr (FMT == kSkinnyInt4) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
@@ -170,41 +177,57 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < XL; ++i)
-            b.x[i] = *reinterpret_cast<const i32x4*>(xrow + (int64_t)kb * (FMT == kSkinnyE4m3 ? 128 : 256) +
-                                                     (kTranspose ? 64 : 16) * i);
+        for (int c = 0; c < MB; ++c) {
+            if constexpr (FMT == kSkinnyE4m3) b.sa[c] = sarow[c][(int64_t)kb * p.M];
+#pragma unroll
+            for (int i = 0; i < XL; ++i)
+                b.x[c][i] = *reinterpret_cast<const i32x4*>(xrow[c] + (int64_t)kb * (FMT == kSkinnyE4m3 ? 128 : 256) +
+                                                            (kTranspose ? 64 : 16) * i);
+        }
     };
 
-    f32x4 acc[RT];
+    f32x4 acc[RT][MB];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < MB; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     auto multiply = [&](const Block& b) FP8K_INLINE {
         if constexpr (FMT == kSkinnyE4m3) {
-            f32x4 part[RT];
+            f32x4 part[RT][MB];
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const f16x8 xv = e4m3x8_to_f16(b.x[s >> 1][2 * (s & 1)], b.x[s >> 1][2 * (s & 1) + 1]);
+                f16x8 xv[MB];
+#pragma unroll
+                for (int c = 0; c < MB; ++c)
+                    xv[c] = e4m3x8_to_f16(b.x[c][s >> 1][2 * (s & 1)], b.x[c][s >> 1][2 * (s & 1) + 1]);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
                     const f16x8 wv = e4m3x8_to_f16(b.w[t][s >> 1][2 * (s & 1)], b.w[t][s >> 1][2 * (s & 1) + 1]);
-                    part[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, xv, s ? part[t] : f32x4{}, 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < MB; ++c)
+                        part[t][c] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, xv[c], s ? part[t][c] : f32x4{}, 0, 0, 0);
                 }
             }
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(b.sab[t], part[t][v], acc[t][v]);
+                for (int c = 0; c < MB; ++c) {
+                    const float f = b.sa[c] * b.sb[t];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[t][c][v] = __builtin_fmaf(f, part[t][c][v], acc[t][c][v]);
+                }
         } else if constexpr (FMT == kSkinnyMxfp4) {
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const bf16x8 xv = __builtin_bit_cast(bf16x8, b.x[s]);
+                const bf16x8 xv = __builtin_bit_cast(bf16x8, b.x[0][s]);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
                     // the lane's 32 weights are group q: its scale byte as an FP32 exponent
                     const float sc = __uint_as_float((b.e[t] >> (8 * q) & 0xFFu) << 23);
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e2m1x8_to_bf16(b.w[t][0][s], sc), xv, acc[t],
-                                                                     0, 0, 0);
+                    acc[t][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e2m1x8_to_bf16(b.w[t][0][s], sc), xv, acc[t][0],
+                                                                        0, 0, 0);
                 }
             }
         } else {
@@ -220,7 +243,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
 #pragma unroll
                 for (int i = 0; i < 4 / NG; ++i) {
                     const int s = g * (4 / NG) + i;
-                    const bf16x8 xv = bf16x8_u4_order(b.x[s]);
+                    const bf16x8 xv = bf16x8_u4_order(b.x[0][s]);
                     sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xv, sx, 0, 0, 0);
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
@@ -239,7 +262,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
                         const uint32_t sw = (uint32_t)(v < 2 ? s4 : s4 >> 32);
                         const float sc = v & 1 ? __uint_as_float(sw & 0xFFFF0000u) : bf16_bits_to_f32(sw);
                         const float off = ZEROS ? (float)(z4 >> (8 * v) & 0xFFu) : 8.f;
-                        acc[t][v] = __builtin_fmaf(sc, __builtin_fmaf(-off, sx[0], part[t][v]), acc[t][v]);
+                        acc[t][0][v] = __builtin_fmaf(sc, __builtin_fmaf(-off, sx[0], part[t][v]), acc[t][0][v]);
                     }
                 }
             }
@@ -278,7 +301,9 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
 
     // ---- join the waves' sums, in wave order; tile t by wave t % KW ----
 #pragma unroll
-    for (int t = 0; t < RT; ++t) sums[wave][t][lane] = acc[t];
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < MB; ++c) sums[wave][t * MB + c][lane] = acc[t][c];
     __syncthreads();
     auto total = [&](int t, int l) FP8K_INLINE {
         f32x4 v = sums[0][t][l];
@@ -286,19 +311,22 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
         return v;
     };
     constexpr int OT = GATED ? (RT + 1) / 2 : RT;       // result tiles
-    for (int t = wave; t < OT; t += KW) {
+    for (int o = wave; o < OT * MB; o += KW) {
+        const int t = o / MB, c = o - t * MB;
         f32x4 v;
         if constexpr (GATED) {
             if (kMixed && q >= 2) continue;             // the up rows' lanes
-            const f32x4 g = total(kMixed ? 0 : 2 * t, lane), u = total(kMixed ? 0 : 2 * t + 1, kMixed ? lane + 32 : lane);
+            const f32x4 g = total((kMixed ? 0 : 2 * t) * MB + c, lane);
+            const f32x4 u = total((kMixed ? 0 : 2 * t + 1) * MB + c, kMixed ? lane + 32 : lane);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = gated_act(p.act, g[i]) * u[i];
         } else {
             v = total(t, lane);
         }
-        if (r >= p.M) continue;
+        const int64_t m = 16 * c + r;
+        if (m >= p.M) continue;
         const int64_t n = n0 + 16 * t + 4 * q;
-        uint16_t* out = p.y + (int64_t)r * N + n;
+        uint16_t* out = p.y + m * N + n;
         const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
         if ((N & 3) == 0 && n + 3 < N) {
             *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);

@@ -1,4 +1,4 @@
-// skinny.h -- launches of the kernels for up to 16 tokens (skinny_launch.hip),
+// skinny.h -- launches of the kernels for few tokens (skinny_launch.hip),
 // used by the entry points in ffn_api.hip.
 #pragma once
 
@@ -21,7 +21,8 @@ struct SkinnyParams {
 
 namespace fp8h {
 
-constexpr int64_t kMaxSkinnyM = 16;
+constexpr int64_t kMaxSkinnyM = 16;         // 4-bit weights
+constexpr int64_t kMaxSkinnyGatedM = 64;    // the gated block on E4M3 operands
 
 // The gated block on E4M3 operands; 4-bit matrix-vector products, plain and
 // gated; the 4-bit integer quantizer.  Arguments are already checked.

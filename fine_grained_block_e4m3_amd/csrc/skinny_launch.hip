@@ -1,5 +1,5 @@
-// skinny_launch.hip -- instances and launches of the kernels for up to 16
-// tokens (kernels_skinny.h).
+// skinny_launch.hip -- instances and launches of the kernels for few tokens
+// (kernels_skinny.h).
 #include "kernels_skinny.h"
 
 namespace {
@@ -27,10 +27,10 @@ int pick_tiles(int64_t tiles, int cus, std::initializer_list<int> allowed) {
 
 constexpr int kWaves = 8, kDepth = 2;
 
-template <int FMT, bool GATED, int RT, int GROUP, bool ZEROS>
+template <int FMT, bool GATED, int RT, int GROUP, bool ZEROS, int MB = 1>
 fp8_status launch_skinny(const fp8k::SkinnyParams& p, hipStream_t stream) {
     const int64_t cols = GATED ? 8 * RT : 16 * RT;
-    hipLaunchKernelGGL((fp8k::skinny_kernel<FMT, GATED, RT, kWaves, kDepth, GROUP, ZEROS>),
+    hipLaunchKernelGGL((fp8k::skinny_kernel<FMT, GATED, RT, kWaves, kDepth, GROUP, ZEROS, MB>),
                        dim3((unsigned)cdiv(p.N, cols)), dim3(64 * kWaves), 0, stream, p);
     return launch_status();
 }
@@ -83,8 +83,28 @@ fp8_status run_w4(const fp8k::SkinnyParams& p, int32_t group, int cus, hipStream
 
 namespace fp8h {
 
+// More than 16 tokens, in blocks of 16: each weight operand serves all blocks,
+// and with three or four blocks only two weight tiles fit the registers.  One
+// MI355X, gated E4M3: 32 x 7168 x 7168 4 tiles 27 us, 2 36; 64 x 7168 x 7168 2
+// tiles 47, 4 97; 37 x 2112 x 1536 2 tiles 6.4, 1 8.9.
+template <int MB>
+static fp8_status run_token_blocks(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
+    const int64_t tiles = cdiv(p.N * 2, 16);
+    const int rt = MB == 2 ? pick_tiles(tiles, cus, {1, 2, 4}) : pick_tiles(tiles, cus, {1, 2});
+    if (rt == 1) return launch_skinny<fp8k::kSkinnyE4m3, true, 1, 128, false, MB>(p, stream);
+    if (rt == 2) return launch_skinny<fp8k::kSkinnyE4m3, true, 2, 128, false, MB>(p, stream);
+    if constexpr (MB == 2) return launch_skinny<fp8k::kSkinnyE4m3, true, 4, 128, false, MB>(p, stream);
+    else return FP8_ERR_UNSUPPORTED;
+}
+
 fp8_status run_skinny_gated_e4m3(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
-    return run_skinny<fp8k::kSkinnyE4m3, true, 128, false>(p, cus, stream);
+    switch (cdiv(p.M, 16)) {
+        case 1: return run_skinny<fp8k::kSkinnyE4m3, true, 128, false>(p, cus, stream);
+        case 2: return run_token_blocks<2>(p, cus, stream);
+        case 3: return run_token_blocks<3>(p, cus, stream);
+        case 4: return run_token_blocks<4>(p, cus, stream);
+        default: return FP8_ERR_UNSUPPORTED;
+    }
 }
 
 fp8_status run_gemv_w4(const fp8k::SkinnyParams& p, bool gated, int32_t group, hipStream_t stream) {

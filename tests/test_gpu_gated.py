@@ -32,12 +32,11 @@ def _values(t):
     return bf16_to_f64(bf16_bits(t))
 
 
-# every M, N pair and its kernel: up to 16 tokens; decode kernels with X
-# resident (short K ranges) and in chunks (12300 columns leave one range of 25
-# blocks); tiles 64x128, 128x128, 128x256, 256x256 on 256 compute units
+# one to four blocks of 16 tokens, with one to six weight tiles per workgroup;
+# then the tiles of every size, with and without K split (256 compute units)
 SHAPES = [(1, 1, 128), (1, 96, 384), (2, 100, 640), (15, 37, 1152), (16, 2112, 256), (7, 4103, 128),
           (17, 1, 128), (33, 130, 640), (64, 500, 1664), (20, 12300, 3200), (40, 6200, 1664),
-          (65, 31, 128), (130, 333, 384), (300, 96, 640), (600, 3300, 128), (1100, 3700, 256), (2100, 3700, 128)]
+          (65, 31, 128), (130, 333, 384), (300, 96, 640), (600, 3300, 128), (1100, 3700, 256), (2100, 3700, 128), (100, 500, 1664), (500, 1000, 384), (700, 4160, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -89,19 +88,23 @@ def test_quantized_output(M, N, K, act, pow2):
     assert np.all(np.abs(got - groups) <= bound)
 
 
-def test_without_workspace_takes_the_tiles():
+def test_without_workspace_takes_unsplit_tiles():
     L = fp8.load_library()
-    M, N, K = 40, 300, 640
+    M, N, K = 100, 300, 1664
     ops, (x, wg, wu) = _case(M, N, K, 5)
     a = [dev(t) for t in ops]
-    assert L.fp8_gated_workspace_size(M, N, K, 0) > 0
-    assert L.fp8_gated_workspace_size(16, N, K, 0) == 0 and L.fp8_gated_workspace_size(65, N, K, 1) == 0
-    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
-    s = torch.cuda.current_stream().cuda_stream
-    say("gated without a workspace")
-    assert L.fp8_gated_nt(*[t.data_ptr() for t in a], out.data_ptr(), None, None, M, N, K, 0, 0, None, 0, s) == 0
+    need = L.fp8_gated_workspace_size(M, N, K, 0)
+    assert need > 0 and L.fp8_gated_workspace_size(64, N, K, 0) == 0
     (h, _, _), (eh, _, _) = ref.gated(x, wg, wu, "silu")
-    ref.assert_bf16(_values(out), h, eh, "h")
+    s = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for nbytes in (0, need - 1, need):
+        say(f"gated with {nbytes} bytes of workspace")
+        full, out = guarded((M, N))
+        assert L.fp8_gated_nt(*[t.data_ptr() for t in a], out.data_ptr(), None, None, M, N, K, 0, 0,
+                              ws.data_ptr() if nbytes else None, nbytes, s) == 0
+        ref.assert_bf16(_values(out), h, eh, "h")
+        check_guards(full, M * N)
 
 
 def test_extreme_gates():
