@@ -86,6 +86,34 @@ __global__ __launch_bounds__(256) void gated_grad_act_kernel(GatedGradParams p) 
     out[p.M * p.NP / 8] = du;
 }
 
+// PER (2 or 4) wave-wide 16-byte-per-lane loads into consecutive 1 KB pieces of
+// LDS from m0 on: piece i from buffer offset voff[i] + soff.
+template <int PER>
+__device__ __forceinline__ void dma_lds16_run(uint32_t m0, const uint32_t (&voff)[PER], i32x4 rsrc, int soff) {
+    static_assert(PER == 2 || PER == 4, "pieces");
+    int saved;
+    if constexpr (PER == 2)
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %2, %4, %5 offen lds\n\t"
+                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %3, %4, %5 offen lds\n\t"
+                     "s_mov_b32 m0, %0"
+                     : "=&s"(saved) : "s"(m0), "v"(voff[0]), "v"(voff[1]), "s"(rsrc), "s"(soff) : "scc");
+    else
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %2, %6, %7 offen lds\n\t"
+                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %3, %6, %7 offen lds\n\t"
+                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %4, %6, %7 offen lds\n\t"
+                     "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %5, %6, %7 offen lds\n\t"
+                     "s_mov_b32 m0, %0"
+                     : "=&s"(saved)
+                     : "s"(m0), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3]), "s"(rsrc), "s"(soff)
+                     : "scc");
+}
+
 // One operand of a product in LDS: a stage of 32 contraction steps of BX rows
 // of the result (or columns).  SLOW: the contraction runs over the operand's
 // memory rows.
@@ -173,11 +201,12 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
     const uint32_t lds0 = uniform((int)lds_addr(smem));
     FP8K_LDS const uint8_t* lds = (FP8K_LDS const uint8_t*)smem;
 
+    // A wave loads PER consecutive 1 KB pieces of each operand.
     uint32_t psrc[P::PER], qsrc[Q::PER];
 #pragma unroll
-    for (int i = 0; i < P::PER; ++i) psrc[i] = P::source(wave + i * NWAVES, lane, (uint32_t)(2 * t.p_ld));
+    for (int i = 0; i < P::PER; ++i) psrc[i] = P::source(wave * P::PER + i, lane, (uint32_t)(2 * t.p_ld));
 #pragma unroll
-    for (int i = 0; i < Q::PER; ++i) qsrc[i] = Q::source(wave + i * NWAVES, lane, (uint32_t)(2 * t.q_ld));
+    for (int i = 0; i < Q::PER; ++i) qsrc[i] = Q::source(wave * Q::PER + i, lane, (uint32_t)(2 * t.q_ld));
     uint32_t pf[FI], qf[FJ];
 #pragma unroll
     for (int a = 0; a < FI; ++a) pf[a] = P::fragment(wm * TM + 32 * a, lane);
@@ -188,23 +217,39 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
     const int all = per_seg * t.segs;
     const int first = (int)((int64_t)all * t.split / t.splits);
     const int nblocks = (int)((int64_t)all * (t.split + 1) / t.splits) - first;
-    // The operands' corners advance block by block; a range that has run out
-    // (past the operand, or past the last block) reads zeros.
+    // The blocks come in runs of one buffer resource per operand, along which
+    // only the scalar offset advances.  A segment's last block is a run of its
+    // own (offset 0), so that the resource's range ends exactly at the operand;
+    // past it, and past the workgroup's blocks, loads read zeros.  Runs are
+    // short enough for 32-bit offsets.
     auto range = [](int64_t elems) FP8K_INLINE {
         return (uint32_t)(elems <= 0 ? 0 : elems >= (1ll << 30) ? (1ll << 31) : 2 * elems);
     };
-    auto issue = [&](int i, int stage) FP8K_INLINE {
-        const bool live = i < nblocks;
-        const int kb = first + i;
+    const int cap = (int)((1ll << 29) / (32 * max(t.p_step, t.q_step)));
+    const uint32_t pstep = (uint32_t)(64 * t.p_step), qstep = (uint32_t)(64 * t.q_step);
+    i32x4 pr = make_rsrc(t.pb[0], 0u), qr = pr;
+    uint32_t poff = 0, qoff = 0;
+    int issued = 0, left = 0;
+    auto start_run = [&]() FP8K_INLINE {
+        const bool live = issued < nblocks;
+        const int kb = first + issued;
         const int z = t.segs > 1 && kb >= per_seg ? 1 : 0;
-        const int64_t k0 = (int64_t)(kb - z * per_seg) * 32;
-        const i32x4 pr = make_rsrc(t.pb[z] + k0 * t.p_step, live ? range(t.p_elems - k0 * t.p_step) : 0u);
-        const i32x4 qr = make_rsrc(t.qb[z] + k0 * t.q_step, live ? range(t.q_elems - k0 * t.q_step) : 0u);
-        const uint32_t dst = lds0 + (uint32_t)(stage * STAGE + wave * 1024);
-#pragma unroll
-        for (int i = 0; i < P::PER; ++i) dma_lds16_one<0>(dst + i * NWAVES * 1024, psrc[i], pr, 0);
-#pragma unroll
-        for (int i = 0; i < Q::PER; ++i) dma_lds16_one<0>(dst + P::BYTES + i * NWAVES * 1024, qsrc[i], qr, 0);
+        const int in = kb - z * per_seg;
+        const int64_t k0 = (int64_t)in * 32;
+        pr = make_rsrc(t.pb[z] + k0 * t.p_step, live ? range(t.p_elems - k0 * t.p_step) : 0u);
+        qr = make_rsrc(t.qb[z] + k0 * t.q_step, live ? range(t.q_elems - k0 * t.q_step) : 0u);
+        poff = qoff = 0;
+        left = !live ? 0x7FFFFFFF : max(1, min(min(per_seg - 1 - in, nblocks - issued), cap));
+    };
+    auto issue = [&](int stage) FP8K_INLINE {
+        if (left == 0) start_run();
+        --left;
+        ++issued;
+        const uint32_t dst = lds0 + (uint32_t)(stage * STAGE);
+        dma_lds16_run<P::PER>(dst + (uint32_t)(wave * P::PER * 1024), psrc, pr, (int)poff);
+        dma_lds16_run<Q::PER>(dst + (uint32_t)(P::BYTES + wave * Q::PER * 1024), qsrc, qr, (int)qoff);
+        poff += pstep;
+        qoff += qstep;
     };
 
     f32x16 acc[FI][FJ];
@@ -221,7 +266,7 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
     // block STAGES further then overwrite, and its own loads of the next
     // block have landed.
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) issue(s, s);
+    for (int s = 0; s < STAGES; ++s) issue(s);
     wait_vmcnt<(STAGES - 1) * NL>();
     lds_barrier();
     struct Operands {
@@ -255,7 +300,7 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
         read(o0, next, 0);
-        issue(kb + STAGES, stage);
+        issue(stage);
         multiply(o1);
         stage = next;
     }
