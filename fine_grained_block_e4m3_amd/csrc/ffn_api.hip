@@ -164,39 +164,39 @@ int64_t grad_np(int64_t N) { return cdiv(N, 64) * 64; }
 
 // Tiles and splits of the two products.
 struct GradPlan {
-    bool big;                   // 128x256 tiles, else 128x128
+    bool dx_wide, dw_wide;      // 128x256 tiles, else 128x128
     bool dw_first;
     int64_t dx_tiles, dw_tiles, dx_splits, dw_splits;
     size_t d_bytes, dx_part, dw_part;   // workspace: dg and du, then FP32 sums
     size_t bytes() const { return d_bytes + dx_part + dw_part; }
 };
 
-// Two 128x256 workgroups of four waves fit a compute unit, or three of 128x128
-// (64x128 and 64x64 per wave); a second and third workgroup multiply while one
-// waits at a barrier, fills its stages or stores.  128x256 reads a quarter
-// less from LDS per product and is faster once the work of a slot is several
-// times the longest tile; below that the finer tiles balance better (one
-// MI355X, 128x256 against 128x128: 4096x2048x7168 408 and 458 us,
-// 3000x2048x7168 371 and 369, 8192x7168x640 384 and 329, 500x2112x7168 87 and
-// 75).  One 256x256 workgroup of eight waves per unit: 437 us on the first.
+// Two workgroups of four waves with 128x256 tiles (64x128 per wave) fit a
+// compute unit, or three with 128x128 tiles: one multiplies while another
+// waits at a barrier, fills its stages or stores.  The wide tile reads a
+// quarter less per product; a product takes it where it still gives every
+// such slot a tile.  One MI355X, dX / dW columns per tile: 4096x2048x7168
+// 256/256 409 us, 128/128 491; 500x2112x7168 (112 and 952 wide tiles) 128/256
+// 87, 256/256 100, 128/128 91; 777x500x640 128/128 12.6, 256/256 17.7.  One
+// 256x256 workgroup of eight waves per compute unit: 440 us on the first.
 GradPlan grad_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int cus) {
     GradPlan pl{};
-    const int64_t dx_blocks = 2 * grad_np(N) / 32, dw_blocks = cdiv(M, 32);
-    auto tiles = [&](int bn) {
-        pl.dx_tiles = dx ? cdiv(M, 128) * cdiv(K, bn) : 0;
-        pl.dw_tiles = dw ? 2 * cdiv(N, 128) * cdiv(K, bn) : 0;
-        return pl.dx_tiles * dx_blocks + pl.dw_tiles * dw_blocks;   // 32-step blocks
-    };
-    const int64_t longest = dx && (!dw || dx_blocks > dw_blocks) ? dx_blocks : dw_blocks;
-    pl.big = tiles(256) >= 2 * cus * 3 * longest;
-    const int64_t share = tiles(pl.big ? 256 : 128) / (3 * cus);    // blocks per slot
+    const int64_t dx_blocks = 2 * grad_np(N) / 32, dw_blocks = cdiv(M, 32);     // of 32 steps
+    const int64_t dx_rows = dx ? cdiv(M, 128) : 0, dw_rows = dw ? 2 * cdiv(N, 128) : 0;
+    pl.dx_wide = dx_rows * cdiv(K, 256) >= 2 * cus;
+    pl.dw_wide = dw_rows * cdiv(K, 256) >= 2 * cus;
+    pl.dx_tiles = dx_rows * cdiv(K, pl.dx_wide ? 256 : 128);
+    pl.dw_tiles = dw_rows * cdiv(K, pl.dw_wide ? 256 : 128);
     pl.dw_first = dw_blocks > dx_blocks;
     pl.d_bytes = (size_t)(2 * M * grad_np(N)) * sizeof(uint16_t);
     // A product whose few tiles have contractions several times the share of a
     // slot would run alone at the end: split it.
+    const int64_t slots = (pl.dx_wide || pl.dw_wide ? 2 : 3) * cus;
+    const int64_t share = (pl.dx_tiles * dx_blocks * (pl.dx_wide ? 2 : 1) +
+                           pl.dw_tiles * dw_blocks * (pl.dw_wide ? 2 : 1)) / slots;
     auto splits = [&](int64_t n_tiles, int64_t blocks) {
         const int64_t s = n_tiles ? blocks / (share > 16 ? share : 16) : 1;
-        return pl.big || s < 3 ? (int64_t)1 : s > 8 ? (int64_t)8 : s;
+        return s < 3 ? (int64_t)1 : s > 8 ? (int64_t)8 : s;
     };
     pl.dx_splits = splits(pl.dx_tiles, dx_blocks);
     pl.dw_splits = splits(pl.dw_tiles, dw_blocks);
@@ -205,11 +205,11 @@ GradPlan grad_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int cus) {
     return pl;
 }
 
-template <int BN, int OCC>
+template <int BNX, int BNW, int OCC>
 fp8_status launch_grad(const fp8k::GatedGradParams& p, bool dw_first, hipStream_t stream) {
     const int64_t wgs = (int64_t)p.dx_tiles * p.dx_splits + (int64_t)p.dw_tiles * p.dw_splits;
-    hipLaunchKernelGGL((fp8k::gated_grad_gemm_kernel<128, BN, 2, 2, 3, OCC>), dim3((unsigned)wgs), dim3(256), 0, stream,
-                       p, dw_first);
+    hipLaunchKernelGGL((fp8k::gated_grad_gemm_kernel<128, BNX, BNW, 2, 2, 3, OCC>), dim3((unsigned)wgs), dim3(256), 0,
+                       stream, p, dw_first);
     return launch_status();
 }
 
@@ -239,7 +239,10 @@ fp8_status run_grad(fp8k::GatedGradParams& p, const GradPlan& pl, uint8_t* ws, h
         else hipLaunchKernelGGL(fp8k::gated_grad_act_kernel<false>, grid, block, 0, s, p);
         st = launch_status();
     }
-    if (st == FP8_OK) st = pl.big ? launch_grad<256, 2>(p, pl.dw_first, s) : launch_grad<128, 3>(p, pl.dw_first, s);
+    if (st == FP8_OK) {
+        if (pl.dx_wide) st = pl.dw_wide ? launch_grad<256, 256, 2>(p, pl.dw_first, s) : launch_grad<256, 128, 2>(p, pl.dw_first, s);
+        else st = pl.dw_wide ? launch_grad<128, 256, 2>(p, pl.dw_first, s) : launch_grad<128, 128, 3>(p, pl.dw_first, s);
+    }
     if (st == FP8_OK && pl.dx_splits > 1)
         st = launch_grad_join(p.dx_part, pl.dx_splits, p.M * p.K, p.M * p.K, p.dx, nullptr, s);
     if (st == FP8_OK && pl.dw_splits > 1)

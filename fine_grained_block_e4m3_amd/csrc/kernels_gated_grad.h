@@ -286,6 +286,13 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
             for (int b = 0; b < FJ; ++b)
                 acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.q[b], o.p[a], acc[a][b], 0, 0, 0);
     };
+    // two reads between one matrix instruction and the next
+    auto spread = [&]() FP8K_INLINE {
+        static_for<FI * FJ>([&](auto) FP8K_INLINE {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        });
+    };
     Operands o0, o1;
     read(o0, 0, 0);
     int stage = 0;
@@ -294,49 +301,76 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
         __builtin_amdgcn_sched_barrier(0);
         read(o1, stage, 1);
         multiply(o0);
+        spread();
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_vmcnt<(STAGES - 2) * NL>();
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        read(o0, next, 0);
         issue(stage);
+        read(o0, next, 0);
         multiply(o1);
+        spread();
         stage = next;
     }
     wait_vmcnt<0>();
 
     // lane l, value v of subtile (a, b): row 32a + l%32, column 32b + 8(v/4) + 4(l/32) + v%4
     const int h = lane >> 5;
+    if (t.splits > 1) {
 #pragma unroll
-    for (int a = 0; a < FI; ++a) {
-        const int m = wm * TM + 32 * a + (lane & 31);
-        if (m >= t.rows) continue;
+        for (int a = 0; a < FI; ++a) {
+            const int m = wm * TM + 32 * a + (lane & 31);
+            if (m >= t.rows) continue;
+#pragma unroll
+            for (int b = 0; b < FJ; ++b)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int n = wn * TN + 32 * b + 8 * q + 4 * h;
+                    // K % 128 == 0: whole groups of 4 columns, 16-byte aligned
+                    if (n < t.cols)
+                        *reinterpret_cast<f32x4*>(t.part + (int64_t)m * t.out_ld + n) =
+                            f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+                }
+        }
+        return;
+    }
+    // BF16 results through LDS, so that a wave stores whole rows of the tile
+    // (straight from the accumulators a store covers 16 bytes of each of 32
+    // rows).  Rows of 2 BN + 16 bytes; the stages are done with.
+    constexpr int ROW = 2 * BN + 16;
+    static_assert(BM * ROW <= STAGES * STAGE, "the tile fits the stages");
+    lds_barrier();
+#pragma unroll
+    for (int a = 0; a < FI; ++a)
 #pragma unroll
         for (int b = 0; b < FJ; ++b)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = wn * TN + 32 * b + 8 * q + 4 * h;
-                // K % 128 == 0: whole groups of 4 columns, 8-byte aligned
-                if (n >= t.cols) continue;
-                if (t.splits > 1)
-                    *reinterpret_cast<f32x4*>(t.part + (int64_t)m * t.out_ld + n) =
-                        f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
-                else
-                    *reinterpret_cast<uint2*>(t.out + (int64_t)m * t.out_ld + n) =
-                        make_uint2(pack_bf16x2(acc[a][b][4 * q], acc[a][b][4 * q + 1]),
-                                   pack_bf16x2(acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]));
-            }
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint2*>(smem + (wm * TM + 32 * a + (lane & 31)) * ROW +
+                                          2 * (wn * TN + 32 * b + 8 * q + 4 * h)) =
+                    make_uint2(pack_bf16x2(acc[a][b][4 * q], acc[a][b][4 * q + 1]),
+                               pack_bf16x2(acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]));
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    lds_barrier();
+    constexpr int LPR = BN / 8, RPW = 64 / LPR;         // lanes per row, rows per wave store
+    const int n = 8 * (lane % LPR);
+#pragma unroll
+    for (int i = 0; i < BM / (RPW * NWAVES); ++i) {
+        const int m = (i * NWAVES + wave) * RPW + lane / LPR;
+        // K % 128 == 0: whole groups of 8 columns, 16-byte aligned
+        if (m < t.rows && n < t.cols)
+            *reinterpret_cast<i32x4*>(t.out + (int64_t)m * t.out_ld + n) =
+                *reinterpret_cast<const i32x4*>(smem + m * ROW + 2 * n);
     }
 }
 
 // Workgroups: the tiles of dX, then those of dWg and dWu (dw_first: the other
 // way round, the product with the longer contraction first), each tile's
 // splits side by side.
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int OCC>
+template <int BM, int BNX, int BNW, int WAVES_M, int WAVES_N, int STAGES, int OCC>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void gated_grad_gemm_kernel(GatedGradParams p, bool dw_first) {
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * (BM + BN) * 64];
-    const int nt = (int)((p.K + BN - 1) / BN);
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * (BM + (BNX > BNW ? BNX : BNW)) * 64];
     // workgroup b of a dispatch wave lands on XCD b % 8: each XCD takes a run
     // of consecutive tiles (and shares their operands in its L2)
     auto run_of = [](int b, int count) FP8K_INLINE {
@@ -351,11 +385,12 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void gated_grad_gemm_k
     t.q_ld = t.q_step = p.K;
     t.out_ld = p.K;
     if (is_dx) {
+        const int nt = (int)((p.K + BNX - 1) / BNX);
         const int at = run_of(id, dx_wgs);
         t.splits = p.dx_splits;
         t.split = at % t.splits;
         raster(at / t.splits, (int)((p.M + BM - 1) / BM), nt, 4, mt, ntile);
-        const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)ntile * BN;
+        const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)ntile * BNX;
         for (int z = 0; z < 2; ++z) {
             t.pb[z] = p.d + (z * p.M + m0) * p.NP;
             t.qb[z] = p.w[z] + n0;
@@ -369,9 +404,10 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void gated_grad_gemm_k
         t.out = p.dx + m0 * p.K + n0;
         t.part = p.dx_part + (t.split * p.M + m0) * p.K + n0;
         t.rows = (int)min((int64_t)BM, p.M - m0);
-        t.cols = (int)min((int64_t)BN, p.K - n0);
-        grad_tile<BM, BN, WAVES_M, WAVES_N, STAGES, false>(t, smem);
+        t.cols = (int)min((int64_t)BNX, p.K - n0);
+        grad_tile<BM, BNX, WAVES_M, WAVES_N, STAGES, false>(t, smem);
     } else {
+        const int nt = (int)((p.K + BNW - 1) / BNW);
         const int rt = (int)((p.N + BM - 1) / BM);
         const int at = run_of(id, dw_wgs);
         t.splits = p.dw_splits;
@@ -379,7 +415,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void gated_grad_gemm_k
         const int tile = at / t.splits;
         const int z = tile >= rt * nt;
         raster(tile - z * rt * nt, rt, nt, 4, mt, ntile);
-        const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)ntile * BN;
+        const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)ntile * BNW;
         t.pb[0] = t.pb[1] = p.d + z * p.M * p.NP + m0;
         t.qb[0] = t.qb[1] = p.x + n0;
         t.p_elems = p.M * p.NP - m0;
@@ -390,8 +426,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void gated_grad_gemm_k
         t.out = p.dw[z] + m0 * p.K + n0;
         t.part = p.dw_part + ((2 * t.split + z) * p.N + m0) * p.K + n0;
         t.rows = (int)min((int64_t)BM, p.N - m0);
-        t.cols = (int)min((int64_t)BN, p.K - n0);
-        grad_tile<BM, BN, WAVES_M, WAVES_N, STAGES, true>(t, smem);
+        t.cols = (int)min((int64_t)BNW, p.K - n0);
+        grad_tile<BM, BNW, WAVES_M, WAVES_N, STAGES, true>(t, smem);
     }
 }
 
