@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 import torch
 
@@ -133,9 +134,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fp8_gemv_w4.argtypes = [P] * 5 + [I64, I64, I64, I32, P]
     L.fp8_gated_gemv_w4.argtypes = [P] * 8 + [I64, I64, I64, I32, I32, P]
     L.fp8_quant_int4.argtypes = [P, I64, I64, I32, P, P, P, P]
-    PTRS, I64S, I32S = ctypes.POINTER(P), ctypes.POINTER(I64), ctypes.POINTER(I32)
-    L.fp8_clip_grad_norm.argtypes = [PTRS, PTRS, I64S, I32S, I32, ctypes.c_float, P, P, ctypes.c_size_t, P]
-    L.fp8_clip_workspace_size.argtypes = [I64S, I32]
+    # (host arrays of pointers, counts and types)
+    L.fp8_clip_grad_norm.argtypes = [P, P, P, P, I32, ctypes.c_float, P, P, ctypes.c_size_t, P]
+    L.fp8_clip_workspace_size.argtypes = [P, I32]
     L.fp8_clip_workspace_size.restype = ctypes.c_size_t
     for fn in ("fp8_quant_1x128", "fp8_quant_128x128", "fp8_gemm_nt", "fp8_gemm_nt_ws", "fp8_gemm_nt_noalloc",
                "fp8_gemm_plan",
@@ -450,9 +451,10 @@ def _workspace(workspace, nbytes: int, like: torch.Tensor):
     if workspace is None:
         if not nbytes:
             return None, 0, None
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    _need(workspace, "workspace", torch.uint8, 1)
-    _same_device(like, workspace)
+        workspace = like.new_empty(nbytes, dtype=torch.uint8)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1)
+        _same_device(like, workspace)
     return _ptr(workspace), workspace.numel(), workspace
 
 
@@ -647,24 +649,23 @@ def clip_grad_norm(grads, max_norm: float, out=None, workspace=None) -> torch.Te
     T = torch.Tensor
     both = grads if outs is grads else grads + outs
     # one pass per property: the calls that matter here hold hundreds of tensors
-    dtypes, counts, devices = [t.dtype for t in both], list(map(T.numel, both)), set(map(T.get_device, both))
     try:
-        types = [CLIP_TYPES[d] for d in dtypes]
+        types = [CLIP_TYPES[t.dtype] for t in both]
     except KeyError as e:
         raise TypeError(f"clip_grad_norm: gradients must be fp32, bf16 or fp16, got {e.args[0]}") from None
+    counts, devices = list(map(T.numel, both)), set(map(T.get_device, both))
     if len(devices) != 1 or -1 in devices:
         raise ValueError("clip_grad_norm: gradients must be GPU tensors of one device (no CPU path exists)")
     if not all(map(T.is_contiguous, both)):
         raise ValueError("clip_grad_norm: gradients must be contiguous")
-    if outs is not grads and (dtypes[:n] != dtypes[n:] or counts[:n] != counts[n:]):
+    if outs is not grads and (types[:n] != types[n:] or counts[:n] != counts[n:]):
         raise ValueError("clip_grad_norm: out[i] must have the type and size of grads[i]")
-    ptrs = list(map(T.data_ptr, both))
-    P = ctypes.c_void_p
-    sizes, kinds = (ctypes.c_int64 * n)(*counts[:n]), (ctypes.c_int32 * n)(*types[:n])
-    gp = (P * n)(*ptrs[:n])
-    op = gp if outs is grads else (P * n)(*ptrs[n:])
-    norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
-    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_clip_workspace_size(sizes, n)), grads[0])
-    _check("fp8_clip_grad_norm", L.fp8_clip_grad_norm(gp, op, sizes, kinds, n, float(max_norm), _ptr(norm), ws,
+    ptrs = array("q", map(T.data_ptr, both))
+    sizes, kinds = array("q", counts), array("i", types)
+    gp, sp, kp = ptrs.buffer_info()[0], sizes.buffer_info()[0], kinds.buffer_info()[0]
+    op = gp if outs is grads else gp + n * ptrs.itemsize
+    norm = grads[0].new_empty((), dtype=torch.float32)
+    ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_clip_workspace_size(sp, n)), grads[0])
+    _check("fp8_clip_grad_norm", L.fp8_clip_grad_norm(gp, op, sp, kp, n, float(max_norm), norm.data_ptr(), ws,
                                                       ws_bytes, _stream(grads[0])))
     return norm
