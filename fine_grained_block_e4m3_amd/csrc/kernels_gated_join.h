@@ -11,7 +11,7 @@ namespace fp8k {
 // the device): joins the FP32 partial sums of the gate (part[0][s]) and up
 // (part[1][s]) projections, s in order, and forms h = act(g) * u.  A wave
 // takes 128 columns of one row (two per lane), the group of the quantized
-// form.
+// form.  A stream of the sums (300 x 2048, 8 splits: 5.4 us with its launch).
 // ---------------------------------------------------------------------------
 template <bool QOUT, bool POW2>
 __global__ __launch_bounds__(256) void gated_join_kernel(GemmParams p, int S) {
