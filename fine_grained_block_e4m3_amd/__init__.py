@@ -169,6 +169,18 @@ def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _launch_stream(t: torch.Tensor) -> int:
+    """The current stream of t's device, which has to be the current device:
+    kernels are launched there."""
+    if t.get_device() != _current_device():
+        raise ValueError(f"operands on {t.device}, but the current device is cuda:{_current_device()}: "
+                         f"call within torch.cuda.device({t.get_device()})")
+    return _stream(t)
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> None:
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
         return
@@ -458,7 +470,26 @@ def _workspace(workspace, nbytes: int, like: torch.Tensor):
     return _ptr(workspace), workspace.numel(), workspace
 
 
+_U8, _F32, _BF16 = torch.uint8, torch.float32, torch.bfloat16
+
+
 def _gated_operands(xq, sa, wgq, sbg, wuq, sbu, fn: str):
+    # A decode-sized call spends more time here than on the device: operands
+    # that fit pass one expression, and what follows finds the fault in others.
+    try:
+        M, K = xq.shape
+        N = len(wgq)
+        blocks = ((N + 127) // 128, K // 128)
+        if (xq.dtype is _U8 and wgq.dtype is _U8 and wuq.dtype is _U8
+                and sa.dtype is _F32 and sbg.dtype is _F32 and sbu.dtype is _F32
+                and wgq.shape == wuq.shape == (N, K) and sa.shape == (K // 128, M) and sbg.shape == sbu.shape == blocks
+                and xq.is_contiguous() and wgq.is_contiguous() and wuq.is_contiguous()
+                and sa.is_contiguous() and sbg.is_contiguous() and sbu.is_contiguous()
+                and (0 <= xq.get_device() == wgq.get_device() == wuq.get_device()
+                     == sa.get_device() == sbg.get_device() == sbu.get_device())):
+            return M, N, K
+    except (AttributeError, TypeError, ValueError):
+        pass
     for t, name, dtype in ((xq, "xq", torch.uint8), (sa, "sa", torch.float32), (wgq, "wgq", torch.uint8),
                            (sbg, "sbg", torch.float32), (wuq, "wuq", torch.uint8), (sbu, "sbu", torch.float32)):
         _need(t, name, dtype, 2)
@@ -488,19 +519,20 @@ def gated_nt(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = False,
     L = load_library()
     a = _act(act)
     M, N, K = _gated_operands(xq, sa, wgq, sbg, wuq, sbu, "gated_nt")
-    count = 3 if save else 1
     if out is None:
-        ys = [xq.new_empty((M, N), dtype=torch.bfloat16) for _ in range(count)]
+        ys = [xq.new_empty((M, N), dtype=_BF16)]
+        if save:
+            ys += [torch.empty_like(ys[0]), torch.empty_like(ys[0])]
     else:
         ys = list(out) if save else [out]
-        if len(ys) != count:
+        if len(ys) != (3 if save else 1):
             raise ValueError("gated_nt: out must be (h, g, u) with save")
         ys = [_out(t, f"out[{i}]", torch.bfloat16, (M, N), xq) for i, t in enumerate(ys)]
     ws, ws_bytes, keep = _workspace(workspace, _gated_workspace_size(M, N, K, 1 if save else 0), xq)
     _check("fp8_gated_nt", L.fp8_gated_nt(
-        _ptr(xq), _ptr(sa), _ptr(wgq), _ptr(sbg), _ptr(wuq), _ptr(sbu), _ptr(ys[0]),
+        xq.data_ptr(), sa.data_ptr(), wgq.data_ptr(), sbg.data_ptr(), wuq.data_ptr(), sbu.data_ptr(), ys[0].data_ptr(),
         _ptr(ys[1]) if save else None, _ptr(ys[2]) if save else None, M, N, K, a, _flags(ue8m0), ws, ws_bytes,
-        _stream(xq)))
+        _launch_stream(xq)))
     return tuple(ys) if save else ys[0]
 
 
@@ -519,7 +551,7 @@ def gated_nt_qout(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = F
     ws, ws_bytes, keep = _workspace(workspace, _gated_workspace_size(M, N, K, 2), xq)
     _check("fp8_gated_nt_qout", L.fp8_gated_nt_qout(
         _ptr(xq), _ptr(sa), _ptr(wgq), _ptr(sbg), _ptr(wuq), _ptr(sbu), _ptr(hq), _ptr(sh), M, N, K, a,
-        _flags(ue8m0), ws, ws_bytes, _stream(xq)))
+        _flags(ue8m0), ws, ws_bytes, _launch_stream(xq)))
     return hq, sh
 
 
@@ -547,22 +579,38 @@ def gated_nt_grad(dh, g, u, x, wg, wu, act: str = "silu", need_dx: bool = True, 
     ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_gated_grad_workspace_size(M, N, K)), dh)
     _check("fp8_gated_nt_grad", L.fp8_gated_nt_grad(
         _ptr(dh), _ptr(g), _ptr(u), _ptr(x), _ptr(wg), _ptr(wu), *[_ptr(t) if t is not None else None for t in ys],
-        M, N, K, a, ws, ws_bytes, _stream(dh)))
+        M, N, K, a, ws, ws_bytes, _launch_stream(dh)))
     return tuple(ys)
 
 
-def _w4(w, s, z, N: int, K: int, name: str) -> int:
-    """Checks one 4-bit weight and returns its `group` (W4_MXFP4 for packed
-    E8M0 scales)."""
+def _w4(w, s, z, N: int, K: int, name: str, x) -> int:
+    """Checks one 4-bit weight for the activations x and returns its `group`
+    (W4_MXFP4 for packed E8M0 scales)."""
+    # (one expression for weights that fit, as in _gated_operands)
+    try:
+        groups, cols = s.shape
+        if (w.dtype is _U8 and w.shape == (N, K // 2) and cols == N and w.is_contiguous() and s.is_contiguous()
+                and x.get_device() == w.get_device() == s.get_device()):
+            if s.dtype is torch.int32 and z is None and groups == K // 128:
+                return W4_MXFP4
+            if s.dtype is _BF16 and groups and K in (32 * groups, 64 * groups, 128 * groups) and (
+                    z is None or (z.dtype is _U8 and z.shape == s.shape and z.is_contiguous()
+                                  and z.get_device() == s.get_device())):
+                return K // groups
+    except (AttributeError, TypeError, ValueError):
+        pass
     _need(w, name, torch.uint8, 2)
+    _same_device(x, w)
     if w.shape != (N, K // 2):
         raise ValueError(f"{name} must have shape {(N, K // 2)}, got {tuple(w.shape)}")
     if isinstance(s, torch.Tensor) and s.dtype == torch.int32:
         _need(s, f"scales of {name}", torch.int32, 2)
+        _same_device(x, s)
         if s.shape != (K // 128, N) or z is not None:
             raise ValueError(f"MXFP4 {name}: scales must be (K/128, N), without zeros")
         return W4_MXFP4
     _need(s, f"scales of {name}", torch.bfloat16, 2)
+    _same_device(x, s)
     groups = s.shape[0]
     if s.shape[1] != N or groups == 0 or K % groups or K // groups not in (32, 64, 128):
         raise ValueError(f"scales of {name} must be (K/group, N) with a group of 32, 64 or 128")
@@ -582,12 +630,12 @@ def gemv_w4(x, w, scales, zeros=None, out=None) -> torch.Tensor:
     _need(x, "x", torch.bfloat16, 2)
     M, K = x.shape
     N = w.shape[0]
-    group = _w4(w, scales, zeros, N, K, "w")
-    _same_device(x, w, scales)
+    group = _w4(w, scales, zeros, N, K, "w", x)
     y = _out(out, "out", torch.bfloat16, (M, N), x) if out is not None \
         else x.new_empty((M, N))
-    _check("fp8_gemv_w4", L.fp8_gemv_w4(_ptr(x), _ptr(w), _ptr(scales), _ptr(zeros) if zeros is not None else None,
-                                        _ptr(y), M, N, K, group, _stream(x)))
+    _check("fp8_gemv_w4", L.fp8_gemv_w4(
+        x.data_ptr(), w.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), y.data_ptr(),
+        M, N, K, group, _launch_stream(x)))
     return y
 
 
@@ -600,15 +648,15 @@ def gated_gemv_w4(x, wg, scales_g, wu, scales_u, zeros_g=None, zeros_u=None, act
     _need(x, "x", torch.bfloat16, 2)
     M, K = x.shape
     N = wg.shape[0]
-    group = _w4(wg, scales_g, zeros_g, N, K, "wg")
-    if _w4(wu, scales_u, zeros_u, N, K, "wu") != group or (zeros_g is None) != (zeros_u is None):
+    group = _w4(wg, scales_g, zeros_g, N, K, "wg", x)
+    if _w4(wu, scales_u, zeros_u, N, K, "wu", x) != group or (zeros_g is None) != (zeros_u is None):
         raise ValueError("gated_gemv_w4: both weights must have one format")
-    _same_device(x, wg, scales_g, wu, scales_u)
     y = _out(out, "out", torch.bfloat16, (M, N), x) if out is not None \
         else x.new_empty((M, N))
     _check("fp8_gated_gemv_w4", L.fp8_gated_gemv_w4(
-        _ptr(x), _ptr(wg), _ptr(scales_g), _ptr(zeros_g) if zeros_g is not None else None, _ptr(wu), _ptr(scales_u),
-        _ptr(zeros_u) if zeros_u is not None else None, _ptr(y), M, N, K, group, a, _stream(x)))
+        x.data_ptr(), wg.data_ptr(), scales_g.data_ptr(), None if zeros_g is None else zeros_g.data_ptr(),
+        wu.data_ptr(), scales_u.data_ptr(), None if zeros_u is None else zeros_u.data_ptr(), y.data_ptr(),
+        M, N, K, group, a, _launch_stream(x)))
     return y
 
 
@@ -629,7 +677,7 @@ def quant_int4(w: torch.Tensor, group: int = 128, symmetric: bool = False, out=N
         s = _out(out[1], "out[1]", torch.bfloat16, (K // group, N), w)
         z = None if symmetric else _out(out[2], "out[2]", torch.uint8, (K // group, N), w)
     _check("fp8_quant_int4", L.fp8_quant_int4(_ptr(w), N, K, group, _ptr(q), _ptr(s),
-                                              _ptr(z) if z is not None else None, _stream(w)))
+                                              _ptr(z) if z is not None else None, _launch_stream(w)))
     return q, s, z
 
 
@@ -667,5 +715,5 @@ def clip_grad_norm(grads, max_norm: float, out=None, workspace=None) -> torch.Te
     norm = grads[0].new_empty((), dtype=torch.float32)
     ws, ws_bytes, keep = _workspace(workspace, int(L.fp8_clip_workspace_size(sp, n)), grads[0])
     _check("fp8_clip_grad_norm", L.fp8_clip_grad_norm(gp, op, sp, kp, n, float(max_norm), norm.data_ptr(), ws,
-                                                      ws_bytes, _stream(grads[0])))
+                                                      ws_bytes, _launch_stream(grads[0])))
     return norm
