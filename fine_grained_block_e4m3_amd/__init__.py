@@ -504,7 +504,7 @@ def _gated_operands(xq, sa, wgq, sbg, wuq, sbu, fn: str):
 
 
 def _gated_workspace_size(M: int, N: int, K: int, outputs: int) -> int:
-    if M <= 64 and outputs == 0:
+    if M <= 16 and outputs != 2:
         return 0            # one kernel, K split inside its workgroups
     return int(load_library().fp8_gated_workspace_size(M, N, K, outputs))
 

@@ -24,11 +24,8 @@ bool act_ok(int32_t act) { return act == FP8_ACT_SILU || act == FP8_ACT_GELU; }
 // ---------------------------------------------------------------------------
 enum GatedOutputs : int32_t { kOutH = 0, kOutSave = 1, kOutQuant = 2 };
 
-// Up to 64 tokens, and only h wanted: one kernel built around the weights'
-// stream (kernels_skinny.h), K split inside its workgroups.
-bool gated_skinny(int64_t M, int32_t outputs) { return M <= kMaxSkinnyGatedM && outputs == kOutH; }
-
-// Tiles of the rest: rows x output columns, and the time of one K block when
+// Up to 64 tokens may take a kernel built around the weights' stream
+// (kernels_skinny.h), K split inside its workgroups.  Tiles of the rest: rows x output columns, and the time of one K block when
 // every compute unit has one (one MI355X, K 7168, us).
 enum GatedTile : int { kGated256x128, kGated128x128, kGated128x64, kGated64x128, kGated64x64, kGatedTiles };
 struct GatedTileInfo {
@@ -43,12 +40,27 @@ constexpr GatedTileInfo kGatedTile[kGatedTiles] = {
 // compute units idle, all in one round), with the least estimated time: the
 // rounds' K blocks, 3 us to start and end a round, and for a split a second
 // launch (4 us) and its FP32 sums written and read at 4 TB/s.
+//
+// The kernel for few tokens is the faster one up to 16 tokens (one MI355X, it
+// against the tiles: 1 x 2048 x 7168 8.1 us, 16.6; 16 x 24576 x 7168 68, 70).
+// More tokens read x again in each of its workgroups, so that the estimates
+// decide (64 x 512 x 1536 6.9, 14.0; 64 x 2048 x 7168 19.7, 19.7; 48 x 7168 x
+// 7168 45, 31; 64 x 24576 x 7168 140, 79); a second launch counts 3 us more
+// there, and no tiles are faster than the weights arrive (5 TB/s).  Codes are
+// formed by the joining kernel then, whose launch it has to make up for.
 struct GatedPlan {
+    bool skinny;
     GatedTile tile;
     int64_t splits;
+    size_t ws_bytes;            // of FP32 sums
 };
-GatedPlan gated_plan(int64_t M, int64_t N, int64_t K, bool quant, bool may_split, int cus) {
-    GatedPlan best{kGated256x128, 1};
+GatedPlan gated_plan(int64_t M, int64_t N, int64_t K, int32_t outputs, bool may_split, int cus) {
+    GatedPlan best{false, kGated256x128, 1, 0};
+    const bool quant = outputs == kOutQuant;
+    if (M <= 16 && !quant) {
+        best.skinny = true;
+        return best;
+    }
     double least = 1e30;
     const int64_t kb = K / 128;
     for (int t = 0; t < kGatedTiles; ++t) {
@@ -61,17 +73,20 @@ GatedPlan gated_plan(int64_t M, int64_t N, int64_t K, bool quant, bool may_split
             if (s > 1) us += 4.0 + 16.0 * (double)(s * M * N) / 4e6;
             if (us < least) {
                 least = us;
-                best = {(GatedTile)t, s};
+                best.tile = (GatedTile)t;
+                best.splits = s;
             }
         }
     }
+    if (M <= kMaxSkinnyGatedM && (may_split || !quant)) {
+        const double few = skinny_gated_e4m3_us(M, N, K, cus) + (quant ? 4.0 + 16.0 * (double)(M * N) / 4e6 : 0.0);
+        if (best.splits > 1) least += 3.0;
+        const double stream = 3.0 + (double)(2 * N * K) / 5e6;
+        best.skinny = few <= (least > stream ? least : stream);
+    }
+    if (best.skinny) best.splits = 1;
+    if (best.skinny ? quant : best.splits > 1) best.ws_bytes = (size_t)(2 * best.splits * M * N) * sizeof(float);
     return best;
-}
-
-size_t gated_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t outputs, int cus) {
-    if (gated_skinny(M, outputs)) return 0;
-    const int64_t s = gated_plan(M, N, K, outputs == kOutQuant, true, cus).splits;
-    return s > 1 ? (size_t)(2 * s * M * N) * sizeof(float) : 0;
 }
 
 template <int BM, int BN, int WM, int WN, bool POW2, int STAGES, bool QOUT = false>
@@ -99,8 +114,7 @@ fp8_status launch_gated_join(const fp8k::GemmParams& p, bool quant, bool pow2, i
 }
 
 template <bool POW2>
-fp8_status run_gated_tiles(const fp8k::GemmParams& p, bool quant, bool may_split, int cus, hipStream_t stream) {
-    const GatedPlan pl = gated_plan(p.M, p.N, p.K, quant, may_split, cus);
+fp8_status run_gated_tiles(const fp8k::GemmParams& p, const GatedPlan& pl, bool quant, int cus, hipStream_t stream) {
     const int64_t s = pl.splits;
     if (s == 1 && quant) {
         switch (pl.tile) {
@@ -143,18 +157,19 @@ fp8_status run_gated(fp8k::GemmParams& p, int32_t outputs, uint32_t flags, void*
     int cus = 0;
     const fp8_status st = current_device_cus(&cus);
     if (st != FP8_OK) return st;
-    if (gated_skinny(p.M, outputs)) {
+    const bool quant = outputs == kOutQuant, pow2 = flags & FP8_FLAG_UE8M0;
+    GatedPlan pl = gated_plan(p.M, p.N, p.K, outputs, true, cus);
+    if (pl.ws_bytes > ws_bytes) pl = gated_plan(p.M, p.N, p.K, outputs, false, cus);
+    if (pl.ws_bytes) p.part = static_cast<float*>(ws);
+    if (pl.skinny) {
         fp8k::SkinnyParams q{};
         q.x = p.xq; q.sa = p.sa; q.w[0] = p.wq; q.w[1] = p.wq2; q.s[0] = p.sb; q.s[1] = p.sb2;
-        q.y = p.y; q.M = p.M; q.N = p.N; q.K = p.K; q.act = p.act;
-        return run_skinny_gated_e4m3(q, cus, stream);
+        q.y = p.y; q.g = p.g_out; q.u = p.u_out; q.part = p.part;
+        q.M = p.M; q.N = p.N; q.K = p.K; q.act = p.act;
+        const fp8_status run = run_skinny_gated_e4m3(q, cus, stream);
+        return run == FP8_OK && quant ? launch_gated_join(p, true, pow2, 1, stream) : run;
     }
-    const bool quant = outputs == kOutQuant, pow2 = flags & FP8_FLAG_UE8M0;
-    const size_t need = gated_ws_bytes(p.M, p.N, p.K, outputs, cus);
-    const bool split = need && ws_bytes >= need;
-    if (split) p.part = static_cast<float*>(ws);
-    return pow2 ? run_gated_tiles<true>(p, quant, split, cus, stream)
-                : run_gated_tiles<false>(p, quant, split, cus, stream);
+    return pow2 ? run_gated_tiles<true>(p, pl, quant, cus, stream) : run_gated_tiles<false>(p, pl, quant, cus, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -283,7 +298,7 @@ size_t fp8_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t outputs
         return 0;
     int cus = 0;
     if (current_device_cus(&cus) != FP8_OK) return 0;
-    return gated_ws_bytes(M, N, K, outputs, cus);
+    return gated_plan(M, N, K, outputs, true, cus).ws_bytes;
 }
 
 fp8_status fp8_gated_nt(const uint8_t* xq, const float* sa, const uint8_t* wgq, const float* sbg,

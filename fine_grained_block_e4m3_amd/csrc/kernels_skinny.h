@@ -37,6 +37,8 @@
 // (29 MB: 3.7 TB/s, the launch's 2.3 us included), MXFP4 1 x 24576 x 7168
 // 22 us (4.2 TB/s) and 16 x 24576 x 7168 26 us, int4 with groups of 128 23 and
 // 27-29 us, gated int4 (groups of 64, zero points) 3 x 2112 x 7168 11 us.
+// Gated E4M3 with g and u stored as well: 1 x 2048 x 7168 8.4 us; with codes
+// instead (FP32 sums, then the joining kernel) 11.2, the tiles 16.6 and 17.2.
 #pragma once
 
 #include "gated_common.h"
@@ -317,28 +319,44 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     constexpr int OT = GATED ? (RT + 1) / 2 : RT;       // result tiles
     for (int o = wave; o < OT * MB; o += KW) {
         const int t = o / MB, c = o - t * MB;
-        f32x4 v;
+        const int64_t m = 16 * c + r, n = n0 + 16 * t + 4 * q;
+        const bool whole = (N & 3) == 0 && n + 3 < N;
+        auto store = [&](uint16_t* out, f32x4 v) FP8K_INLINE {
+            const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
+            if (whole) {
+                *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+            } else {
+                if (n < N) out[0] = (uint16_t)(lo & 0xFFFF);
+                if (n + 1 < N) out[1] = (uint16_t)(lo >> 16);
+                if (n + 2 < N) out[2] = (uint16_t)(hi & 0xFFFF);
+                if (n + 3 < N) out[3] = (uint16_t)(hi >> 16);
+            }
+        };
         if constexpr (GATED) {
             if (kMixed && q >= 2) continue;             // the up rows' lanes
             const f32x4 g = total((kMixed ? 0 : 2 * t) * MB + c, lane);
             const f32x4 u = total((kMixed ? 0 : 2 * t + 1) * MB + c, kMixed ? lane + 32 : lane);
+            if (m >= p.M) continue;
+            if constexpr (FMT == kSkinnyE4m3) {
+                if (p.part) {                           // N % 128 == 0
+                    if (n < N) {
+                        *reinterpret_cast<f32x4*>(p.part + m * N + n) = g;
+                        *reinterpret_cast<f32x4*>(p.part + (p.M + m) * N + n) = u;
+                    }
+                    continue;
+                }
+                if (p.g) {
+                    store(p.g + m * N + n, g);
+                    store(p.u + m * N + n, u);
+                }
+            }
+            f32x4 v;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = gated_act(p.act, g[i]) * u[i];
+            store(p.y + m * N + n, v);
         } else {
-            v = total(t, lane);
-        }
-        const int64_t m = 16 * c + r;
-        if (m >= p.M) continue;
-        const int64_t n = n0 + 16 * t + 4 * q;
-        uint16_t* out = p.y + m * N + n;
-        const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
-        if ((N & 3) == 0 && n + 3 < N) {
-            *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
-        } else {
-            if (n < N) out[0] = (uint16_t)(lo & 0xFFFF);
-            if (n + 1 < N) out[1] = (uint16_t)(lo >> 16);
-            if (n + 2 < N) out[2] = (uint16_t)(hi & 0xFFFF);
-            if (n + 3 < N) out[3] = (uint16_t)(hi >> 16);
+            const f32x4 v = total(t, lane);
+            if (m < p.M) store(p.y + m * N + n, v);
         }
     }
 }

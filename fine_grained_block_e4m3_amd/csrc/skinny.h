@@ -13,6 +13,9 @@ struct SkinnyParams {
     const void* s[2];       // scales
     const uint8_t* z[2];    // 4-bit integers: zero points, or null (8)
     uint16_t* y;            // BF16 (M, N)
+    uint16_t* g;            // gated E4M3: also the projections, BF16 (M, N), or null
+    uint16_t* u;
+    float* part;            // ... or instead of all three their FP32 sums, (2, M, N)
     int64_t M, N, K;
     int32_t act;
 };
@@ -23,6 +26,9 @@ namespace fp8h {
 
 constexpr int64_t kMaxSkinnyM = 16;         // 4-bit weights
 constexpr int64_t kMaxSkinnyGatedM = 64;    // the gated block on E4M3 operands
+
+// Estimated time of the gated block on E4M3 operands, us.
+double skinny_gated_e4m3_us(int64_t M, int64_t N, int64_t K, int cus);
 
 // The gated block on E4M3 operands; 4-bit matrix-vector products, plain and
 // gated; the 4-bit integer quantizer.  Arguments are already checked.

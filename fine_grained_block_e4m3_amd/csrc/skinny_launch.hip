@@ -87,14 +87,28 @@ namespace fp8h {
 // and with three or four blocks only two weight tiles fit the registers.  One
 // MI355X, gated E4M3: 32 x 7168 x 7168 4 tiles 27 us, 2 36; 64 x 7168 x 7168 2
 // tiles 47, 4 97; 37 x 2112 x 1536 2 tiles 6.4, 1 8.9.
+static int pick_block_tiles(int64_t tiles, int cus, int token_blocks) {
+    return token_blocks == 2 ? pick_tiles(tiles, cus, {1, 2, 4}) : pick_tiles(tiles, cus, {1, 2});
+}
+
 template <int MB>
 static fp8_status run_token_blocks(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
-    const int64_t tiles = cdiv(p.N * 2, 16);
-    const int rt = MB == 2 ? pick_tiles(tiles, cus, {1, 2, 4}) : pick_tiles(tiles, cus, {1, 2});
+    const int rt = pick_block_tiles(cdiv(p.N * 2, 16), cus, MB);
     if (rt == 1) return launch_skinny<fp8k::kSkinnyE4m3, true, 1, 128, false, MB>(p, stream);
     if (rt == 2) return launch_skinny<fp8k::kSkinnyE4m3, true, 2, 128, false, MB>(p, stream);
     if constexpr (MB == 2) return launch_skinny<fp8k::kSkinnyE4m3, true, 4, 128, false, MB>(p, stream);
     else return FP8_ERR_UNSUPPORTED;
+}
+
+// Of a K block a workgroup reads and widens its token blocks (0.05 us each) and
+// its weight tiles (0.08 each), and multiplies them (0.01 a pair); fitted on
+// one MI355X to 1-64 x 512-24576 x 1536 and 7168, within 20% (64 x 512 x 1536
+// 6.8 us for 6.9, 64 x 7168 x 7168 52 for 50, 64 x 24576 x 7168 151 for 140).
+double skinny_gated_e4m3_us(int64_t M, int64_t N, int64_t K, int cus) {
+    const int64_t tiles = cdiv(N * 2, 16);
+    const int mb = (int)cdiv(M, 16);
+    const int rt = mb == 1 ? pick_tiles(tiles, cus, {1, 2, 4, 6}) : pick_block_tiles(tiles, cus, mb);
+    return 3.0 + (double)(K / 128 * cdiv(cdiv(tiles, rt), cus)) * (0.05 * mb + rt * (0.08 + 0.01 * mb));
 }
 
 fp8_status run_skinny_gated_e4m3(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {

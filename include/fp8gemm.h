@@ -361,10 +361,10 @@ fp8_status fp8_gemm_plan(int32_t layout, int64_t M, int64_t N, int64_t K,
  * g and u are formed with exact block partials as on fp8_gemm_nt's default
  * path; the activation and the product are FP32, and each output is rounded
  * once.  flags: FP8_FLAG_UE8M0 (the scales are powers of two).
- * workspace: where the output has too few tiles to fill the device, a
- * workspace of fp8_gated_workspace_size() bytes (0: none is used) lets K be
- * split over workgroups; without it, or with a smaller one, the call runs
- * unsplit.  outputs (of the size query): 0 h, 1 h with g and u, 2 quantized.
+ * workspace: where the output has too few tiles to fill the device, or has
+ * few tokens and is quantized, fp8_gated_workspace_size() bytes (0: none is
+ * used) hold FP32 sums for a second kernel; without them, or with fewer, one
+ * kernel does all, slower.  outputs (of the size query): 0 h, 1 h with g and u, 2 quantized.
  */
 fp8_status fp8_gated_nt(const uint8_t* xq, const float* sa, const uint8_t* wgq,
                         const float* sbg, const uint8_t* wuq, const float* sbu,

@@ -71,8 +71,12 @@ def test_saved_projections(M, N, K, act):
 @pytest.mark.parametrize("act,pow2", [("silu", True), ("gelu", False)])
 def test_quantized_output(M, N, K, act, pow2):
     say(f"gated quantized M={M} N={N} K={K} act={act} pow2={pow2}")
+    _check_quantized(M, N, K, act, pow2)
+
+
+def _check_quantized(M, N, K, act, pow2, workspace=None):
     ops, (x, wg, wu) = _case(M, N, K, 7 * M + N, pow2)
-    hq, sh = fp8.gated_nt_qout(*[dev(a) for a in ops], act=act, ue8m0=pow2)
+    hq, sh = fp8.gated_nt_qout(*[dev(a) for a in ops], act=act, ue8m0=pow2, workspace=workspace)
     (h, _, _), (eh, _, _) = ref.gated(x, wg, wu, act)
     s = host(sh).astype(np.float64)
     groups = h.reshape(M, N // 128, 128)
@@ -86,6 +90,41 @@ def test_quantized_output(M, N, K, act, pow2):
     # nearest E4M3: half a unit of 3 fraction bits, or of the subnormals
     bound = 1.01 * e + 2.0 ** -4 * (np.abs(groups) + e) * (1 + 2 ** -20) + 2.0 ** -10 * s.T[..., None] * (1 + 2 ** -20)
     assert np.all(np.abs(got - groups) <= bound)
+
+
+# Up to 64 tokens, each number of token blocks and weight tiles, and shapes that
+# the tiles take; then the same without a workspace.
+FEW = [(1, 3, 256), (16, 2000, 384), (9, 5002, 128), (20, 7001, 384), (30, 1300, 256), (48, 2100, 640), (40, 401, 1664),
+       (64, 3001, 256), (50, 260, 896), (64, 24704, 128), (17, 12300, 3200)]
+
+
+@pytest.mark.parametrize("M,N,K", FEW)
+@pytest.mark.parametrize("workspace", [True, False])
+def test_few_tokens(M, N, K, workspace):
+    say(f"gated few tokens M={M} N={N} K={K} workspace={workspace}")
+    ops, (x, wg, wu) = _case(M, N, K, M * 5 + N)
+    a = [dev(t) for t in ops]
+    ws = None if workspace else torch.empty(0, dtype=torch.uint8, device="cuda")
+    refs, errs = ref.gated(x, wg, wu, "silu")
+    full, out = guarded((M, N))
+    fp8.gated_nt(*a, out=out, workspace=ws)
+    ref.assert_bf16(_values(out), refs[0], errs[0], "h")
+    check_guards(full, M * N)
+    bufs = [guarded((M, N)) for _ in range(3)]
+    outs = fp8.gated_nt(*a, save=True, out=[b[1] for b in bufs], workspace=ws)
+    for (full, _), got, r, e, name in zip(bufs, outs, refs, errs, "hgu"):
+        ref.assert_bf16(_values(got), r, e, name)
+        check_guards(full, M * N)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 2048, 640), (5, 128, 1664), (16, 5120, 128), (17, 7168, 384), (48, 2176, 256),
+                                   (64, 3200, 256), (64, 24704, 128), (33, 384, 2560)])
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_quantized_few_tokens(M, N, K, workspace, pow2):
+    say(f"gated quantized few tokens M={M} N={N} K={K} workspace={workspace} pow2={pow2}")
+    _check_quantized(M, N, K, "gelu" if pow2 else "silu", pow2,
+                     None if workspace else torch.empty(0, dtype=torch.uint8, device="cuda"))
 
 
 def test_without_workspace_takes_unsplit_tiles():
