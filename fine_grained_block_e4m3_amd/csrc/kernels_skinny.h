@@ -59,6 +59,31 @@ __device__ __forceinline__ i32x4 transpose_quads(i32x4 v) {
     return i32x4{(int)c[0], (int)c[1], (int)d[0], (int)d[1]};
 }
 
+// Transposes 16-byte items over four registers and the four lanes of a quad:
+// afterwards v[s] of quad lane a is what v[a] of quad lane s was.
+__device__ __forceinline__ void transpose_quad_lanes(i32x4 (&v)[4], int lane) {
+    const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int p = 0; p < 4; p += 2) {        // lanes 1 apart
+            const int a = v[p][j], b = v[p + 1][j];
+            const int ax = __builtin_amdgcn_mov_dpp(a, 0xB1, 0xF, 0xF, true);
+            const int bx = __builtin_amdgcn_mov_dpp(b, 0xB1, 0xF, 0xF, true);
+            v[p][j] = odd ? bx : a;
+            v[p + 1][j] = odd ? b : ax;
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {           // lanes 2 apart
+            const int a = v[p][j], b = v[p + 2][j];
+            const int ax = __builtin_amdgcn_mov_dpp(a, 0x4E, 0xF, 0xF, true);
+            const int bx = __builtin_amdgcn_mov_dpp(b, 0x4E, 0xF, 0xF, true);
+            v[p][j] = high ? bx : a;
+            v[p + 2][j] = high ? b : ax;
+        }
+    }
+}
+
 // Eight 4-bit codes of a dword as BF16 integers, in the order 0, 2, 4, 6, 1, 3,
 // 5, 7.  A byte of value q < 16 is the E4M3 value q * 2^-9 (subnormal below 8,
 // exponent 1 above), so the hardware converter widens them at scale 2^9.
@@ -145,15 +170,32 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
         brow[t] = static_cast<const float*>(p.s[ri]) + (min(nr, N - 1) >> 7) * KB;
     }
     // x of this lane's token: 4-bit with whole-block groups and E4M3: the 32
-    // elements 32q ..; transposed: elements 32 s + 8 q of step s
-    const uint8_t* xrow[MB];
+    // elements 32q ..; transposed: elements 32 s + 8 q of step s.
+    // A load whose neighbouring lanes read different rows takes a cycle per
+    // lane, and x outweighs the weights of a workgroup with few tiles.  With
+    // more than a few tokens (4-bit formats) the four lanes of a quad read 64
+    // contiguous bytes, a token of the quad per load, and exchange them in
+    // registers.  One MI355X, K 7168, us: MXFP4 16 x 500 10.5 -> 6.4, 1 x 500
+    // 6.0 -> 6.4; int4 (128) 16 x 24576 27.9 -> 24.5, 1 x 500 6.4 -> 7.9; with
+    // groups of 64, whose x is transposed once more, 16 x 24576 43.9 -> 41.3,
+    // 1 x 24576 31.0 -> 39.6.
+    const bool quads = FMT != kSkinnyE4m3 && p.M > (kTranspose ? 8 : 4);
+    const uint8_t* xrow[MB == 1 ? XL : MB];
     const float* sarow[MB];
+    if constexpr (FMT == kSkinnyE4m3) {
 #pragma unroll
-    for (int c = 0; c < MB; ++c) {
-        const int64_t m = min((int64_t)(16 * c + r), p.M - 1);
-        xrow[c] = static_cast<const uint8_t*>(p.x) + m * p.K * (FMT == kSkinnyE4m3 ? 1 : 2) +
-                  (FMT == kSkinnyE4m3 ? 32 * q : kTranspose ? 16 * q : 64 * q);
-        sarow[c] = p.sa + m;
+        for (int c = 0; c < MB; ++c) {
+            const int64_t m = min((int64_t)(16 * c + r), p.M - 1);
+            xrow[c] = static_cast<const uint8_t*>(p.x) + m * p.K + 32 * q;
+            sarow[c] = p.sa + m;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            const int64_t m = min((int64_t)(quads ? 4 * (r >> 2) + i : r), p.M - 1);
+            xrow[i] = static_cast<const uint8_t*>(p.x) + m * p.K * 2 +
+                      (quads ? 64 * q + 16 * (r & 3) : kTranspose ? 16 * q + 64 * i : 64 * q + 16 * i);
+        }
     }
 
     struct Block {
@@ -187,8 +229,9 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
             if constexpr (FMT == kSkinnyE4m3) b.sa[c] = sarow[c][(int64_t)kb * p.M];
 #pragma unroll
             for (int i = 0; i < XL; ++i)
-                b.x[c][i] = *reinterpret_cast<const i32x4*>(xrow[c] + (int64_t)kb * (FMT == kSkinnyE4m3 ? 128 : 256) +
-                                                            (kTranspose ? 64 : 16) * i);
+                b.x[c][i] = FMT == kSkinnyE4m3
+                                ? *reinterpret_cast<const i32x4*>(xrow[c] + (int64_t)kb * 128 + 16 * i)
+                                : *reinterpret_cast<const i32x4*>(xrow[i] + (int64_t)kb * 256);
         }
     };
 
@@ -198,7 +241,18 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
 #pragma unroll
         for (int c = 0; c < MB; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto multiply = [&](const Block& b) FP8K_INLINE {
+    auto multiply = [&](Block& b) FP8K_INLINE {
+        if constexpr (FMT != kSkinnyE4m3)
+            if (quads) {
+                transpose_quad_lanes(b.x[0], lane);
+                if constexpr (kTranspose)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const i32x4 y = transpose_quads(i32x4{b.x[0][0][j], b.x[0][1][j], b.x[0][2][j], b.x[0][3][j]});
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) b.x[0][i][j] = y[i];
+                    }
+            }
         if constexpr (FMT == kSkinnyE4m3) {
             f32x4 part[RT][MB];
 #pragma unroll
