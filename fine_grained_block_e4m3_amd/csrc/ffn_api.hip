@@ -139,7 +139,6 @@ fp8_status check_gemv(int64_t M, int64_t N, int64_t K, int32_t group) {
         !(group == FP8_W4_MXFP4 || group == 32 || group == 64 || group == 128))
         return FP8_ERR_INVALID_ARG;
     if (K % 128 || K == 0 || M > kMaxSkinnyM) return FP8_ERR_SHAPE;
-    if (group != FP8_W4_MXFP4 && N && N < 4) return FP8_ERR_SHAPE;   // the kernel reads 4 scales at once
     if (K > kMaxGemmK) return FP8_ERR_UNSUPPORTED;
     return FP8_OK;
 }

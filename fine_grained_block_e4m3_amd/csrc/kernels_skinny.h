@@ -18,8 +18,10 @@
 //     instruction takes them: lane (r, q) = (l%16, l/16) of a wave reads the
 //     16 bytes q of row r's 64-byte K block (128 4-bit weights), which are
 //     the four MFMA steps' operands.  No LDS, no barrier in the K loop.
-//   * v_mfma_f32_16x16x32 with the 16 weight rows as A and the tokens as B:
-//     tokens past M repeat the last one (their loads coalesce with it) and
+//   * v_mfma_f32_16x16x32 with the 16 weight rows as A and the tokens as B
+//     (4-bit integers: the other way round, so that a lane's results have one
+//     scale; up to 4 tokens repeat in groups of 4 rows, and a lane scales one
+//     result): tokens past M repeat the last one (their loads coalesce with it) and
 //     are not stored.  A vector-FMA form would spend M operations per weight;
 //     this one spends the decoding only, whatever M.
 //   * The KW waves of a workgroup share its rows and split K; one LDS exchange
@@ -35,8 +37,11 @@
 // s * (sum x q - z * sum x) is formed in FP32 per group.  E4M3 is widened exactly to FP16.
 // Measured (one MI355X, kernel time): gated E4M3 1 x 2048 x 7168 7.8-8.2 us
 // (29 MB: 3.7 TB/s, the launch's 2.3 us included), MXFP4 1 x 24576 x 7168
-// 22 us (4.2 TB/s) and 16 x 24576 x 7168 26 us, int4 with groups of 128 23 and
-// 27-29 us, gated int4 (groups of 64, zero points) 3 x 2112 x 7168 11 us.
+// 21 us (4.4 TB/s) and 16 x 24576 x 7168 23 us, int4 with groups of 128 23 and
+// 25 us, with groups of 32 and zero points 31 and 40, gated int4 (groups of 64,
+// zero points) 3 x 2112 x 7168 9.5 us.  With the weights as A for 4-bit
+// integers too, four scales and zero points per lane and group: 24 and 29 (zero
+// points), 45 and 51, 11.4.
 // Gated E4M3 with g and u stored as well: 1 x 2048 x 7168 8.4 us; with codes
 // instead (FP32 sums, then the joining kernel) 11.2, the tiles 16.6 and 17.2.
 #pragma once
@@ -142,18 +147,13 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     const int G = gridDim.x, per = G / 8, rest = G % 8, xcd = blockIdx.x % 8;
     const int64_t n0 = (int64_t)(xcd * per + min(xcd, rest) + (int)(blockIdx.x / 8)) * COLS;
 
-    const bool edge = n0 + COLS > N;
-
-    // operand row of this lane in each tile, and the first of the 4 result
-    // rows it holds (rows past N repeat the last one; they are not stored)
+    // operand row of this lane in each tile (rows past N repeat the last one;
+    // they are not stored)
     const uint8_t* wrow[RT];
     const uint32_t* erow[RT];       // MXFP4: this lane's scale dwords
-    // 4-bit integers: the 4 scales and zero points of the lane's result rows
-    // (N >= 4; rows that end past N are read up to N and shifted down)
-    const uint16_t* srow[RT];
-    const uint8_t* zrow[RT];
-    int sshift[RT];
-    const float* brow[RT];          // E4M3: the block scales of the result rows
+    const uint16_t* srow[RT];       // 4-bit integers: scales and zero points
+    const uint8_t* zrow[RT];        // of group q % NG of a block
+    const float* brow[RT];          // E4M3: the block scales of the lane's 4 result rows
     const int64_t row_bytes = FMT == kSkinnyE4m3 ? p.K : p.K / 2;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -163,10 +163,8 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
         erow[t] = reinterpret_cast<const uint32_t*>(p.s[wi]) + n;
         const int ri = kMixed ? q >> 1 : GATED ? t & 1 : 0;
         const int64_t nr = n0 + (kMixed ? 4 * (q & 1) : 16 * (GATED ? t >> 1 : t) + 4 * q);
-        const int64_t from = min(nr, N - 4);
-        srow[t] = static_cast<const uint16_t*>(p.s[ri]) + from;
-        zrow[t] = ZEROS ? p.z[ri] + from : nullptr;
-        sshift[t] = (int)min(nr - from, (int64_t)3);
+        srow[t] = static_cast<const uint16_t*>(p.s[wi]) + (q % NG) * N + n;
+        zrow[t] = ZEROS ? p.z[wi] + (q % NG) * N + n : nullptr;
         brow[t] = static_cast<const float*>(p.s[ri]) + (min(nr, N - 1) >> 7) * KB;
     }
     // x of this lane's token: 4-bit with whole-block groups and E4M3: the 32
@@ -177,8 +175,9 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     // contiguous bytes, a token of the quad per load, and exchange them in
     // registers.  One MI355X, K 7168, us: MXFP4 16 x 500 10.5 -> 6.4, 1 x 500
     // 6.0 -> 6.4; int4 (128) 16 x 24576 27.9 -> 24.5, 1 x 500 6.4 -> 7.9; with
-    // groups of 64, whose x is transposed once more, 16 x 24576 43.9 -> 41.3,
-    // 1 x 24576 31.0 -> 39.6.
+    // groups of 64, whose x is transposed once more, 16 x 500 11.6 -> 9.3, 1 x
+    // 500 7.3 -> 9.6.
+    const bool four = FMT == kSkinnyInt4 && p.M <= 4;   // token m in operand rows 4m .. 4m + 3
     const bool quads = FMT != kSkinnyE4m3 && p.M > (kTranspose ? 8 : 4);
     const uint8_t* xrow[MB == 1 ? XL : MB];
     const float* sarow[MB];
@@ -192,7 +191,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     } else {
 #pragma unroll
         for (int i = 0; i < XL; ++i) {
-            const int64_t m = min((int64_t)(quads ? 4 * (r >> 2) + i : r), p.M - 1);
+            const int64_t m = min((int64_t)(quads ? 4 * (r >> 2) + i : four ? r >> 2 : r), p.M - 1);
             xrow[i] = static_cast<const uint8_t*>(p.x) + m * p.K * 2 +
                       (quads ? 64 * q + 16 * (r & 3) : kTranspose ? 16 * q + 64 * i : 64 * q + 16 * i);
         }
@@ -202,8 +201,8 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
         i32x4 w[RT][WL];
         i32x4 x[MB][XL];
         uint32_t e[RT];             // MXFP4: scale dword of the operand row
-        uint64_t s[RT][NG];         // int4: 4 BF16 scales of the result rows
-        uint32_t z[RT][NG];         // ... and 4 zero points
+        uint16_t s[RT];             // int4: BF16 scale and zero point of one group
+        uint8_t z[RT];
         float sa[MB], sb[RT];       // E4M3: scales of the token and of the result rows
     };
     auto load = [&](Block& b, int kb) FP8K_INLINE {
@@ -215,13 +214,9 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
             if constexpr (FMT == kSkinnyMxfp4) b.e[t] = erow[t][(int64_t)kb * N];
             if constexpr (FMT == kSkinnyE4m3) b.sb[t] = brow[t][kb];
             if constexpr (FMT == kSkinnyInt4) {
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    // 8 and 4 bytes, aligned to their elements
-                    const int64_t at = ((int64_t)kb * NG + g) * N;
-                    __builtin_memcpy(&b.s[t][g], srow[t] + at, 8);
-                    if constexpr (ZEROS) __builtin_memcpy(&b.z[t][g], zrow[t] + at, 4);
-                }
+                const int64_t at = (int64_t)kb * NG * N;
+                b.s[t] = srow[t][at];
+                if constexpr (ZEROS) b.z[t] = zrow[t][at];
             }
         }
 #pragma unroll
@@ -295,6 +290,22 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
             i32x4 wt[RT];
 #pragma unroll
             for (int t = 0; t < RT; ++t) wt[t] = kTranspose ? transpose_quads(b.w[t][0]) : b.w[t][0];
+            // the block's groups' scales (high half) and zero points, from the
+            // lanes that loaded them to all
+            uint32_t sz[RT][4];
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                sz[t][0] = (uint32_t)b.s[t] << 16 | (ZEROS ? b.z[t] : 8u);
+                if constexpr (NG == 4) {
+                    const auto h = __builtin_amdgcn_permlane32_swap(sz[t][0], sz[t][0], false, false);
+                    const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+                    const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+                    sz[t][0] = lo[0]; sz[t][1] = lo[1]; sz[t][2] = hi[0]; sz[t][3] = hi[1];
+                } else if constexpr (NG == 2) {
+                    const auto h = __builtin_amdgcn_permlane16_swap(sz[t][0], sz[t][0], false, false);
+                    sz[t][0] = h[0]; sz[t][1] = h[1];
+                }
+            }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 f32x4 part[RT], sx{};
@@ -304,26 +315,20 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
                 for (int i = 0; i < 4 / NG; ++i) {
                     const int s = g * (4 / NG) + i;
                     const bf16x8 xv = bf16x8_u4_order(b.x[0][s]);
-                    sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xv, sx, 0, 0, 0);
+                    sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, sx, 0, 0, 0);
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
-                        part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u4x8_to_bf16(wt[t][s]), xv, part[t], 0, 0, 0);
+                        part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, u4x8_to_bf16(wt[t][s]), part[t], 0, 0, 0);
                 }
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    uint64_t s4 = b.s[t][g];
-                    uint32_t z4 = ZEROS ? b.z[t][g] : 0u;
-                    if (edge) {
-                        s4 >>= 16 * sshift[t];
-                        z4 >>= 8 * sshift[t];
-                    }
+                    const float sc = __uint_as_float(sz[t][g] & 0xFFFF0000u);
+                    const float off = ZEROS ? (float)(sz[t][g] & 0xFFu) : 8.f;
+                    acc[t][0][0] = __builtin_fmaf(sc, __builtin_fmaf(-off, sx[0], part[t][0]), acc[t][0][0]);
+                    if (!four)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const uint32_t sw = (uint32_t)(v < 2 ? s4 : s4 >> 32);
-                        const float sc = v & 1 ? __uint_as_float(sw & 0xFFFF0000u) : bf16_bits_to_f32(sw);
-                        const float off = ZEROS ? (float)(z4 >> (8 * v) & 0xFFu) : 8.f;
-                        acc[t][0][v] = __builtin_fmaf(sc, __builtin_fmaf(-off, sx[0], part[t][v]), acc[t][0][v]);
-                    }
+                        for (int v = 1; v < 4; ++v)
+                            acc[t][0][v] = __builtin_fmaf(sc, __builtin_fmaf(-off, sx[v], part[t][v]), acc[t][0][v]);
                 }
             }
         }
@@ -366,8 +371,16 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
         for (int c = 0; c < MB; ++c) sums[wave][t * MB + c][lane] = acc[t][c];
     __syncthreads();
     auto total = [&](int t, int l) FP8K_INLINE {
-        f32x4 v = sums[0][t][l];
-        for (int w = 1; w < KW; ++w) v += sums[w][t][l];
+        f32x4 v{};
+        if constexpr (FMT == kSkinnyInt4) {
+            // weights are the columns there: four lanes' sums of one token
+            const int m = l & 15, from = (four ? 16 * (m & 3) : 16 * (m >> 2)) + 4 * (l >> 4), e = four ? 0 : m & 3;
+            for (int w = 0; w < KW; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += sums[w][t][from + i][e];
+        } else {
+            for (int w = 0; w < KW; ++w) v += sums[w][t][l];
+        }
         return v;
     };
     constexpr int OT = GATED ? (RT + 1) / 2 : RT;       // result tiles

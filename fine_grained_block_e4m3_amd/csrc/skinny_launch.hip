@@ -9,7 +9,7 @@ using namespace fp8h;
 // 16-row weight tiles per workgroup: the number that leaves the fullest compute
 // unit the fewest tiles, and of those the largest, whose tiles share the x
 // operands.  One MI355X, int4 weights with groups of 128, 16 x 24576 x 7168
-// (1536 tiles): 6 per workgroup 27-29 us, 3 34, 2 38, 1 56; gated MXFP4
+// (1536 tiles): 6 per workgroup 25 us, 2 28; groups of 64 30 and 37; gated MXFP4
 // 1 x 2048 x 7168 (256 tiles): 1 per workgroup 6.4 us, 2 7.7; 3 x 2112 x 7168
 // (264): 1 10.9, 2 8.5.
 int pick_tiles(int64_t tiles, int cus, std::initializer_list<int> allowed) {
@@ -38,27 +38,19 @@ fp8_status launch_skinny(const fp8k::SkinnyParams& p, hipStream_t stream) {
 template <int FMT, bool GATED, int GROUP, bool ZEROS>
 fp8_status run_skinny(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
     const int64_t tiles = cdiv(p.N * (GATED ? 2 : 1), 16);
-    if constexpr (FMT == fp8k::kSkinnyInt4 && GROUP < 128) {
-        // scales and zero points of several groups per block: more tiles than
-        // two do not fit the registers
-        return pick_tiles(tiles, cus, {1, 2}) == 1 ? launch_skinny<FMT, GATED, 1, GROUP, ZEROS>(p, stream)
-                                                   : launch_skinny<FMT, GATED, 2, GROUP, ZEROS>(p, stream);
-    } else {
-        int rt;
-        if constexpr (GATED) rt = pick_tiles(tiles, cus, {1, 2, 4, 6});
-        else if constexpr (ZEROS) rt = pick_tiles(tiles, cus, {1, 2, 3, 4});   // 6 spill
-        else rt = pick_tiles(tiles, cus, {1, 2, 3, 4, 6});
-        switch (rt) {
-            case 1: return launch_skinny<FMT, GATED, 1, GROUP, ZEROS>(p, stream);
-            case 2: return launch_skinny<FMT, GATED, 2, GROUP, ZEROS>(p, stream);
-            case 3:
-                if constexpr (!GATED) return launch_skinny<FMT, GATED, 3, GROUP, ZEROS>(p, stream);
-                else return FP8_ERR_UNSUPPORTED;
-            case 4: return launch_skinny<FMT, GATED, 4, GROUP, ZEROS>(p, stream);
-            default:
-                if constexpr (GATED || !ZEROS) return launch_skinny<FMT, GATED, 6, GROUP, ZEROS>(p, stream);
-                else return FP8_ERR_UNSUPPORTED;
-        }
+    constexpr bool kSix = !(FMT == fp8k::kSkinnyInt4 && GROUP == 32 && ZEROS);  // 6 spill registers there
+    const int rt = GATED ? (kSix ? pick_tiles(tiles, cus, {1, 2, 4, 6}) : pick_tiles(tiles, cus, {1, 2, 4}))
+                         : (kSix ? pick_tiles(tiles, cus, {1, 2, 3, 4, 6}) : pick_tiles(tiles, cus, {1, 2, 3, 4}));
+    switch (rt) {
+        case 1: return launch_skinny<FMT, GATED, 1, GROUP, ZEROS>(p, stream);
+        case 2: return launch_skinny<FMT, GATED, 2, GROUP, ZEROS>(p, stream);
+        case 3:
+            if constexpr (!GATED) return launch_skinny<FMT, GATED, 3, GROUP, ZEROS>(p, stream);
+            else return FP8_ERR_UNSUPPORTED;
+        case 4: return launch_skinny<FMT, GATED, 4, GROUP, ZEROS>(p, stream);
+        default:
+            if constexpr (kSix) return launch_skinny<FMT, GATED, 6, GROUP, ZEROS>(p, stream);
+            else return FP8_ERR_UNSUPPORTED;
     }
 }
 

@@ -59,6 +59,13 @@ def test_gemv_matches_the_64_bit_form(M, N, K, fmt, group, zeros):
     check_guards(full, M * N)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1, 128), (4, 2, 384), (6, 3, 256), (16, 1, 640), (9, 7, 128)])
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+def test_very_narrow_weights(M, N, K, fmt, group, zeros):
+    test_gemv_matches_the_64_bit_form(M, N, K, fmt, group, zeros)
+    test_gated_gemv_matches_the_64_bit_form(M, N, K, fmt, group, zeros)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 4, 128), (3, 9, 384), (16, 100, 1152), (2, 2112, 256), (7, 3000, 128),
                                    (16, 7168, 128), (1, 12285, 128)])
 @pytest.mark.parametrize("fmt,group,zeros", FORMATS)
@@ -145,9 +152,6 @@ def test_refusals():
         fp8.quant_int4(torch.zeros((4, 128), device="cuda"), group=16)
     with pytest.raises(fp8.Fp8GemmError) as e:
         fp8.gemv_w4(torch.ones((17, K), dtype=torch.bfloat16, device="cuda"), q, s, zeros=z)
-    assert e.value.status == 2
-    with pytest.raises(fp8.Fp8GemmError) as e:
-        fp8.gemv_w4(x, q[:3], s[:, :3].contiguous())
     assert e.value.status == 2
     assert fp8.gemv_w4(x[:0], q, s, zeros=z).shape == (0, N)
 
