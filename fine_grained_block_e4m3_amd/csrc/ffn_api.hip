@@ -42,12 +42,13 @@ constexpr GatedTileInfo kGatedTile[kGatedTiles] = {
 // launch (4 us) and its FP32 sums written and read at 4 TB/s.
 //
 // The kernel for few tokens is the faster one up to 16 tokens (one MI355X, it
-// against the tiles: 1 x 2048 x 7168 8.1 us, 16.6; 16 x 24576 x 7168 68, 70).
-// More tokens read x again in each of its workgroups, so that the estimates
-// decide (64 x 512 x 1536 6.9, 14.0; 64 x 2048 x 7168 19.7, 19.7; 48 x 7168 x
-// 7168 45, 31; 64 x 24576 x 7168 140, 79); a second launch counts 3 us more
-// there, and no tiles are faster than the weights arrive (5 TB/s).  Codes are
-// formed by the joining kernel then, whose launch it has to make up for.
+// against the tiles: 1 x 2048 x 7168 7.5 us, 16.6; 16 x 24576 x 7168 67, 70).
+// More tokens widen x again in each of its workgroups, so that the estimates
+// decide (64 x 512 x 1536 6.0, 14.0; 64 x 2048 x 7168 14.2, 19.7; 32 x 7168 x
+// 7168 23.6, 28.9; 48 x 7168 x 7168, before its loads were paired, 45, 31); a
+// second launch counts 3 us more there, and no tiles are faster than the
+// weights arrive (5 TB/s).  Codes are formed by the joining kernel then, whose
+// launch it has to make up for.
 struct GatedPlan {
     bool skinny;
     GatedTile tile;
@@ -61,9 +62,17 @@ GatedPlan gated_plan(int64_t M, int64_t N, int64_t K, int32_t outputs, bool may_
         best.skinny = true;
         return best;
     }
-    double least = 1e30;
     const int64_t kb = K / 128;
-    for (int t = 0; t < kGatedTiles; ++t) {
+    double few = 1e30;
+    if (M <= kMaxSkinnyGatedM && (may_split || !quant)) {
+        few = skinny_gated_e4m3_us(M, N, K, cus) + (quant ? 4.0 + 16.0 * (double)(M * N) / 4e6 : 0.0);
+        // no tiles can take less: one round of the smallest, split or not
+        const double unsplit = 3.0 + kGatedTile[kGated64x64].us * (double)kb;
+        const double split = 3.0 + kGatedTile[kGated64x64].us * (double)kb / 8 + 7.0;
+        best.skinny = few <= (unsplit < split ? unsplit : split);
+    }
+    double least = 1e30;
+    for (int t = 0; t < kGatedTiles && !best.skinny; ++t) {
         const GatedTileInfo& i = kGatedTile[t];
         const int64_t tiles = cdiv(M, i.bm) * cdiv(N, i.cols);
         for (int64_t s = 1; s <= 8; ++s) {
@@ -78,12 +87,9 @@ GatedPlan gated_plan(int64_t M, int64_t N, int64_t K, int32_t outputs, bool may_
             }
         }
     }
-    if (M <= kMaxSkinnyGatedM && (may_split || !quant)) {
-        const double few = skinny_gated_e4m3_us(M, N, K, cus) + (quant ? 4.0 + 16.0 * (double)(M * N) / 4e6 : 0.0);
-        if (best.splits > 1) least += 3.0;
-        const double stream = 3.0 + (double)(2 * N * K) / 5e6;
-        best.skinny = few <= (least > stream ? least : stream);
-    }
+    if (best.splits > 1) least += 3.0;
+    const double stream = 3.0 + (double)(2 * N * K) / 5e6;
+    best.skinny = few <= (least > stream ? least : stream);
     if (best.skinny) best.splits = 1;
     if (best.skinny ? quant : best.splits > 1) best.ws_bytes = (size_t)(2 * best.splits * M * N) * sizeof(float);
     return best;

@@ -35,15 +35,15 @@
 // sums).  4-bit integers enter as the BF16 integers q; the group's sum of x
 // comes from the same instruction with a matrix of ones, and
 // s * (sum x q - z * sum x) is formed in FP32 per group.  E4M3 is widened exactly to FP16.
-// Measured (one MI355X, kernel time): gated E4M3 1 x 2048 x 7168 7.8-8.2 us
-// (29 MB: 3.7 TB/s, the launch's 2.3 us included), MXFP4 1 x 24576 x 7168
+// Measured (one MI355X, kernel time): gated E4M3 1 x 2048 x 7168 7.4 us
+// (29 MB: 4.0 TB/s, the launch's 2.3 us included), MXFP4 1 x 24576 x 7168
 // 21 us (4.4 TB/s) and 16 x 24576 x 7168 23 us, int4 with groups of 128 23 and
 // 25 us, with groups of 32 and zero points 31 and 40, gated int4 (groups of 64,
 // zero points) 3 x 2112 x 7168 9.5 us.  With the weights as A for 4-bit
 // integers too, four scales and zero points per lane and group: 24 and 29 (zero
 // points), 45 and 51, 11.4.
-// Gated E4M3 with g and u stored as well: 1 x 2048 x 7168 8.4 us; with codes
-// instead (FP32 sums, then the joining kernel) 11.2, the tiles 16.6 and 17.2.
+// Gated E4M3 with g and u stored as well: 1 x 2048 x 7168 7.6 us; with codes
+// instead (FP32 sums, then the joining kernel) 11, the tiles 16.6 and 17.2.
 #pragma once
 
 #include "gated_common.h"
@@ -62,6 +62,20 @@ __device__ __forceinline__ i32x4 transpose_quads(i32x4 v) {
     const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
     const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
     return i32x4{(int)c[0], (int)c[1], (int)d[0], (int)d[1]};
+}
+
+// Swaps the second item of even lanes with the first of the odd lane next to
+// them.
+__device__ __forceinline__ void swap_pair_lanes(i32x4& v0, i32x4& v1, int lane) {
+    const bool odd = lane & 1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int a = v0[j], b = v1[j];
+        const int ax = __builtin_amdgcn_mov_dpp(a, 0xB1, 0xF, 0xF, true);
+        const int bx = __builtin_amdgcn_mov_dpp(b, 0xB1, 0xF, 0xF, true);
+        v0[j] = odd ? bx : a;
+        v1[j] = odd ? b : ax;
+    }
 }
 
 // Transposes 16-byte items over four registers and the four lanes of a quad:
@@ -149,7 +163,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
 
     // operand row of this lane in each tile (rows past N repeat the last one;
     // they are not stored)
-    const uint8_t* wrow[RT];
+    const uint8_t* wrow[RT][WL];
     const uint32_t* erow[RT];       // MXFP4: this lane's scale dwords
     const uint16_t* srow[RT];       // 4-bit integers: scales and zero points
     const uint8_t* zrow[RT];        // of group q % NG of a block
@@ -158,8 +172,14 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int wi = kMixed ? r >> 3 : GATED ? t & 1 : 0;
-        const int64_t n = min(n0 + (kMixed ? r & 7 : 16 * (GATED ? t >> 1 : t) + r), N - 1);
-        wrow[t] = p.w[wi] + n * row_bytes + 16 * WL * q;
+        auto row = [&](int i) FP8K_INLINE {
+            return min(n0 + (kMixed ? i & 7 : 16 * (GATED ? t >> 1 : t) + i), N - 1);
+        };
+        const int64_t n = row(r);
+        if constexpr (WL == 1) wrow[t][0] = p.w[wi] + n * row_bytes + 16 * q;
+        else
+#pragma unroll
+            for (int i = 0; i < WL; ++i) wrow[t][i] = p.w[wi] + row((r & 14) + i) * row_bytes + 32 * q + 16 * (r & 1);
         erow[t] = reinterpret_cast<const uint32_t*>(p.s[wi]) + n;
         const int ri = kMixed ? q >> 1 : GATED ? t & 1 : 0;
         const int64_t nr = n0 + (kMixed ? 4 * (q & 1) : 16 * (GATED ? t >> 1 : t) + 4 * q);
@@ -173,20 +193,25 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     // lane, and x outweighs the weights of a workgroup with few tiles.  With
     // more than a few tokens (4-bit formats) the four lanes of a quad read 64
     // contiguous bytes, a token of the quad per load, and exchange them in
-    // registers.  One MI355X, K 7168, us: MXFP4 16 x 500 10.5 -> 6.4, 1 x 500
+    // registers; the two lanes of a pair do so for E4M3 (and always for its
+    // weights).  One MI355X, K 7168, us: MXFP4 16 x 500 10.5 -> 6.4, 1 x 500
     // 6.0 -> 6.4; int4 (128) 16 x 24576 27.9 -> 24.5, 1 x 500 6.4 -> 7.9; with
     // groups of 64, whose x is transposed once more, 16 x 500 11.6 -> 9.3, 1 x
-    // 500 7.3 -> 9.6.
+    // 500 7.3 -> 9.6.  Gated E4M3 16 x 2048 10.2 -> 9.0, 48 x 2048 17.2 -> 13.3,
+    // with the weights 1 x 2048 8.0 -> 7.5, 16 x 2048 -> 7.8, 48 x 2048 -> 12.0.
     const bool four = FMT == kSkinnyInt4 && p.M <= 4;   // token m in operand rows 4m .. 4m + 3
-    const bool quads = FMT != kSkinnyE4m3 && p.M > (kTranspose ? 8 : 4);
-    const uint8_t* xrow[MB == 1 ? XL : MB];
+    const bool quads = MB > 1 || p.M > (kTranspose ? 8 : 4);
+    const uint8_t* xrow[MB * XL];
     const float* sarow[MB];
     if constexpr (FMT == kSkinnyE4m3) {
 #pragma unroll
         for (int c = 0; c < MB; ++c) {
-            const int64_t m = min((int64_t)(16 * c + r), p.M - 1);
-            xrow[c] = static_cast<const uint8_t*>(p.x) + m * p.K + 32 * q;
-            sarow[c] = p.sa + m;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t m = min((int64_t)(16 * c + (quads ? (r & 14) + i : r)), p.M - 1);
+                xrow[2 * c + i] = static_cast<const uint8_t*>(p.x) + m * p.K + 32 * q + 16 * (quads ? r & 1 : i);
+            }
+            sarow[c] = p.sa + min((int64_t)(16 * c + r), p.M - 1);
         }
     } else {
 #pragma unroll
@@ -210,7 +235,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
         for (int t = 0; t < RT; ++t) {
 #pragma unroll
             for (int i = 0; i < WL; ++i)
-                b.w[t][i] = *reinterpret_cast<const i32x4*>(wrow[t] + (int64_t)kb * 64 * WL + 16 * i);
+                b.w[t][i] = *reinterpret_cast<const i32x4*>(wrow[t][i] + (int64_t)kb * 64 * WL);
             if constexpr (FMT == kSkinnyMxfp4) b.e[t] = erow[t][(int64_t)kb * N];
             if constexpr (FMT == kSkinnyE4m3) b.sb[t] = brow[t][kb];
             if constexpr (FMT == kSkinnyInt4) {
@@ -224,9 +249,8 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
             if constexpr (FMT == kSkinnyE4m3) b.sa[c] = sarow[c][(int64_t)kb * p.M];
 #pragma unroll
             for (int i = 0; i < XL; ++i)
-                b.x[c][i] = FMT == kSkinnyE4m3
-                                ? *reinterpret_cast<const i32x4*>(xrow[c] + (int64_t)kb * 128 + 16 * i)
-                                : *reinterpret_cast<const i32x4*>(xrow[i] + (int64_t)kb * 256);
+                b.x[c][i] = *reinterpret_cast<const i32x4*>(xrow[XL * c + i] +
+                                                            (int64_t)kb * (FMT == kSkinnyE4m3 ? 128 : 256));
         }
     };
 
@@ -237,7 +261,13 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
         for (int c = 0; c < MB; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     auto multiply = [&](Block& b) FP8K_INLINE {
-        if constexpr (FMT != kSkinnyE4m3)
+        if constexpr (FMT == kSkinnyE4m3) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) swap_pair_lanes(b.w[t][0], b.w[t][1], lane);
+            if (quads)
+#pragma unroll
+                for (int c = 0; c < MB; ++c) swap_pair_lanes(b.x[c][0], b.x[c][1], lane);
+        } else
             if (quads) {
                 transpose_quad_lanes(b.x[0], lane);
                 if constexpr (kTranspose)

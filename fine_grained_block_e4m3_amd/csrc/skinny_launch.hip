@@ -38,7 +38,8 @@ fp8_status launch_skinny(const fp8k::SkinnyParams& p, hipStream_t stream) {
 template <int FMT, bool GATED, int GROUP, bool ZEROS>
 fp8_status run_skinny(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
     const int64_t tiles = cdiv(p.N * (GATED ? 2 : 1), 16);
-    constexpr bool kSix = !(FMT == fp8k::kSkinnyInt4 && GROUP == 32 && ZEROS);  // 6 spill registers there
+    // six tiles spill registers where a tile takes most
+    constexpr bool kSix = FMT != fp8k::kSkinnyE4m3 && !(FMT == fp8k::kSkinnyInt4 && GROUP == 32 && ZEROS);
     const int rt = GATED ? (kSix ? pick_tiles(tiles, cus, {1, 2, 4, 6}) : pick_tiles(tiles, cus, {1, 2, 4}))
                          : (kSix ? pick_tiles(tiles, cus, {1, 2, 3, 4, 6}) : pick_tiles(tiles, cus, {1, 2, 3, 4}));
     switch (rt) {
@@ -77,8 +78,9 @@ namespace fp8h {
 
 // More than 16 tokens, in blocks of 16: each weight operand serves all blocks,
 // and with three or four blocks only two weight tiles fit the registers.  One
-// MI355X, gated E4M3: 32 x 7168 x 7168 4 tiles 27 us, 2 36; 64 x 7168 x 7168 2
-// tiles 47, 4 97; 37 x 2112 x 1536 2 tiles 6.4, 1 8.9.
+// MI355X, gated E4M3, before x and the weights were read by pairs of lanes: 32 x
+// 7168 x 7168 4 tiles 27 us, 2 36; 64 x 7168 x 7168 2 tiles 47, 4 97; 37 x 2112
+// x 1536 2 tiles 6.4, 1 8.9.
 static int pick_block_tiles(int64_t tiles, int cus, int token_blocks) {
     return token_blocks == 2 ? pick_tiles(tiles, cus, {1, 2, 4}) : pick_tiles(tiles, cus, {1, 2});
 }
@@ -92,15 +94,15 @@ static fp8_status run_token_blocks(const fp8k::SkinnyParams& p, int cus, hipStre
     else return FP8_ERR_UNSUPPORTED;
 }
 
-// Of a K block a workgroup reads and widens its token blocks (0.05 us each) and
-// its weight tiles (0.08 each), and multiplies them (0.01 a pair); fitted on
-// one MI355X to 1-64 x 512-24576 x 1536 and 7168, within 20% (64 x 512 x 1536
-// 6.8 us for 6.9, 64 x 7168 x 7168 52 for 50, 64 x 24576 x 7168 151 for 140).
+// Of a K block a workgroup reads and widens its token blocks (0.015 us each) and
+// its weight tiles (0.05 each), and multiplies them (0.024 a pair); fitted on
+// one MI355X to 1-64 x 512-24576 x 1536 and 7168, within 15% (64 x 512 x 1536
+// 5.5 us for 6.0, 64 x 2048 x 7168 14.5 for 14.2, 32 x 7168 x 7168 26.6 for 23.6).
 double skinny_gated_e4m3_us(int64_t M, int64_t N, int64_t K, int cus) {
     const int64_t tiles = cdiv(N * 2, 16);
     const int mb = (int)cdiv(M, 16);
-    const int rt = mb == 1 ? pick_tiles(tiles, cus, {1, 2, 4, 6}) : pick_block_tiles(tiles, cus, mb);
-    return 3.0 + (double)(K / 128 * cdiv(cdiv(tiles, rt), cus)) * (0.05 * mb + rt * (0.08 + 0.01 * mb));
+    const int rt = mb == 1 ? pick_tiles(tiles, cus, {1, 2, 4}) : pick_block_tiles(tiles, cus, mb);
+    return 3.0 + (double)(K / 128 * cdiv(cdiv(tiles, rt), cus)) * (0.015 * mb + rt * (0.05 + 0.024 * mb));
 }
 
 fp8_status run_skinny_gated_e4m3(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
