@@ -5,6 +5,8 @@
 // As in fp8gemm_api.hip every entry point validates on the host, enqueues
 // nothing on an error, launches on the caller's stream, and neither
 // allocates, frees nor synchronizes.
+#include <algorithm>
+
 #include "host_common.h"
 #include "kernels_clip.h"
 #include "kernels_exact.h"
@@ -187,8 +189,9 @@ struct GradPlan {
     bool dx_wide, dw_wide;      // 128x256 tiles, else 128x128
     bool dw_first;
     int64_t dx_tiles, dw_tiles, dx_splits, dw_splits;
-    size_t d_bytes, dx_part, dw_part;   // workspace: dg and du, then FP32 sums
-    size_t bytes() const { return d_bytes + dx_part + dw_part; }
+    int64_t arrived;            // tiles with splits
+    size_t d_bytes, dx_part, dw_part;   // workspace: dg and du, then FP32 sums, then a count per such tile
+    size_t bytes() const { return d_bytes + dx_part + dw_part + (size_t)arrived * sizeof(int32_t); }
 };
 
 // Two workgroups of four waves with 128x256 tiles (64x128 per wave) fit a
@@ -209,19 +212,31 @@ GradPlan grad_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int cus) {
     pl.dw_tiles = dw_rows * cdiv(K, pl.dw_wide ? 256 : 128);
     pl.dw_first = dw_blocks > dx_blocks;
     pl.d_bytes = (size_t)(2 * M * grad_np(N)) * sizeof(uint16_t);
-    // A product whose few tiles have contractions several times the share of a
-    // slot would run alone at the end: split it.
+    // Split a product whose few tiles have contractions several times the share
+    // of a slot (they would run alone at the end), and tiles that leave half of
+    // the slots empty; the sums of more splits, written past the caches, cost
+    // more than they save.  One MI355X, us: 256x4096x7168 106 (unsplit 145),
+    // 384x4096x4096 90 (129), 20x600x1024 15.0 (18.0), 777x500x640 16.1 (18.3);
+    // tiles of about a share: 500x2112x7168 92 (87), 1500x1024x2048 53 (39).
     const int64_t slots = (pl.dx_wide || pl.dw_wide ? 2 : 3) * cus;
     const int64_t share = (pl.dx_tiles * dx_blocks * (pl.dx_wide ? 2 : 1) +
                            pl.dw_tiles * dw_blocks * (pl.dw_wide ? 2 : 1)) / slots;
+    const int64_t tiles = pl.dx_tiles + pl.dw_tiles;
     auto splits = [&](int64_t n_tiles, int64_t blocks) {
-        const int64_t s = n_tiles ? blocks / (share > 16 ? share : 16) : 1;
-        return s < 3 ? (int64_t)1 : s > 8 ? (int64_t)8 : s;
+        if (!n_tiles) return (int64_t)1;
+        int64_t s = blocks / (share > 16 ? share : 16);
+        if (s < 2) s = std::min(blocks / 16, slots / tiles);
+        return std::clamp(s, (int64_t)1, (int64_t)8);
     };
     pl.dx_splits = splits(pl.dx_tiles, dx_blocks);
     pl.dw_splits = splits(pl.dw_tiles, dw_blocks);
-    if (pl.dx_splits > 1) pl.dx_part = (size_t)(pl.dx_splits * M * K) * sizeof(float);
-    if (pl.dw_splits > 1) pl.dw_part = (size_t)(pl.dw_splits * 2 * N * K) * sizeof(float);
+    auto part = [&](int64_t n_tiles, int64_t s, bool wide) -> size_t {
+        if (s == 1) return 0;
+        pl.arrived += n_tiles;
+        return (size_t)(n_tiles * s * 128 * (wide ? 256 : 128)) * sizeof(float);
+    };
+    pl.dx_part = part(pl.dx_tiles, pl.dx_splits, pl.dx_wide);
+    pl.dw_part = part(pl.dw_tiles, pl.dw_splits, pl.dw_wide);
     return pl;
 }
 
@@ -233,13 +248,6 @@ fp8_status launch_grad(const fp8k::GatedGradParams& p, bool dw_first, hipStream_
     return launch_status();
 }
 
-fp8_status launch_grad_join(const float* part, int64_t splits, int64_t half, int64_t total, uint16_t* out0,
-                            uint16_t* out1, hipStream_t stream) {
-    hipLaunchKernelGGL(fp8k::gated_grad_join_kernel, dim3((unsigned)cdiv(total, 1024)), dim3(256), 0, stream, part,
-                       (int)splits, half, total, out0, out1);
-    return launch_status();
-}
-
 fp8_status run_grad(fp8k::GatedGradParams& p, const GradPlan& pl, uint8_t* ws, hipStream_t s) {
     if (pl.dx_tiles * pl.dx_splits + pl.dw_tiles * pl.dw_splits > 0x7FFFFFFF ||
         cdiv(p.M * (p.NP / 8), 256) > 0x7FFFFFFF)
@@ -247,6 +255,8 @@ fp8_status run_grad(fp8k::GatedGradParams& p, const GradPlan& pl, uint8_t* ws, h
     p.d = reinterpret_cast<uint16_t*>(ws);
     p.dx_part = reinterpret_cast<float*>(ws + pl.d_bytes);
     p.dw_part = reinterpret_cast<float*>(ws + pl.d_bytes + pl.dx_part);
+    p.arrived = reinterpret_cast<int32_t*>(ws + pl.d_bytes + pl.dx_part + pl.dw_part);
+    p.arrived_tiles = (int32_t)pl.arrived;
     p.dx_tiles = (int32_t)pl.dx_tiles;
     p.dw_tiles = (int32_t)pl.dw_tiles;
     p.dx_splits = (int32_t)pl.dx_splits;
@@ -263,10 +273,6 @@ fp8_status run_grad(fp8k::GatedGradParams& p, const GradPlan& pl, uint8_t* ws, h
         if (pl.dx_wide) st = pl.dw_wide ? launch_grad<256, 256, 2>(p, pl.dw_first, s) : launch_grad<256, 128, 2>(p, pl.dw_first, s);
         else st = pl.dw_wide ? launch_grad<128, 256, 2>(p, pl.dw_first, s) : launch_grad<128, 128, 3>(p, pl.dw_first, s);
     }
-    if (st == FP8_OK && pl.dx_splits > 1)
-        st = launch_grad_join(p.dx_part, pl.dx_splits, p.M * p.K, p.M * p.K, p.dx, nullptr, s);
-    if (st == FP8_OK && pl.dw_splits > 1)
-        st = launch_grad_join(p.dw_part, pl.dw_splits, p.N * p.K, 2 * p.N * p.K, p.dw[0], p.dw[1], s);
     return st;
 }
 

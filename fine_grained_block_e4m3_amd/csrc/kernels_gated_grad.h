@@ -10,7 +10,8 @@
 //
 //   1. gated_grad_act_kernel writes dg and du, rows padded with zeros to a
 //      multiple of 64 columns (a stream: 6 bytes read, 4 written per element).
-//   2. gated_grad_gemm_kernel forms the products.  None of the operands is
+//   2. gated_grad_gemm_kernel forms the products, long contractions of few
+//      tiles split over workgroups, the last of which joins the FP32 sums.  None of the operands is
 //      transposed in memory: an operand whose contraction runs along its rows'
 //      elements (dg, du in dX) is staged in LDS as 64-byte row pieces and read
 //      with ds_read_b128; one whose contraction runs over its rows (W in dX,
@@ -47,8 +48,10 @@ struct GatedGradParams {
     int32_t act;
     int32_t dx_tiles, dw_tiles; // tiles of dX, and of dWg and dWu together
     int32_t dx_splits, dw_splits;   // workgroups per tile along the contraction
-    float* dx_part;             // dx_splits > 1: FP32 sums [split][M][K]
-    float* dw_part;             // dw_splits > 1: FP32 sums [split][2][N][K]
+    float* dx_part;             // splits > 1: FP32 sums [tile][split] of whole tiles
+    float* dw_part;
+    int32_t* arrived;           // ... and how many splits of a tile are done: dX's tiles, then the others
+    int32_t arrived_tiles;
 };
 
 // Eight elements of a row per thread.
@@ -56,6 +59,7 @@ template <bool VEC>
 __global__ __launch_bounds__(256) void gated_grad_act_kernel(GatedGradParams p) {
     const int64_t per_row = p.NP / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    for (int64_t j = i; j < p.arrived_tiles; j += (int64_t)gridDim.x * 256) p.arrived[j] = 0;
     if (i >= p.M * per_row) return;
     const int64_t m = i / per_row, n = (i - m * per_row) * 8;
     const int64_t at = m * p.N + n;
@@ -189,7 +193,8 @@ struct GradTile {
     int64_t len;
     int split, splits;          // this workgroup's share of the contraction
     uint16_t* out;              // result element (0, 0) of the tile
-    float* part;                // ... of this split's FP32 sums (splits > 1)
+    float* part;                // splits > 1: the tile's FP32 sums, split by split
+    int32_t* arrived;           // ... and its splits that are done
     int64_t out_ld;
     int rows, cols;             // valid part
 };
@@ -326,22 +331,53 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
     // lane l, value v of subtile (a, b): row 32a + l%32, column 32b + 8(v/4) + 4(l/32) + v%4
     const int h = lane >> 5;
     if (t.splits > 1) {
+        // The split that comes last adds all of them, in split order, so that
+        // the result does not depend on which one it is.  A thread reads back
+        // what the same threads of the other splits wrote.
+        // The sums are stored past the caches of an XCD and read the same way (a
+        // fence would write back and drop the whole L2: 500 x 2112 x 7168 188
+        // us for 92).
+        constexpr int THREADS = 64 * NWAVES, kDeviceScope = 16;
+        typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+        const auto sums = __builtin_amdgcn_make_buffer_rsrc(t.part, 0, t.splits * BM * BN * 4, 0x00027000);
+        const int own = t.split * (BM * BN * 4);
 #pragma unroll
-        for (int a = 0; a < FI; ++a) {
-            const int m = wm * TM + 32 * a + (lane & 31);
-            if (m >= t.rows) continue;
+        for (int a = 0; a < FI; ++a)
 #pragma unroll
             for (int b = 0; b < FJ; ++b)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = wn * TN + 32 * b + 8 * q + 4 * h;
-                    // K % 128 == 0: whole groups of 4 columns, 16-byte aligned
-                    if (n < t.cols)
-                        *reinterpret_cast<f32x4*>(t.part + (int64_t)m * t.out_ld + n) =
-                            f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
-                }
-        }
-        return;
+                for (int q = 0; q < 4; ++q)
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        __builtin_bit_cast(u32x4, f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2],
+                                                        acc[a][b][4 * q + 3]}),
+                        sums, 16 * (int)threadIdx.x, own + ((a * FJ + b) * 4 + q) * 16 * THREADS, kDeviceScope);
+        wait_vmcnt<0>();
+        __syncthreads();
+        int32_t* const before = reinterpret_cast<int32_t*>(smem);   // the stages are done with
+        if (threadIdx.x == 0)
+            *before = __hip_atomic_fetch_add(t.arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (uniform(*before) != t.splits - 1) return;
+#pragma unroll
+        for (int a = 0; a < FI; ++a)
+#pragma unroll
+            for (int b = 0; b < FJ; ++b)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.f;
+        for (int s = 0; s < t.splits; ++s)
+#pragma unroll
+            for (int a = 0; a < FI; ++a)
+#pragma unroll
+                for (int b = 0; b < FJ; ++b)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 v = __builtin_bit_cast(
+                            f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                       sums, 16 * (int)threadIdx.x,
+                                       s * (BM * BN * 4) + ((a * FJ + b) * 4 + q) * 16 * THREADS, kDeviceScope));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[a][b][4 * q + e] += v[e];
+                    }
     }
     // BF16 results through LDS, so that a wave stores whole rows of the tile
     // (straight from the accumulators a store covers 16 bytes of each of 32
@@ -410,7 +446,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void gated_grad_gemm_k
         t.segs = 2;
         t.len = p.NP;
         t.out = p.dx + m0 * p.K + n0;
-        t.part = p.dx_part + (t.split * p.M + m0) * p.K + n0;
+        t.part = p.dx_part + (int64_t)(at / t.splits) * t.splits * (BM * BNX);
+        t.arrived = p.arrived + at / t.splits;
         t.rows = (int)min((int64_t)BM, p.M - m0);
         t.cols = (int)min((int64_t)BNX, p.K - n0);
         grad_tile<BM, BNX, WAVES_M, WAVES_N, STAGES, false>(t, smem);
@@ -432,23 +469,12 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void gated_grad_gemm_k
         t.segs = 1;
         t.len = p.M;
         t.out = p.dw[z] + m0 * p.K + n0;
-        t.part = p.dw_part + ((2 * t.split + z) * p.N + m0) * p.K + n0;
+        t.part = p.dw_part + (int64_t)tile * t.splits * (BM * BNW);
+        t.arrived = p.arrived + (p.dx_splits > 1 ? p.dx_tiles : 0) + tile;
         t.rows = (int)min((int64_t)BM, p.N - m0);
         t.cols = (int)min((int64_t)BNW, p.K - n0);
         grad_tile<BM, BNW, WAVES_M, WAVES_N, STAGES, true>(t, smem);
     }
-}
-
-// out = the splits' FP32 sums in split order, rounded; four elements per
-// thread of `half` to out0 and the next `half` to out1 (K % 128 == 0).
-__global__ __launch_bounds__(256) void gated_grad_join_kernel(const float* __restrict__ part, int splits, int64_t half,
-                                                              int64_t total, uint16_t* out0, uint16_t* out1) {
-    const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
-    if (i >= total) return;
-    f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
-    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(part + s * total + i);
-    uint16_t* out = i < half ? out0 + i : out1 + (i - half);
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
 }  // namespace fp8k

@@ -203,3 +203,48 @@ def test_side_stream_and_graph():
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
         fp8.gated_nt_grad(*ops)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M,N,K", [(777, 500, 640), (2000, 130, 256), (256, 1024, 1024), (20, 600, 1024),
+                                   (256, 4096, 7168)])
+def test_split_contractions_are_repeatable(M, N, K):
+    """Tiles whose splits are joined by whichever comes last: the same bits in
+    every call, in a workspace that holds other values each time, eagerly and
+    replayed, and for each result alone."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+
+    def rand(r, c, s):
+        return torch.randn((r, c), generator=g, device="cuda").mul_(s).bfloat16()
+
+    ops = [rand(M, N, 0.1), rand(M, N, 1.5), rand(M, N, 1.5), rand(M, K, 1.0), rand(N, K, 0.05), rand(N, K, 0.05)]
+    size = fp8.load_library().fp8_gated_grad_workspace_size(M, N, K)
+    say(f"grad splits M={M} N={N} K={K} workspace={size}")
+    assert size > 2 * 2 * M * ((N + 63) // 64 * 64)
+    full, ws = guarded((size // 2,))
+    ws = ws.view(torch.uint8)
+    want = [t.clone() for t in fp8.gated_nt_grad(*ops)]
+    dg, du = (t.bfloat16().float() for t in _act_grads(*(t.float() for t in ops[:3])))
+    for got, ref32 in ((want[0], dg @ ops[4].float() + du @ ops[5].float()), (want[1], dg.t() @ ops[3].float()),
+                       (want[2], du.t() @ ops[3].float())):
+        # one rounding of each result, one of dg and du, in the 2-norm
+        assert float((got.float() - ref32).norm()) <= 2.0 ** -8 * float(ref32.norm())
+    for i in range(12):
+        ws.fill_(17 * i)
+        assert all(torch.equal(a, b) for a, b in zip(fp8.gated_nt_grad(*ops, workspace=ws), want))
+    check_guards(full, size // 2)
+    outs = [torch.empty_like(t) for t in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fp8.gated_nt_grad(*ops, out=outs, workspace=ws)
+    for _ in range(4):
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        fp8.gated_nt_grad(*ops)
+
+
+def _act_grads(dh, g, u):
+    p = torch.sigmoid(g)
+    return dh * u * p * (1 + g * (1 - p)), dh * g * p
