@@ -555,13 +555,20 @@ def gated_nt_qout(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = F
     return hq, sh
 
 
-def gated_nt_grad(dh, g, u, x, wg, wu, act: str = "silu", need_dx: bool = True, need_dw: bool = True, out=None,
-                  workspace=None):
-    """Gradient of the gated block, BF16: dh, g, u (M, N), x (M, K), wg, wu
-    (N, K) -> (dx (M, K), dwg (N, K), dwu (N, K)); dx is None without need_dx,
-    dwg and dwu without need_dw.  out: (dx, dwg, dwu) buffers."""
-    L = load_library()
-    a = _act(act)
+def _grad_operands(dh, g, u, x, wg, wu):
+    # (one expression for operands that fit, as in _gated_operands)
+    try:
+        M, N = dh.shape
+        K = x.shape[1]
+        if (dh.dtype is _BF16 and g.dtype is _BF16 and u.dtype is _BF16 and x.dtype is _BF16 and wg.dtype is _BF16
+                and wu.dtype is _BF16 and g.shape == u.shape == (M, N) and x.shape == (M, K)
+                and wg.shape == wu.shape == (N, K) and dh.is_contiguous() and g.is_contiguous() and u.is_contiguous()
+                and x.is_contiguous() and wg.is_contiguous() and wu.is_contiguous()
+                and (0 <= dh.get_device() == g.get_device() == u.get_device() == x.get_device()
+                     == wg.get_device() == wu.get_device())):
+            return M, N, K
+    except (AttributeError, TypeError, ValueError, IndexError):
+        pass
     for t, name in ((dh, "dh"), (g, "g"), (u, "u"), (x, "x"), (wg, "wg"), (wu, "wu")):
         _need(t, name, torch.bfloat16, 2)
     M, N = dh.shape
@@ -569,10 +576,20 @@ def gated_nt_grad(dh, g, u, x, wg, wu, act: str = "silu", need_dx: bool = True, 
     if g.shape != (M, N) or u.shape != (M, N) or x.shape[0] != M or wg.shape != (N, K) or wu.shape != (N, K):
         raise ValueError("gated_nt_grad: inconsistent operand shapes")
     _same_device(dh, g, u, x, wg, wu)
+    return M, N, K
+
+
+def gated_nt_grad(dh, g, u, x, wg, wu, act: str = "silu", need_dx: bool = True, need_dw: bool = True, out=None,
+                  workspace=None):
+    """Gradient of the gated block, BF16: dh, g, u (M, N), x (M, K), wg, wu
+    (N, K) -> (dx (M, K), dwg (N, K), dwu (N, K)); dx is None without need_dx,
+    dwg and dwu without need_dw.  out: (dx, dwg, dwu) buffers."""
+    L = load_library()
+    a = _act(act)
+    M, N, K = _grad_operands(dh, g, u, x, wg, wu)
     shapes, wanted = ((M, K), (N, K), (N, K)), (need_dx, need_dw, need_dw)
     if out is None:
-        ys = [torch.empty(shape, dtype=torch.bfloat16, device=dh.device) if w else None
-              for shape, w in zip(shapes, wanted)]
+        ys = [dh.new_empty(shape) if w else None for shape, w in zip(shapes, wanted)]
     else:
         ys = [_out(t, f"out[{i}]", torch.bfloat16, shape, dh) if w else None
               for i, (t, shape, w) in enumerate(zip(out, shapes, wanted))]
