@@ -27,8 +27,9 @@ bool act_ok(int32_t act) { return act == FP8_ACT_SILU || act == FP8_ACT_GELU; }
 enum GatedOutputs : int32_t { kOutH = 0, kOutSave = 1, kOutQuant = 2 };
 
 // Up to 64 tokens may take a kernel built around the weights' stream
-// (kernels_skinny.h), K split inside its workgroups.  Tiles of the rest: rows x output columns, and the time of one K block when
-// every compute unit has one (one MI355X, K 7168, us).
+// (kernels_skinny.h), K split inside its workgroups.  Tiles of the rest: rows x
+// output columns, and the time of one K block when every compute unit has one
+// (one MI355X, K 7168, us).
 enum GatedTile : int { kGated256x128, kGated128x128, kGated128x64, kGated64x128, kGated64x64, kGatedTiles };
 struct GatedTileInfo {
     int bm, cols;

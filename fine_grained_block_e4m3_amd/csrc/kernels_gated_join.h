@@ -9,9 +9,9 @@ namespace fp8k {
 // ---------------------------------------------------------------------------
 // Gated feed-forward block with K split over workgroups (tiles too few to fill
 // the device), or codes of few tokens, whose groups of 128 columns no workgroup
-// of kernels_skinny.h holds (S = 1): joins the FP32 partial sums of the gate (part[0][s]) and up
-// (part[1][s]) projections, s in order, and forms h = act(g) * u.  A wave
-// takes 128 columns of one row (two per lane), the group of the quantized
+// of kernels_skinny.h holds (S = 1): joins the FP32 partial sums of the gate
+// (part[0][s]) and up (part[1][s]) projections, s in order, and forms
+// h = act(g) * u.  A wave takes 128 columns of one row (two per lane), the group of the quantized
 // form.  A stream of the sums (300 x 2048, 8 splits: 5.4 us with its launch).
 // ---------------------------------------------------------------------------
 template <bool QOUT, bool POW2>

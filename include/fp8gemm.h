@@ -364,7 +364,8 @@ fp8_status fp8_gemm_plan(int32_t layout, int64_t M, int64_t N, int64_t K,
  * workspace: where the output has too few tiles to fill the device, or has
  * few tokens and is quantized, fp8_gated_workspace_size() bytes (0: none is
  * used) hold FP32 sums for a second kernel; without them, or with fewer, one
- * kernel does all, slower.  outputs (of the size query): 0 h, 1 h with g and u, 2 quantized.
+ * kernel does all, slower.  outputs (of the size query): 0 h, 1 h with g and
+ * u, 2 quantized.
  */
 fp8_status fp8_gated_nt(const uint8_t* xq, const float* sa, const uint8_t* wgq,
                         const float* sbg, const uint8_t* wuq, const float* sbu,
@@ -395,8 +396,9 @@ fp8_status fp8_gated_nt_qout(const uint8_t* xq, const float* sa, const uint8_t* 
  *   N == 0 dx is.
  * dg and du are formed in FP32 and rounded to BF16, the matrix instruction's
  * type; sums are FP32, and each result is rounded once.  The workspace (dg
- * and du, and FP32 sums where a contraction is split) is required: fp8_gated_grad_workspace_size() bytes, else
- * FP8_ERR_SCRATCH.
+ * and du, and FP32 sums and counts where a contraction is split) is required:
+ * fp8_gated_grad_workspace_size() bytes, else FP8_ERR_SCRATCH.  It needs no
+ * clearing; calls that overlap in time need one each.
  */
 fp8_status fp8_gated_nt_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
                              const uint16_t* x, const uint16_t* wg, const uint16_t* wu,
