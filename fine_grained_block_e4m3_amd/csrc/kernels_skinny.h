@@ -417,11 +417,11 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
     for (int o = wave; o < OT * MB; o += KW) {
         const int t = o / MB, c = o - t * MB;
         const int64_t m = 16 * c + r, n = n0 + 16 * t + 4 * q;
-        const bool whole = (N & 3) == 0 && n + 3 < N;
         auto store = [&](uint16_t* out, f32x4 v) FP8K_INLINE {
             const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
-            if (whole) {
-                *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+            if (n + 3 < N) {
+                const uint2 all = make_uint2(lo, hi);
+                __builtin_memcpy(out, &all, 8);
             } else {
                 if (n < N) out[0] = (uint16_t)(lo & 0xFFFF);
                 if (n + 1 < N) out[1] = (uint16_t)(lo >> 16);
