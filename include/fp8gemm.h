@@ -378,6 +378,10 @@ size_t fp8_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t outputs
  * fp8_gated_nt with h quantized for the next GEMM (the down projection), from
  * the FP32 values, as fp8_gemm_nt_qout does:
  *   hq u8 (M,N) E4M3 codes, sh fp32 [N/128][M] 1x128 scales; N % 128 == 0.
+ * The scale follows the group's FP32 maximum.  A power-of-two scale is a step
+ * function of it: where max|h| / 448 in unlimited precision lies within the
+ * FP32 error of a power of two, the scale is that power or its double, and the
+ * codes go with it; either pair stands for h to within an E4M3 rounding.
  */
 fp8_status fp8_gated_nt_qout(const uint8_t* xq, const float* sa, const uint8_t* wgq,
                              const float* sbg, const uint8_t* wuq, const float* sbu,
