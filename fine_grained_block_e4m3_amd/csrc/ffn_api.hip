@@ -205,7 +205,7 @@ struct GradPlan {
 // 256x256 workgroup of eight waves per compute unit: 440 us on the first.
 GradPlan grad_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int cus) {
     GradPlan pl{};
-    const int64_t dx_blocks = 2 * grad_np(N) / 32, dw_blocks = cdiv(M, 32);     // of 32 steps
+    const int64_t dx_blocks = 2 * cdiv(N, 32), dw_blocks = cdiv(M, 32);     // of 32 steps
     const int64_t dx_rows = dx ? cdiv(M, 128) : 0, dw_rows = dw ? 2 * cdiv(N, 128) : 0;
     pl.dx_wide = dx_rows * cdiv(K, 256) >= 2 * cus;
     pl.dw_wide = dw_rows * cdiv(K, 256) >= 2 * cus;

@@ -232,10 +232,14 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
     const int first = (int)((int64_t)all * t.split / t.splits);
     const int nblocks = (int)((int64_t)all * (t.split + 1) / t.splits) - first;
     // The blocks come in runs of one buffer resource per operand, along which
-    // only the scalar offset advances.  A segment's last block is a run of its
-    // own (offset 0), so that the resource's range ends exactly at the operand;
-    // past it, and past the workgroup's blocks, loads read zeros.  Runs are
-    // short enough for 32-bit offsets.
+    // only the scalar offset advances.  The range check is relied on for the
+    // vector offset alone (whether it counts the scalar offset too makes no
+    // difference): within a run every row of a block is one of the operand's,
+    // and a segment's last block, the only one whose rows may pass the end
+    // (t.len is the contraction's own length), is a run of its own with offset
+    // 0, so that the resource's range ends exactly at the operand.  Past that,
+    // and past the workgroup's blocks, loads read zeros.  Runs are short enough
+    // for 32-bit offsets.
     auto range = [](int64_t elems) FP8K_INLINE {
         return (uint32_t)(elems <= 0 ? 0 : elems >= (1ll << 30) ? (1ll << 31) : 2 * elems);
     };
@@ -445,7 +449,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void gated_grad_gemm_k
         t.p_ld = p.NP;
         t.p_step = 1;
         t.segs = 2;
-        t.len = p.NP;
+        t.len = p.N;
         t.out = p.dx + m0 * p.K + n0;
         t.part = p.dx_part + (int64_t)(at / t.splits) * t.splits * (BM * BNX);
         t.arrived = p.arrived + at / t.splits;
