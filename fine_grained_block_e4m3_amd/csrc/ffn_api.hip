@@ -223,21 +223,22 @@ GradPlan grad_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int cus) {
     const int64_t share = (pl.dx_tiles * dx_blocks * (pl.dx_wide ? 2 : 1) +
                            pl.dw_tiles * dw_blocks * (pl.dw_wide ? 2 : 1)) / slots;
     const int64_t tiles = pl.dx_tiles + pl.dw_tiles;
-    auto splits = [&](int64_t n_tiles, int64_t blocks) {
-        if (!n_tiles) return (int64_t)1;
+    // (a product with wide tiles has one for every slot: it is not split)
+    auto splits = [&](int64_t n_tiles, int64_t blocks, bool wide) {
+        if (!n_tiles || wide) return (int64_t)1;
         int64_t s = blocks / (share > 16 ? share : 16);
         if (s < 2) s = std::min(blocks / 16, slots / tiles);
         return std::clamp(s, (int64_t)1, (int64_t)8);
     };
-    pl.dx_splits = splits(pl.dx_tiles, dx_blocks);
-    pl.dw_splits = splits(pl.dw_tiles, dw_blocks);
-    auto part = [&](int64_t n_tiles, int64_t s, bool wide) -> size_t {
+    pl.dx_splits = splits(pl.dx_tiles, dx_blocks, pl.dx_wide);
+    pl.dw_splits = splits(pl.dw_tiles, dw_blocks, pl.dw_wide);
+    auto part = [&](int64_t n_tiles, int64_t s) -> size_t {
         if (s == 1) return 0;
         pl.arrived += n_tiles;
-        return (size_t)(n_tiles * s * 128 * (wide ? 256 : 128)) * sizeof(float);
+        return (size_t)(n_tiles * s * 128 * 128) * sizeof(float);
     };
-    pl.dx_part = part(pl.dx_tiles, pl.dx_splits, pl.dx_wide);
-    pl.dw_part = part(pl.dw_tiles, pl.dw_splits, pl.dw_wide);
+    pl.dx_part = part(pl.dx_tiles, pl.dx_splits);
+    pl.dw_part = part(pl.dw_tiles, pl.dw_splits);
     return pl;
 }
 

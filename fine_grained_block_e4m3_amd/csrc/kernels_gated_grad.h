@@ -335,13 +335,14 @@ __device__ __forceinline__ void grad_tile(const GradTile& t, uint8_t* smem) {
 
     // lane l, value v of subtile (a, b): row 32a + l%32, column 32b + 8(v/4) + 4(l/32) + v%4
     const int h = lane >> 5;
-    if (t.splits > 1) {
+    // (tiles of 256 columns are taken only where they fill every slot, unsplit)
+    if (BN == 128 && t.splits > 1) {
         // The split that comes last adds all of them, in split order, so that
         // the result does not depend on which one it is.  A thread reads back
         // what the same threads of the other splits wrote.
         // The sums are stored past the caches of an XCD and read the same way (a
         // fence would write back and drop the whole L2: 500 x 2112 x 7168 188
-        // us for 92).
+        // us for 92, while that shape was split).
         constexpr int THREADS = 64 * NWAVES, kDeviceScope = 16;
         typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
         const auto sums = __builtin_amdgcn_make_buffer_rsrc(t.part, 0, t.splits * BM * BN * 4, 0x00027000);
