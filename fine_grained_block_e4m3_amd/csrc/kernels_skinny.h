@@ -32,16 +32,20 @@
 //   * The loads of the D - 1 blocks that follow are in flight while a block is
 //     multiplied.
 // Exactness: E2M1 times a power of two is a BF16 value (products exact, FP32
-// sums).  4-bit integers enter as the BF16 integers q; the group's sum of x
-// comes from the same instruction with a matrix of ones, and
-// s * (sum x q - z * sum x) is formed in FP32 per group.  E4M3 is widened exactly to FP16.
+// sums; weights of 2^128 and more are infinite, and the scale byte 255 is NaN).
+// 4-bit integers enter as the BF16 integers q - z, -15 .. 15, so that a weight
+// of zero adds nothing and an infinite x gives what the definition gives; the
+// group's sum of x (q - z) is scaled in FP32.  (z applied after the sum, as
+// s * (sum x q - z * sum x), takes half the instructions per weight, but
+// cancels, and gives NaN for an infinite x.)  E4M3 is widened exactly to FP16.
 // Measured (one MI355X, kernel time): gated E4M3 1 x 2048 x 7168 7.4 us
 // (29 MB: 4.0 TB/s, the launch's 2.3 us included), MXFP4 1 x 24576 x 7168
-// 21 us (4.4 TB/s) and 16 x 24576 x 7168 23 us, int4 with groups of 128 23 and
-// 25 us, with groups of 32 and zero points 31 and 40, gated int4 (groups of 64,
-// zero points) 3 x 2112 x 7168 9.5 us.  With the weights as A for 4-bit
-// integers too, four scales and zero points per lane and group: 24 and 29 (zero
-// points), 45 and 51, 11.4.
+// 21 us (4.4 TB/s) and 16 x 24576 x 7168 23 us; int4 1 and 16 x 24576 x 7168
+// with groups of 128 24 and 26.4 us, with zero points 26.3 and 28.7, with
+// groups of 64 and zero points 32.5 (16), with groups of 32 and zero points
+// 33.3 and 37.9; gated int4 (groups of 64, zero points) 3 x 2112 x 7168 10.8 us.
+// With z applied after the sum: 22.1 and 25.0, 22.7 and 25.5, 30.0, 31.4 and
+// 39.0; 9.8.
 // Gated E4M3 with g and u stored as well: 1 x 2048 x 7168 7.6 us; with codes
 // instead (FP32 sums, then the joining kernel) 11, the tiles 16.6 and 17.2.
 #pragma once
@@ -103,24 +107,38 @@ __device__ __forceinline__ void transpose_quad_lanes(i32x4 (&v)[4], int lane) {
     }
 }
 
-// Eight 4-bit codes of a dword as BF16 integers, in the order 0, 2, 4, 6, 1, 3,
-// 5, 7.  A byte of value q < 16 is the E4M3 value q * 2^-9 (subnormal below 8,
-// exponent 1 above), so the hardware converter widens them at scale 2^9.
-__device__ __forceinline__ bf16x8 u4x8_to_bf16(int v) {
-    const unsigned lo = (unsigned)v & 0x0F0F0F0Fu, hi = ((unsigned)v >> 4) & 0x0F0F0F0Fu;
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
-    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
-    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
-    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-// Eight BF16 values in that order.
-__device__ __forceinline__ bf16x8 bf16x8_u4_order(i32x4 x) {
+// Eight 4-bit codes of a dword less the zero point z, as BF16 integers in the
+// order of the elements.  A half word with nothing but a code in its low bits is
+// the FP16 subnormal q * 2^-24 (q * 2^-20 four bits higher), which one
+// instruction with FP16 and FP32 operands turns into q - z; BF16 holds that.
+__device__ __forceinline__ bf16x8 u4x8_less_zero_to_bf16(int v, float zero) {
     i32x4 r;
-    r[0] = (int)__builtin_amdgcn_perm((unsigned)x[1], (unsigned)x[0], 0x05040100u);
-    r[1] = (int)__builtin_amdgcn_perm((unsigned)x[3], (unsigned)x[2], 0x05040100u);
-    r[2] = (int)__builtin_amdgcn_perm((unsigned)x[1], (unsigned)x[0], 0x07060302u);
-    r[3] = (int)__builtin_amdgcn_perm((unsigned)x[3], (unsigned)x[2], 0x07060302u);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {       // codes 0, 1, 4, 5 and then 2, 3, 6, 7
+        const unsigned c = (unsigned)v >> (8 * h);
+        const f16x2 a = __builtin_bit_cast(f16x2, c & 0x000F000Fu), b = __builtin_bit_cast(f16x2, c & 0x00F000F0u);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float even = __builtin_fmaf((float)a[j], 0x1p24f, -zero);
+            const float odd = __builtin_fmaf((float)b[j], 0x1p20f, -zero);
+            r[2 * j + h] = (int)__builtin_amdgcn_perm(__float_as_uint(odd), __float_as_uint(even), 0x07060302u);
+        }
+    }
+    return __builtin_bit_cast(bf16x8, r);
+}
+// Eight 4-bit codes of a dword less 8, as BF16 values of 1/16 of that, in the
+// order of the elements: the hardware converter of a byte's low four bits, taken
+// as two's complement, whose FP32 results BF16 holds.
+__device__ __forceinline__ bf16x8 u4x8_less8_to_bf16(int v) {
+    unsigned lo = (unsigned)v ^ 0x88888888u, hi = lo >> 4;
+    asm("" : "+v"(lo), "+v"(hi));       // one shift; then every code is a byte operand
+    i32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = __builtin_amdgcn_cvt_off_f32_i4((int)(lo >> (8 * j) & 0xFFu));
+        const float b = __builtin_amdgcn_cvt_off_f32_i4((int)(hi >> (8 * j) & 0xFFu));
+        r[j] = (int)__builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+    }
     return __builtin_bit_cast(bf16x8, r);
 }
 // Eight E2M1 codes of a dword times the power of two `scale`, as BF16.
@@ -316,7 +334,6 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
                 }
             }
         } else {
-            const bf16x8 ones = __builtin_bit_cast(bf16x8, i32x4{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80});
             i32x4 wt[RT];
 #pragma unroll
             for (int t = 0; t < RT; ++t) wt[t] = kTranspose ? transpose_quads(b.w[t][0]) : b.w[t][0];
@@ -325,7 +342,7 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
             uint32_t sz[RT][4];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                sz[t][0] = (uint32_t)b.s[t] << 16 | (ZEROS ? b.z[t] : 8u);
+                sz[t][0] = (uint32_t)b.s[t] << 16 | (ZEROS ? b.z[t] & 15u : 0u);
                 if constexpr (NG == 4) {
                     const auto h = __builtin_amdgcn_permlane32_swap(sz[t][0], sz[t][0], false, false);
                     const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
@@ -338,27 +355,30 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                f32x4 part[RT], sx{};
+                f32x4 part[RT];
+                float zero[RT];
 #pragma unroll
-                for (int t = 0; t < RT; ++t) part[t] = f32x4{};
+                for (int t = 0; t < RT; ++t) {
+                    part[t] = f32x4{};
+                    zero[t] = (float)(sz[t][g] & 0xFFu);
+                }
 #pragma unroll
                 for (int i = 0; i < 4 / NG; ++i) {
                     const int s = g * (4 / NG) + i;
-                    const bf16x8 xv = bf16x8_u4_order(b.x[0][s]);
-                    sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, sx, 0, 0, 0);
+                    const bf16x8 xv = __builtin_bit_cast(bf16x8, b.x[0][s]);
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
-                        part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, u4x8_to_bf16(wt[t][s]), part[t], 0, 0, 0);
+                        part[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            xv, ZEROS ? u4x8_less_zero_to_bf16(wt[t][s], zero[t]) : u4x8_less8_to_bf16(wt[t][s]), part[t],
+                            0, 0, 0);
                 }
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
                     const float sc = __uint_as_float(sz[t][g] & 0xFFFF0000u);
-                    const float off = ZEROS ? (float)(sz[t][g] & 0xFFu) : 8.f;
-                    acc[t][0][0] = __builtin_fmaf(sc, __builtin_fmaf(-off, sx[0], part[t][0]), acc[t][0][0]);
+                    acc[t][0][0] = __builtin_fmaf(sc, part[t][0], acc[t][0][0]);
                     if (!four)
 #pragma unroll
-                        for (int v = 1; v < 4; ++v)
-                            acc[t][0][v] = __builtin_fmaf(sc, __builtin_fmaf(-off, sx[v], part[t][v]), acc[t][0][v]);
+                        for (int v = 1; v < 4; ++v) acc[t][0][v] = __builtin_fmaf(sc, part[t][v], acc[t][0][v]);
                 }
             }
         }
@@ -408,6 +428,8 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
             for (int w = 0; w < KW; ++w)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] += sums[w][t][from + i][e];
+            // (sums of 1/16 of the weights: what their subnormals lose, BF16 would too)
+            if constexpr (!ZEROS) v *= 16.f;
         } else {
             for (int w = 0; w < KW; ++w) v += sums[w][t][l];
         }

@@ -38,8 +38,10 @@ fp8_status launch_skinny(const fp8k::SkinnyParams& p, hipStream_t stream) {
 template <int FMT, bool GATED, int GROUP, bool ZEROS>
 fp8_status run_skinny(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
     const int64_t tiles = cdiv(p.N * (GATED ? 2 : 1), 16);
-    // six tiles spill registers where a tile takes most
-    constexpr bool kSix = FMT != fp8k::kSkinnyE4m3 && !(FMT == fp8k::kSkinnyInt4 && GROUP == 32 && ZEROS);
+    // Six tiles of E4M3 weights, read by pairs of lanes, spill registers.  One
+    // token x 24576 x 1536: six unpaired 17.5 us, four in pairs 19; x 7168 66 and
+    // 66, and the narrower weights gain by the pairs.
+    constexpr bool kSix = FMT != fp8k::kSkinnyE4m3;
     const int rt = GATED ? (kSix ? pick_tiles(tiles, cus, {1, 2, 4, 6}) : pick_tiles(tiles, cus, {1, 2, 4}))
                          : (kSix ? pick_tiles(tiles, cus, {1, 2, 3, 4, 6}) : pick_tiles(tiles, cus, {1, 2, 3, 4}));
     switch (rt) {

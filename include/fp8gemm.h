@@ -426,8 +426,11 @@ size_t fp8_gated_grad_workspace_size(int64_t M, int64_t N, int64_t K);
  *   group == FP8_W4_MXFP4: w = E2M1 * 2^(e-127), s = u32 [K/128][N] packed
  *     scale bytes, both as fp8_quant_mxfp4 writes them; z NULL.
  *   group 32, 64 or 128: w = s * (q - z), q = 0..15; s bf16 bits [K/group][N];
- *     z u8 [K/group][N] (values 0..15), or NULL for 8 everywhere.
- * Every product is exact, the sums are FP32, y is rounded once.
+ *     z u8 [K/group][N] (values 0..15: the low four bits count), or NULL for 8
+ *     everywhere.
+ * Every product x (q - z), or x w for MXFP4, is exact; the sums are FP32, y is
+ * rounded once.  MXFP4 weights of 2^128 and more (e >= 253) are infinite, and
+ * e = 255 is NaN.
  */
 fp8_status fp8_gemv_w4(const uint16_t* x, const uint8_t* w, const void* s,
                        const uint8_t* z, uint16_t* y, int64_t M, int64_t N,
