@@ -29,6 +29,7 @@ FLAG_FAST_ACCUM = 2
 PLAN_MX = 0x100
 PLAN_QOUT = 0x200
 ACT = {"silu": 0, "gelu": 1}
+GATED_OUTPUTS = {"h": 0, "save": 1, "quant": 2}
 W4_MXFP4 = 0
 CLIP_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 LAYOUT = {"dense": 0, "contiguous": 1, "masked": 2}
@@ -63,6 +64,7 @@ SYMBOLS = (
     "fp8_gated_nt",
     "fp8_gated_nt_qout",
     "fp8_gated_workspace_size",
+    "fp8_gated_plan",
     "fp8_gated_nt_grad",
     "fp8_gated_grad_workspace_size",
     "fp8_gemv_w4",
@@ -87,6 +89,14 @@ class GemmPlan(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class GatedPlan(ctypes.Structure):
+    """fp8_gated_plan_t: the kernels a call of the gated block launches."""
+    _fields_ = [("few_tokens", ctypes.c_int32), ("tile_m", ctypes.c_int32), ("tile_n", ctypes.c_int32),
+                ("k_splits", ctypes.c_int32), ("joined", ctypes.c_int32), ("tiles", ctypes.c_int64),
+                ("workspace_bytes", ctypes.c_size_t)]
+    as_dict = GemmPlan.as_dict
 
 
 class Fp8GemmError(RuntimeError):
@@ -128,6 +138,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fp8_gated_nt_qout.argtypes = [P] * 8 + [I64, I64, I64, I32, U32, P, ctypes.c_size_t, P]
     L.fp8_gated_workspace_size.argtypes = [I64, I64, I64, I32]
     L.fp8_gated_workspace_size.restype = ctypes.c_size_t
+    L.fp8_gated_plan.argtypes = [I64, I64, I64, I32, I32, ctypes.c_size_t, ctypes.POINTER(GatedPlan)]
     L.fp8_gated_nt_grad.argtypes = [P] * 9 + [I64, I64, I64, I32, P, ctypes.c_size_t, P]
     L.fp8_gated_grad_workspace_size.argtypes = [I64, I64, I64]
     L.fp8_gated_grad_workspace_size.restype = ctypes.c_size_t
@@ -142,7 +153,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                "fp8_gemm_plan",
                "fp8_gemm_nt_qout",
                "fp8_grouped_gemm_contiguous", "fp8_grouped_gemm_masked", "fp8_quant_mx",
-               "fp8_gemm_nt_mx", "fp8_quant_mxfp4", "fp8_gemm_nt_mx_w4", "fp8_gated_nt", "fp8_gated_nt_qout",
+               "fp8_gemm_nt_mx", "fp8_quant_mxfp4", "fp8_gemm_nt_mx_w4", "fp8_gated_nt", "fp8_gated_nt_qout", "fp8_gated_plan",
                "fp8_gated_nt_grad", "fp8_gemv_w4", "fp8_gated_gemv_w4", "fp8_quant_int4", "fp8_clip_grad_norm"):
         getattr(L, fn).restype = ctypes.c_int
     L.fp8_get_mk_alignment_for_contiguous_layout.argtypes = []
@@ -507,6 +518,18 @@ def _gated_workspace_size(M: int, N: int, K: int, outputs: int) -> int:
     if M <= 16 and outputs != 2:
         return 0            # one kernel, K split inside its workgroups
     return int(load_library().fp8_gated_workspace_size(M, N, K, outputs))
+
+
+def gated_plan(M: int, N: int, K: int, outputs: str = "h", compute_units: int = 256,
+               workspace_bytes: int | None = None) -> dict:
+    """The kernels gated_nt (outputs "h", or "save" with g and u) or
+    gated_nt_qout ("quant") launches for this shape (host-side arithmetic only;
+    no GPU needed), by default with all the workspace it can use."""
+    plan = GatedPlan()
+    nbytes = ctypes.c_size_t(-1).value if workspace_bytes is None else workspace_bytes
+    _check("fp8_gated_plan", load_library().fp8_gated_plan(M, N, K, GATED_OUTPUTS[outputs], compute_units, nbytes,
+                                                           ctypes.byref(plan)))
+    return plan.as_dict()
 
 
 def gated_nt(xq, sa, wgq, sbg, wuq, sbu, act: str = "silu", ue8m0: bool = False, save: bool = False, out=None,

@@ -98,6 +98,12 @@ GatedPlan gated_plan(int64_t M, int64_t N, int64_t K, int32_t outputs, bool may_
     return best;
 }
 
+// The plan of a call with ws_bytes of workspace.
+GatedPlan gated_plan_within(int64_t M, int64_t N, int64_t K, int32_t outputs, size_t ws_bytes, int cus) {
+    const GatedPlan pl = gated_plan(M, N, K, outputs, true, cus);
+    return pl.ws_bytes > ws_bytes ? gated_plan(M, N, K, outputs, false, cus) : pl;
+}
+
 template <int BM, int BN, int WM, int WN, bool POW2, int STAGES, bool QOUT = false>
 fp8_status launch_gated_tile(fp8k::GemmParams p, int64_t splits, int cus, hipStream_t stream) {
     p.m_tiles = (int)cdiv(p.M, BM);
@@ -166,8 +172,7 @@ fp8_status run_gated(fp8k::GemmParams& p, int32_t outputs, uint32_t flags, void*
     const fp8_status st = current_device_cus(&cus);
     if (st != FP8_OK) return st;
     const bool quant = outputs == kOutQuant, pow2 = flags & FP8_FLAG_UE8M0;
-    GatedPlan pl = gated_plan(p.M, p.N, p.K, outputs, true, cus);
-    if (pl.ws_bytes > ws_bytes) pl = gated_plan(p.M, p.N, p.K, outputs, false, cus);
+    const GatedPlan pl = gated_plan_within(p.M, p.N, p.K, outputs, ws_bytes, cus);
     if (pl.ws_bytes) p.part = static_cast<float*>(ws);
     if (pl.skinny) {
         fp8k::SkinnyParams q{};
@@ -312,6 +317,26 @@ size_t fp8_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t outputs
     int cus = 0;
     if (current_device_cus(&cus) != FP8_OK) return 0;
     return gated_plan(M, N, K, outputs, true, cus).ws_bytes;
+}
+
+fp8_status fp8_gated_plan(int64_t M, int64_t N, int64_t K, int32_t outputs, int32_t compute_units,
+                          size_t workspace_bytes, fp8_gated_plan_t* plan) {
+    if (!plan || !dims_ok(M) || !dims_ok(N) || !dims_ok(K) || outputs < kOutH || outputs > kOutQuant ||
+        compute_units <= 0)
+        return FP8_ERR_INVALID_ARG;
+    if (K % 128 || K == 0 || (outputs == kOutQuant && N % 128)) return FP8_ERR_SHAPE;
+    if (K > kMaxGemmK) return FP8_ERR_UNSUPPORTED;
+    *plan = fp8_gated_plan_t{};
+    if (M == 0 || N == 0) return FP8_OK;
+    const GatedPlan pl = gated_plan_within(M, N, K, outputs, workspace_bytes, compute_units);
+    plan->few_tokens = pl.skinny;
+    plan->tile_m = pl.skinny ? (int32_t)cdiv(M, 16) * 16 : kGatedTile[pl.tile].bm;
+    plan->tile_n = pl.skinny ? 8 * skinny_gated_e4m3_tiles(M, N, compute_units) : kGatedTile[pl.tile].cols;
+    plan->k_splits = (int32_t)pl.splits;
+    plan->joined = pl.ws_bytes != 0;
+    plan->tiles = cdiv(M, plan->tile_m) * cdiv(N, plan->tile_n);
+    plan->workspace_bytes = pl.ws_bytes;
+    return FP8_OK;
 }
 
 fp8_status fp8_gated_nt(const uint8_t* xq, const float* sa, const uint8_t* wgq, const float* sbg,

@@ -27,7 +27,9 @@ namespace fp8h {
 constexpr int64_t kMaxSkinnyM = 16;         // 4-bit weights
 constexpr int64_t kMaxSkinnyGatedM = 64;    // the gated block on E4M3 operands
 
-// Estimated time of the gated block on E4M3 operands, us.
+// 16-row weight tiles per workgroup (8 output columns each) and estimated time
+// (us) of the gated block on E4M3 operands.
+int skinny_gated_e4m3_tiles(int64_t M, int64_t N, int cus);
 double skinny_gated_e4m3_us(int64_t M, int64_t N, int64_t K, int cus);
 
 // The gated block on E4M3 operands; 4-bit matrix-vector products, plain and

@@ -38,12 +38,7 @@ fp8_status launch_skinny(const fp8k::SkinnyParams& p, hipStream_t stream) {
 template <int FMT, bool GATED, int GROUP, bool ZEROS>
 fp8_status run_skinny(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
     const int64_t tiles = cdiv(p.N * (GATED ? 2 : 1), 16);
-    // Six tiles of E4M3 weights, read by pairs of lanes, spill registers.  One
-    // token x 24576 x 1536: six unpaired 17.5 us, four in pairs 19; x 7168 66 and
-    // 66, and the narrower weights gain by the pairs.
-    constexpr bool kSix = FMT != fp8k::kSkinnyE4m3;
-    const int rt = GATED ? (kSix ? pick_tiles(tiles, cus, {1, 2, 4, 6}) : pick_tiles(tiles, cus, {1, 2, 4}))
-                         : (kSix ? pick_tiles(tiles, cus, {1, 2, 3, 4, 6}) : pick_tiles(tiles, cus, {1, 2, 3, 4}));
+    const int rt = GATED ? pick_tiles(tiles, cus, {1, 2, 4, 6}) : pick_tiles(tiles, cus, {1, 2, 3, 4, 6});
     switch (rt) {
         case 1: return launch_skinny<FMT, GATED, 1, GROUP, ZEROS>(p, stream);
         case 2: return launch_skinny<FMT, GATED, 2, GROUP, ZEROS>(p, stream);
@@ -51,9 +46,7 @@ fp8_status run_skinny(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) 
             if constexpr (!GATED) return launch_skinny<FMT, GATED, 3, GROUP, ZEROS>(p, stream);
             else return FP8_ERR_UNSUPPORTED;
         case 4: return launch_skinny<FMT, GATED, 4, GROUP, ZEROS>(p, stream);
-        default:
-            if constexpr (kSix) return launch_skinny<FMT, GATED, 6, GROUP, ZEROS>(p, stream);
-            else return FP8_ERR_UNSUPPORTED;
+        default: return launch_skinny<FMT, GATED, 6, GROUP, ZEROS>(p, stream);
     }
 }
 
@@ -78,21 +71,24 @@ fp8_status run_w4(const fp8k::SkinnyParams& p, int32_t group, int cus, hipStream
 
 namespace fp8h {
 
-// More than 16 tokens, in blocks of 16: each weight operand serves all blocks,
-// and with three or four blocks only two weight tiles fit the registers.  One
-// MI355X, gated E4M3, before x and the weights were read by pairs of lanes: 32 x
-// 7168 x 7168 4 tiles 27 us, 2 36; 64 x 7168 x 7168 2 tiles 47, 4 97; 37 x 2112
-// x 1536 2 tiles 6.4, 1 8.9.
-static int pick_block_tiles(int64_t tiles, int cus, int token_blocks) {
-    return token_blocks == 2 ? pick_tiles(tiles, cus, {1, 2, 4}) : pick_tiles(tiles, cus, {1, 2});
+// E4M3 weights.  Six tiles, read by pairs of lanes, spill registers (one token x
+// 24576 x 1536: six unpaired 17.5 us, four in pairs 19; x 7168 66 and 66; the
+// narrower weights gain by the pairs).  More than 16 tokens are taken in blocks
+// of 16: each weight operand serves all blocks, and with three or four blocks
+// only two weight tiles fit the registers.  One MI355X, gated E4M3, before x
+// and the weights were read by pairs of lanes: 32 x 7168 x 7168 4 tiles 27 us,
+// 2 36; 64 x 7168 x 7168 2 tiles 47, 4 97; 37 x 2112 x 1536 2 tiles 6.4, 1 8.9.
+int skinny_gated_e4m3_tiles(int64_t M, int64_t N, int cus) {
+    const int64_t tiles = cdiv(N * 2, 16);
+    return M <= 32 ? pick_tiles(tiles, cus, {1, 2, 4}) : pick_tiles(tiles, cus, {1, 2});
 }
 
 template <int MB>
 static fp8_status run_token_blocks(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
-    const int rt = pick_block_tiles(cdiv(p.N * 2, 16), cus, MB);
+    const int rt = skinny_gated_e4m3_tiles(p.M, p.N, cus);
     if (rt == 1) return launch_skinny<fp8k::kSkinnyE4m3, true, 1, 128, false, MB>(p, stream);
     if (rt == 2) return launch_skinny<fp8k::kSkinnyE4m3, true, 2, 128, false, MB>(p, stream);
-    if constexpr (MB == 2) return launch_skinny<fp8k::kSkinnyE4m3, true, 4, 128, false, MB>(p, stream);
+    if constexpr (MB <= 2) return launch_skinny<fp8k::kSkinnyE4m3, true, 4, 128, false, MB>(p, stream);
     else return FP8_ERR_UNSUPPORTED;
 }
 
@@ -101,15 +97,13 @@ static fp8_status run_token_blocks(const fp8k::SkinnyParams& p, int cus, hipStre
 // one MI355X to 1-64 x 512-24576 x 1536 and 7168, within 15% (64 x 512 x 1536
 // 5.5 us for 6.0, 64 x 2048 x 7168 14.5 for 14.2, 32 x 7168 x 7168 26.6 for 23.6).
 double skinny_gated_e4m3_us(int64_t M, int64_t N, int64_t K, int cus) {
-    const int64_t tiles = cdiv(N * 2, 16);
-    const int mb = (int)cdiv(M, 16);
-    const int rt = mb == 1 ? pick_tiles(tiles, cus, {1, 2, 4}) : pick_block_tiles(tiles, cus, mb);
-    return 3.0 + (double)(K / 128 * cdiv(cdiv(tiles, rt), cus)) * (0.015 * mb + rt * (0.05 + 0.024 * mb));
+    const int mb = (int)cdiv(M, 16), rt = skinny_gated_e4m3_tiles(M, N, cus);
+    return 3.0 + (double)(K / 128 * cdiv(cdiv(cdiv(N * 2, 16), rt), cus)) * (0.015 * mb + rt * (0.05 + 0.024 * mb));
 }
 
 fp8_status run_skinny_gated_e4m3(const fp8k::SkinnyParams& p, int cus, hipStream_t stream) {
     switch (cdiv(p.M, 16)) {
-        case 1: return run_skinny<fp8k::kSkinnyE4m3, true, 128, false>(p, cus, stream);
+        case 1: return run_token_blocks<1>(p, cus, stream);
         case 2: return run_token_blocks<2>(p, cus, stream);
         case 3: return run_token_blocks<3>(p, cus, stream);
         case 4: return run_token_blocks<4>(p, cus, stream);

@@ -375,6 +375,23 @@ fp8_status fp8_gated_nt(const uint8_t* xq, const float* sa, const uint8_t* wgq,
 size_t fp8_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t outputs);
 
 /*
+ * The kernels a fp8_gated_nt (outputs 0, 1) or fp8_gated_nt_qout (2) call
+ * launches, computed on the host from the shape, a compute-unit count and the
+ * workspace the call passes (no device needed).
+ */
+typedef struct {
+    int32_t few_tokens;     /* 1: the kernel built around the weights' stream; 0: the tile kernel */
+    int32_t tile_m, tile_n; /* rows and output columns of a workgroup (few tokens: M in whole 16s) */
+    int32_t k_splits;       /* workgroups along K per tile */
+    int32_t joined;         /* 1: a second kernel forms the outputs from FP32 sums */
+    int64_t tiles;
+    size_t workspace_bytes; /* of FP32 sums */
+} fp8_gated_plan_t;
+fp8_status fp8_gated_plan(int64_t M, int64_t N, int64_t K, int32_t outputs,
+                          int32_t compute_units, size_t workspace_bytes,
+                          fp8_gated_plan_t* plan);
+
+/*
  * fp8_gated_nt with h quantized for the next GEMM (the down projection), from
  * the FP32 values, as fp8_gemm_nt_qout does:
  *   hq u8 (M,N) E4M3 codes, sh fp32 [N/128][M] 1x128 scales; N % 128 == 0.
