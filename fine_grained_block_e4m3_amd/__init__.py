@@ -67,6 +67,7 @@ SYMBOLS = (
     "fp8_gated_plan",
     "fp8_gated_nt_grad",
     "fp8_gated_grad_workspace_size",
+    "fp8_gated_grad_plan",
     "fp8_gemv_w4",
     "fp8_gated_gemv_w4",
     "fp8_quant_int4",
@@ -96,6 +97,14 @@ class GatedPlan(ctypes.Structure):
     _fields_ = [("few_tokens", ctypes.c_int32), ("tile_m", ctypes.c_int32), ("tile_n", ctypes.c_int32),
                 ("k_splits", ctypes.c_int32), ("joined", ctypes.c_int32), ("tiles", ctypes.c_int64),
                 ("workspace_bytes", ctypes.c_size_t)]
+    as_dict = GemmPlan.as_dict
+
+
+class GatedGradPlan(ctypes.Structure):
+    """fp8_gated_grad_plan_t: the products a call of the gated block's gradient launches."""
+    _fields_ = [("dx_tile_n", ctypes.c_int32), ("dw_tile_n", ctypes.c_int32), ("dx_splits", ctypes.c_int32),
+                ("dw_splits", ctypes.c_int32), ("dw_first", ctypes.c_int32), ("dx_tiles", ctypes.c_int64),
+                ("dw_tiles", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
     as_dict = GemmPlan.as_dict
 
 
@@ -142,6 +151,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fp8_gated_nt_grad.argtypes = [P] * 9 + [I64, I64, I64, I32, P, ctypes.c_size_t, P]
     L.fp8_gated_grad_workspace_size.argtypes = [I64, I64, I64]
     L.fp8_gated_grad_workspace_size.restype = ctypes.c_size_t
+    L.fp8_gated_grad_plan.argtypes = [I64, I64, I64, I32, I32, I32, ctypes.POINTER(GatedGradPlan)]
     L.fp8_gemv_w4.argtypes = [P] * 5 + [I64, I64, I64, I32, P]
     L.fp8_gated_gemv_w4.argtypes = [P] * 8 + [I64, I64, I64, I32, I32, P]
     L.fp8_quant_int4.argtypes = [P, I64, I64, I32, P, P, P, P]
@@ -154,7 +164,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                "fp8_gemm_nt_qout",
                "fp8_grouped_gemm_contiguous", "fp8_grouped_gemm_masked", "fp8_quant_mx",
                "fp8_gemm_nt_mx", "fp8_quant_mxfp4", "fp8_gemm_nt_mx_w4", "fp8_gated_nt", "fp8_gated_nt_qout", "fp8_gated_plan",
-               "fp8_gated_nt_grad", "fp8_gemv_w4", "fp8_gated_gemv_w4", "fp8_quant_int4", "fp8_clip_grad_norm"):
+               "fp8_gated_grad_plan", "fp8_gated_nt_grad", "fp8_gemv_w4", "fp8_gated_gemv_w4", "fp8_quant_int4",
+               "fp8_clip_grad_norm"):
         getattr(L, fn).restype = ctypes.c_int
     L.fp8_get_mk_alignment_for_contiguous_layout.argtypes = []
     L.fp8_get_mk_alignment_for_contiguous_layout.restype = I32
@@ -600,6 +611,16 @@ def _grad_operands(dh, g, u, x, wg, wu):
         raise ValueError("gated_nt_grad: inconsistent operand shapes")
     _same_device(dh, g, u, x, wg, wu)
     return M, N, K
+
+
+def gated_grad_plan(M: int, N: int, K: int, need_dx: bool = True, need_dw: bool = True,
+                    compute_units: int = 256) -> dict:
+    """The products gated_nt_grad launches for this shape (host-side arithmetic
+    only; no GPU needed)."""
+    plan = GatedGradPlan()
+    _check("fp8_gated_grad_plan", load_library().fp8_gated_grad_plan(M, N, K, need_dx, need_dw, compute_units,
+                                                                     ctypes.byref(plan)))
+    return plan.as_dict()
 
 
 def gated_nt_grad(dh, g, u, x, wg, wu, act: str = "silu", need_dx: bool = True, need_dw: bool = True, out=None,

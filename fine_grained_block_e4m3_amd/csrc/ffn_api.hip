@@ -393,6 +393,25 @@ size_t fp8_gated_grad_workspace_size(int64_t M, int64_t N, int64_t K) {
     return most;
 }
 
+fp8_status fp8_gated_grad_plan(int64_t M, int64_t N, int64_t K, int32_t dx, int32_t dw, int32_t compute_units,
+                               fp8_gated_grad_plan_t* plan) {
+    if (!plan || !dims_ok(M) || !dims_ok(N) || !dims_ok(K) || compute_units <= 0) return FP8_ERR_INVALID_ARG;
+    if (K % 128) return FP8_ERR_SHAPE;
+    if (K > kMaxGemmK || N > kMaxGemmK - 64) return FP8_ERR_UNSUPPORTED;
+    *plan = fp8_gated_grad_plan_t{};
+    if (K == 0 || (!dx && !dw)) return FP8_OK;
+    const GradPlan pl = grad_plan(M, N, K, dx && M, dw && N, compute_units);
+    plan->dx_tile_n = pl.dx_wide ? 256 : 128;
+    plan->dw_tile_n = pl.dw_wide ? 256 : 128;
+    plan->dx_splits = (int32_t)pl.dx_splits;
+    plan->dw_splits = (int32_t)pl.dw_splits;
+    plan->dw_first = pl.dw_first;
+    plan->dx_tiles = pl.dx_tiles;
+    plan->dw_tiles = pl.dw_tiles;
+    plan->workspace_bytes = pl.bytes();
+    return FP8_OK;
+}
+
 fp8_status fp8_gated_nt_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, const uint16_t* x,
                              const uint16_t* wg, const uint16_t* wu, uint16_t* dx, uint16_t* dwg, uint16_t* dwu,
                              int64_t M, int64_t N, int64_t K, int32_t act, void* workspace, size_t workspace_bytes,

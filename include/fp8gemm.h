@@ -428,6 +428,22 @@ fp8_status fp8_gated_nt_grad(const uint16_t* dh, const uint16_t* g, const uint16
                              size_t workspace_bytes, void* stream);
 size_t fp8_gated_grad_workspace_size(int64_t M, int64_t N, int64_t K);
 
+/*
+ * The products a fp8_gated_nt_grad call launches, computed on the host from
+ * the shape, which results are wanted (dx, dw: 0 or 1) and a compute-unit
+ * count (no device needed).
+ */
+typedef struct {
+    int32_t dx_tile_n, dw_tile_n;   /* columns of a tile of 128 rows: 128 or 256 */
+    int32_t dx_splits, dw_splits;   /* workgroups along the contraction per tile */
+    int32_t dw_first;               /* 1: dW's tiles are started first */
+    int64_t dx_tiles, dw_tiles;     /* 0 where not wanted */
+    size_t workspace_bytes;
+} fp8_gated_grad_plan_t;
+fp8_status fp8_gated_grad_plan(int64_t M, int64_t N, int64_t K, int32_t dx,
+                               int32_t dw, int32_t compute_units,
+                               fp8_gated_grad_plan_t* plan);
+
 /* ---------------------------------------------------------------------------
  * Matrix-vector products with 4-bit weights and group scales, for up to 16
  * tokens (M <= 16, else FP8_ERR_SHAPE).
