@@ -742,11 +742,33 @@ def quant_int4(w: torch.Tensor, group: int = 128, symmetric: bool = False, out=N
     return q, s, z
 
 
+def _dims(t: torch.Tensor) -> list:
+    return [(stride, size) for stride, size in zip(t.stride(), t.shape) if size != 1]
+
+
+def _is_dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill a run of memory, in any order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    run = 1
+    for stride, size in sorted(_dims(t)):
+        if stride != run:
+            return False
+        run *= size
+    return True
+
+
+def _same_order(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two dense tensors hold their elements in one order."""
+    return a.is_contiguous() and b.is_contiguous() or _dims(a) == _dims(b)
+
+
 def clip_grad_norm(grads, max_norm: float, out=None, workspace=None) -> torch.Tensor:
-    """Scales the tensors of `grads` (fp32, bf16 or fp16, contiguous, any mix)
-    by min(1, max_norm / (norm + 1e-6)), norm being the 2-norm over all of
-    them, and returns norm (0-dim fp32, on the device).  In place unless `out`
-    gives one tensor of the same type and size per gradient."""
+    """Scales the tensors of `grads` (fp32, bf16 or fp16, any mix; dense, with
+    their dimensions in any order of memory) by min(1, max_norm / (norm +
+    1e-6)), norm being the 2-norm over all of them, and returns norm (0-dim
+    fp32, on the device).  In place unless `out` gives one tensor of the same
+    type, size and order of memory per gradient."""
     L = load_library()
     grads = list(grads)
     outs = grads if out is None else list(out)
@@ -765,10 +787,14 @@ def clip_grad_norm(grads, max_norm: float, out=None, workspace=None) -> torch.Te
     counts, devices = list(map(T.numel, both)), set(map(T.get_device, both))
     if len(devices) != 1 or -1 in devices:
         raise ValueError("clip_grad_norm: gradients must be GPU tensors of one device (no CPU path exists)")
-    if not all(map(T.is_contiguous, both)):
-        raise ValueError("clip_grad_norm: gradients must be contiguous")
     if outs is not grads and (types[:n] != types[n:] or counts[:n] != counts[n:]):
         raise ValueError("clip_grad_norm: out[i] must have the type and size of grads[i]")
+    if not all(map(T.is_contiguous, both)):
+        # any order of the dimensions, as long as out has the same
+        if not all(map(_is_dense, both)):
+            raise ValueError("clip_grad_norm: gradients must be dense (every element of their memory once)")
+        if outs is not grads and not all(map(_same_order, grads, outs)):
+            raise ValueError("clip_grad_norm: out[i] must have the strides of grads[i]")
     ptrs = array("q", map(T.data_ptr, both))
     sizes, kinds = array("q", counts), array("i", types)
     gp, sp, kp = ptrs.buffer_info()[0], sizes.buffer_info()[0], kinds.buffer_info()[0]
