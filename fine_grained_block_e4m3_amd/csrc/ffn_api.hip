@@ -287,6 +287,7 @@ fp8_status run_grad(fp8k::GatedGradParams& p, const GradPlan& pl, uint8_t* ws, h
 // Gradient clipping.
 // ---------------------------------------------------------------------------
 int64_t clip_chunks(int64_t n) { return cdiv(n, fp8k::kClipChunk); }
+constexpr int64_t kMaxClipChunks = (int64_t)1 << 30;     // per launch: counted in int32, a grid at a time
 int clip_grid(int64_t chunks) { return (int)(chunks < fp8k::kClipMaxGrid ? chunks : fp8k::kClipMaxGrid); }
 
 // Calls f(first tensor, tensors, chunks) for each batch of the call, or from
@@ -299,7 +300,7 @@ fp8_status clip_batches(const int64_t* sizes, int32_t count, bool backwards, F&&
         const int32_t k = count - i < fp8k::kClipBatch ? count - i : fp8k::kClipBatch;
         int64_t chunks = 0;
         for (int32_t j = 0; j < k; ++j) chunks += clip_chunks(sizes[i + j]);
-        if (chunks > 0x7FFFFFFF) return FP8_ERR_UNSUPPORTED;
+        if (chunks > kMaxClipChunks) return FP8_ERR_UNSUPPORTED;
         const fp8_status st = f(i, k, chunks);
         if (st != FP8_OK) return st;
     }
@@ -488,11 +489,12 @@ size_t fp8_clip_workspace_size(const int64_t* sizes, int32_t count) {
     if (count < 0 || (count && !sizes)) return 0;
     size_t slots = 0;
     for (int32_t i = 0; i < count; ++i)
-        if (sizes[i] < 0) return 0;
-    (void)clip_batches(sizes, count, false, [&](int32_t, int32_t, int64_t chunks) {
+        if (sizes[i] < 0 || sizes[i] > kMaxClipChunks * fp8k::kClipChunk) return 0;
+    const fp8_status st = clip_batches(sizes, count, false, [&](int32_t, int32_t, int64_t chunks) {
         slots += (size_t)clip_grid(chunks);
         return FP8_OK;
     });
+    if (st != FP8_OK) return 0;
     return 8 * (slots ? slots : 1);
 }
 
@@ -509,7 +511,10 @@ fp8_status fp8_clip_grad_norm(const void* const* grads, void* const* outs, const
     }
     if (((uintptr_t)norm & 3) || ((uintptr_t)workspace & 7)) return FP8_ERR_ALIGNMENT;
     if (!workspace) return FP8_ERR_INVALID_ARG;
-    if (workspace_bytes < fp8_clip_workspace_size(sizes, count)) return FP8_ERR_SCRATCH;
+    // (every batch is known to be one that can be launched before the first is)
+    const size_t need = fp8_clip_workspace_size(sizes, count);
+    if (need == 0) return FP8_ERR_UNSUPPORTED;
+    if (workspace_bytes < need) return FP8_ERR_SCRATCH;
     int cus = 0;
     fp8_status st = current_device_cus(&cus);
     if (st != FP8_OK) return st;

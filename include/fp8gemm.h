@@ -504,7 +504,9 @@ fp8_status fp8_quant_int4(const float* w, int64_t N, int64_t K, int32_t group,
  * overlaps nothing else.  norm: one FP32 on the device.  Squares are summed
  * in FP64 in a fixed order.  A NaN among the gradients makes the norm and all
  * outputs NaN; an infinity makes the factor 0.  The workspace is required:
- * fp8_clip_workspace_size() bytes, 8-byte aligned, else FP8_ERR_SCRATCH.
+ * fp8_clip_workspace_size() bytes, 8-byte aligned, else FP8_ERR_SCRATCH (the
+ * size is 0 for bad sizes, and where 120 tensors in turn hold more than 2^43
+ * elements, which is FP8_ERR_UNSUPPORTED).
  */
 fp8_status fp8_clip_grad_norm(const void* const* grads, void* const* outs,
                               const int64_t* sizes, const int32_t* types,
