@@ -65,8 +65,10 @@
 //     and odd subtiles of a wave hold g and u of the same 32 output columns
 //     in the same registers of the same lanes: the activation and the product
 //     are lane-local in the epilogue, and one X tile feeds both projections.
-//     Measured (one MI355X): 4096 x 2048 x 7168 storing h, g and u 196 us
-//     (1.22 PFLOP/s), 8192 x 4096 x 7168 quantized 731 us (1.32 PFLOP/s).
+//     Measured (one MI355X): 4096 x 2048 x 7168 storing h, g and u 193 us
+//     (1.25 PFLOP/s), 8192 x 4096 x 7168 quantized 727 us (1.32 PFLOP/s); on a
+//     card with a lower clock 202 and 768.  The 256 x 256 instances spill 5-10
+//     registers of a lane (24-44 bytes).
 #pragma once
 
 #include "gemm_common.h"

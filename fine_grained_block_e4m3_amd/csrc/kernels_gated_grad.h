@@ -22,11 +22,11 @@
 // rate, the tiles' traffic from L2), the weights and their gradients for few.
 // A workgroup of four waves has a 128 x 256 (or 128 x 128) tile and three
 // stages of 32 contraction steps; two (three) of them share a compute unit.
-// Measured (one MI355X, both kernels): 4096 x 2048 x 7168 425-446 us, 1.12
-// PFLOP/s in the products at a clock of about 1.8 GHz, LDS bank conflicts
-// in the results' pass only, L2 read at 13 TB/s; 500 x 2112 x 7168 91 us; 64 x 7168 x 7168 114 us
-// (450 MB of operands and results: 3.9 TB/s); 256 x 4096 x 7168 106 us; 777 x
-// 500 x 640 17 us.
+// Measured (one MI355X, both kernels): 4096 x 2048 x 7168 434 us (446 on
+// a card with a lower clock), 1.16 PFLOP/s in the products at a clock of about
+// 1.8 GHz, LDS bank conflicts in the results' pass only, L2 read at 13 TB/s;
+// 500 x 2112 x 7168 83-91 us; 64 x 7168 x 7168 114 us (450 MB of operands and
+// results: 3.9 TB/s); 256 x 4096 x 7168 107 us; 777 x 500 x 640 17 us.
 #pragma once
 
 #include "gated_common.h"

@@ -41,11 +41,13 @@
 // Measured (one MI355X, kernel time): gated E4M3 1 x 2048 x 7168 7.4 us
 // (29 MB: 4.0 TB/s, the launch's 2.3 us included), MXFP4 1 x 24576 x 7168
 // 21 us (4.4 TB/s) and 16 x 24576 x 7168 23 us; int4 1 and 16 x 24576 x 7168
-// with groups of 128 24 and 26.4 us, with zero points 26.3 and 28.7, with
+// with groups of 128 24 and 26 us, with zero points 26.3 and 28.7, with
 // groups of 64 and zero points 32.5 (16), with groups of 32 and zero points
 // 33.3 and 37.9; gated int4 (groups of 64, zero points) 3 x 2112 x 7168 10.8 us.
 // With z applied after the sum: 22.1 and 25.0, 22.7 and 25.5, 30.0, 31.4 and
-// 39.0; 9.8.
+// 39.0; 9.8.  That form with the weights as A for 4-bit integers too, four
+// scales and zero points per lane and group: groups of 128 24 and 29 (16 tokens,
+// zero points), of 32 45 and 51; gated 11.4.
 // Gated E4M3 with g and u stored as well: 1 x 2048 x 7168 7.6 us; with codes
 // instead (FP32 sums, then the joining kernel) 11, the tiles 16.6 and 17.2.
 #pragma once
@@ -486,7 +488,9 @@ __global__ __launch_bounds__(64 * KW) void skinny_kernel(SkinnyParams p) {
 // symmetric: s = BF16(amax / 7), z = 8; q = clamp(round(w / s) + z, 0, 15).
 // All roundings to nearest, ties to even, quotients correctly rounded; the
 // scale is at least BF16(1e-8), so a group of zeros is z everywhere.
-// One group per 8 lanes of 4 elements (group 32), 16 or 32 lanes; a stream.
+// One group per 8 lanes of 4 elements (group 32), 16 or 32 lanes; a stream:
+// 24576 x 7168 204-218 us, 7168 x 2048 20-24 (one MI355X: 3.7-3.9 and 2.8-3.4
+// TB/s; with zero points the slower ones).
 // ---------------------------------------------------------------------------
 template <int GROUP>
 __global__ __launch_bounds__(256) void quant_int4_kernel(const float* __restrict__ w, uint8_t* __restrict__ qd,

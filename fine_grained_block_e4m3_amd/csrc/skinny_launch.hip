@@ -71,9 +71,9 @@ fp8_status run_w4(const fp8k::SkinnyParams& p, int32_t group, int cus, hipStream
 
 namespace fp8h {
 
-// E4M3 weights.  Six tiles, read by pairs of lanes, spill registers (one token x
-// 24576 x 1536: six unpaired 17.5 us, four in pairs 19; x 7168 66 and 66; the
-// narrower weights gain by the pairs).  More than 16 tokens are taken in blocks
+// E4M3 weights.  Six tiles, read by pairs of lanes, spill 26 registers (one token
+// x 24576 x 7168 91 us, four tiles 66; x 1536 20.5 and 18.8, where six tiles
+// without the pairs took 17.5).  More than 16 tokens are taken in blocks
 // of 16: each weight operand serves all blocks, and with three or four blocks
 // only two weight tiles fit the registers.  One MI355X, gated E4M3, before x
 // and the weights were read by pairs of lanes: 32 x 7168 x 7168 4 tiles 27 us,
