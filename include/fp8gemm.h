@@ -462,8 +462,8 @@ fp8_status fp8_gated_grad_plan(int64_t M, int64_t N, int64_t K, int32_t dx,
  *     z u8 [K/group][N] (values 0..15: the low four bits count), or NULL for 8
  *     everywhere.
  * Every product x (q - z), or x w for MXFP4, is exact; the sums are FP32, y is
- * rounded once.  MXFP4 weights of 2^128 and more (e >= 253) are infinite, and
- * e = 255 is NaN.
+ * rounded once, and an infinite or NaN x gives what the definition gives.
+ * MXFP4 weights of 2^128 and more (e >= 253) are infinite, and e = 255 is NaN.
  */
 fp8_status fp8_gemv_w4(const uint16_t* x, const uint8_t* w, const void* s,
                        const uint8_t* z, uint16_t* y, int64_t M, int64_t N,
