@@ -11,13 +11,18 @@ Names follow the C ABI: ``quant_1x128``, ``quant_128x128``, ``gemm_nt``,
 ``grouped_gemm_contiguous``, ``grouped_gemm_masked``,
 ``get_mk_alignment_for_contiguous_layout``; the feed-forward operators
 ``gated_nt``, ``gated_nt_qout``, ``gated_nt_grad``, ``gemv_w4``,
-``gated_gemv_w4``, ``quant_int4``, ``clip_grad_norm``.
+``gated_gemv_w4``, ``quant_int4``, ``clip_grad_norm``; around the experts'
+products ``route_topk``, ``expert_sort``, ``expert_sort_masked``,
+``expert_dispatch``, ``expert_dispatch_quant``, ``expert_combine`` and their
+gradients; beside a shared projection ``adapter_rows``, ``add_adapters``.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 from array import array
+
+from typing import NamedTuple
 
 import torch
 
@@ -73,6 +78,19 @@ SYMBOLS = (
     "fp8_quant_int4",
     "fp8_clip_grad_norm",
     "fp8_clip_workspace_size",
+    "fp8_route_topk",
+    "fp8_route_topk_grad",
+    "fp8_expert_rows",
+    "fp8_expert_sort_workspace_size",
+    "fp8_expert_sort_contiguous",
+    "fp8_expert_sort_masked",
+    "fp8_expert_dispatch",
+    "fp8_expert_dispatch_quant",
+    "fp8_expert_combine",
+    "fp8_expert_combine_grad",
+    "fp8_add_adapters",
+    "fp8_adapters_workspace_size",
+    "fp8_adapters_plan",
     "fp8_get_mk_alignment_for_contiguous_layout",
     "fp8_status_string",
 )
@@ -105,6 +123,13 @@ class GatedGradPlan(ctypes.Structure):
     _fields_ = [("dx_tile_n", ctypes.c_int32), ("dw_tile_n", ctypes.c_int32), ("dx_splits", ctypes.c_int32),
                 ("dw_splits", ctypes.c_int32), ("dw_first", ctypes.c_int32), ("dx_tiles", ctypes.c_int64),
                 ("dw_tiles", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
+    as_dict = GemmPlan.as_dict
+
+
+class AdaptersPlan(ctypes.Structure):
+    """fp8_adapters_plan_t: the kernels a call of add_adapters launches."""
+    _fields_ = [("tiles", ctypes.c_int64), ("shared", ctypes.c_int32), ("k_splits", ctypes.c_int32),
+                ("k_range", ctypes.c_int64), ("n_range", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
     as_dict = GemmPlan.as_dict
 
 
@@ -159,13 +184,32 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fp8_clip_grad_norm.argtypes = [P, P, P, P, I32, ctypes.c_float, P, P, ctypes.c_size_t, P]
     L.fp8_clip_workspace_size.argtypes = [P, I32]
     L.fp8_clip_workspace_size.restype = ctypes.c_size_t
+    F32, SIZE = ctypes.c_float, ctypes.c_size_t
+    L.fp8_route_topk.argtypes = [P, I64, I32, I32, I32, I32, F32, P, P, P]
+    L.fp8_route_topk_grad.argtypes = [P, P, P, I64, I32, I32, I32, I32, F32, P, P]
+    L.fp8_expert_rows.argtypes = [I64, I32, I32]
+    L.fp8_expert_rows.restype = I64
+    L.fp8_expert_sort_workspace_size.argtypes = [I64, I32]
+    L.fp8_expert_sort_workspace_size.restype = SIZE
+    L.fp8_expert_sort_contiguous.argtypes = [P, I32, I64, I32, I32, I64, I32, P, P, P, P, P, SIZE, P]
+    L.fp8_expert_sort_masked.argtypes = [P, I32, I64, I32, I64, P, P, P, P, SIZE, P]
+    L.fp8_expert_dispatch.argtypes = [P, P, P, P, I64, I32, I64, I64, I32, P]
+    L.fp8_expert_dispatch_quant.argtypes = [P, P, P, P, I64, I32, I64, I64, I32, U32, P]
+    L.fp8_expert_combine.argtypes = [P, P, P, P, I64, I32, I64, I64, I32, P]
+    L.fp8_expert_combine_grad.argtypes = [P] * 7 + [I64, I32, I64, I64, I32, P]
+    L.fp8_add_adapters.argtypes = [P] * 8 + [I64, I64, I64, I32, I32, I64, P, SIZE, P]
+    L.fp8_adapters_workspace_size.argtypes = [I64, I64, I64, I32]
+    L.fp8_adapters_workspace_size.restype = SIZE
+    L.fp8_adapters_plan.argtypes = [I64, I64, I64, I32, I32, ctypes.POINTER(AdaptersPlan)]
     for fn in ("fp8_quant_1x128", "fp8_quant_128x128", "fp8_gemm_nt", "fp8_gemm_nt_ws", "fp8_gemm_nt_noalloc",
                "fp8_gemm_plan",
                "fp8_gemm_nt_qout",
                "fp8_grouped_gemm_contiguous", "fp8_grouped_gemm_masked", "fp8_quant_mx",
                "fp8_gemm_nt_mx", "fp8_quant_mxfp4", "fp8_gemm_nt_mx_w4", "fp8_gated_nt", "fp8_gated_nt_qout", "fp8_gated_plan",
                "fp8_gated_grad_plan", "fp8_gated_nt_grad", "fp8_gemv_w4", "fp8_gated_gemv_w4", "fp8_quant_int4",
-               "fp8_clip_grad_norm"):
+               "fp8_clip_grad_norm", "fp8_route_topk", "fp8_route_topk_grad", "fp8_expert_sort_contiguous",
+               "fp8_expert_sort_masked", "fp8_expert_dispatch", "fp8_expert_dispatch_quant", "fp8_expert_combine",
+               "fp8_expert_combine_grad", "fp8_add_adapters", "fp8_adapters_plan"):
         getattr(L, fn).restype = ctypes.c_int
     L.fp8_get_mk_alignment_for_contiguous_layout.argtypes = []
     L.fp8_get_mk_alignment_for_contiguous_layout.restype = I32
@@ -804,3 +848,292 @@ def clip_grad_norm(grads, max_norm: float, out=None, workspace=None) -> torch.Te
     _check("fp8_clip_grad_norm", L.fp8_clip_grad_norm(gp, op, sp, kp, n, float(max_norm), norm.data_ptr(), ws,
                                                       ws_bytes, _launch_stream(grads[0])))
     return norm
+
+
+# ---------------------------------------------------------------------------
+# Around the experts' products.
+# ---------------------------------------------------------------------------
+ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_I32 = torch.int32
+
+
+def _typed(t, name: str, ndim: int) -> int:
+    """Checks rows of fp32 or bf16 and returns their FP8_TYPE_*."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    kind = ROW_TYPES.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be fp32 or bf16, got {t.dtype}")
+    _need(t, name, t.dtype, ndim)
+    return kind
+
+
+def _shape(t, name: str, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _optional(t):
+    return None if t is None else t.data_ptr()
+
+
+def route_topk(logits, k: int, renormalize: bool = True, scale: float = 1.0, out=None):
+    """The k experts of each row of logits (T, E) fp32 or bf16 with the largest
+    logits (equal ones by index): (weights fp32 (T, k), ids int32 (T, k)).
+    weights = scale * softmax(logits)[ids], divided by their sum with
+    renormalize.  -inf masks an expert; ids are -1, with weight 0, where too
+    few are left."""
+    L = load_library()
+    kind = _typed(logits, "logits", 2)
+    T, E = logits.shape
+    if out is None:
+        w, ids = logits.new_empty((T, k), dtype=_F32), logits.new_empty((T, k), dtype=_I32)
+    else:
+        w, ids = _out(out[0], "out[0]", _F32, (T, k), logits), _out(out[1], "out[1]", _I32, (T, k), logits)
+    _check("fp8_route_topk", L.fp8_route_topk(logits.data_ptr(), T, E, k, kind, renormalize, scale, w.data_ptr(),
+                                              ids.data_ptr(), _launch_stream(logits)))
+    return w, ids
+
+
+def route_topk_grad(dweights, logits, ids, renormalize: bool = True, scale: float = 1.0, out=None) -> torch.Tensor:
+    """Gradient of route_topk's weights: dlogits (T, E) in the logits' type from
+    dweights fp32 (T, k) and the call's logits, ids, renormalize and scale."""
+    L = load_library()
+    kind = _typed(logits, "logits", 2)
+    _need(dweights, "dweights", _F32, 2)
+    _need(ids, "ids", _I32, 2)
+    T, E = logits.shape
+    k = ids.shape[1]
+    _shape(ids, "ids", (T, k))
+    _shape(dweights, "dweights", (T, k))
+    _same_device(logits, dweights, ids)
+    d = torch.empty_like(logits) if out is None else _out(out, "out", logits.dtype, (T, E), logits)
+    _check("fp8_route_topk_grad", L.fp8_route_topk_grad(
+        dweights.data_ptr(), logits.data_ptr(), ids.data_ptr(), T, E, k, kind, renormalize, scale, d.data_ptr(),
+        _launch_stream(logits)))
+    return d
+
+
+def _ids(ids) -> int:
+    """Checks expert (or adapter) indices of any shape and returns their bytes."""
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
+    _need(ids, "ids", ids.dtype, ids.dim())
+    return ids.element_size()
+
+
+def expert_rows(pairs: int, experts: int, align: int = 128) -> int:
+    """The most rows that `pairs` pairs take in the contiguous layout."""
+    rows = int(load_library().fp8_expert_rows(pairs, experts, align))
+    if rows < 0:
+        raise ValueError(f"expert_rows: bad sizes {(pairs, experts, align)}")
+    return rows
+
+
+def _sorted_out(out, shapes, like):
+    if out is None:
+        return [like.new_empty(shape, dtype=_I32) for shape in shapes]
+    if len(out) != len(shapes):
+        raise ValueError(f"out must hold {len(shapes)} tensors")
+    return [_out(t, f"out[{i}]", _I32, shape, like) for i, (t, shape) in enumerate(zip(out, shapes))]
+
+
+def expert_sort(ids, experts: int, align: int = 128, rows: int | None = None, keep: bool = False, out=None,
+                workspace=None):
+    """Rows of the contiguous layout for the experts ids (T, k) int32 or int64
+    of T tokens: (pos int32 (T, k), src int32 (rows), m_indices int32 (rows),
+    counts int32 (experts)).  pos is each pair's row (-1: none), src each row's
+    pair t * k + j (-1: none), m_indices what grouped_gemm_contiguous takes.
+    Pairs keep their order within an expert; ids outside [0, experts) have no
+    row, or with keep rows behind the experts', of m_indices -1.  rows: as many
+    as any choice can need, unless given (pairs that do not fit have none)."""
+    L = load_library()
+    size = _ids(ids)
+    n = ids.numel()
+    if rows is None:
+        rows = expert_rows(n, experts + 1 if keep else experts, align)
+    pos, src, m_indices, counts = _sorted_out(out, (tuple(ids.shape), (rows,), (rows,), (experts,)), ids)
+    ws, ws_bytes, held = _workspace(workspace, int(L.fp8_expert_sort_workspace_size(n, experts)), ids)
+    _check("fp8_expert_sort_contiguous", L.fp8_expert_sort_contiguous(
+        ids.data_ptr(), size, n, experts, align, rows, keep, pos.data_ptr(), src.data_ptr(), m_indices.data_ptr(),
+        counts.data_ptr(), ws, ws_bytes, _launch_stream(ids)))
+    return pos, src, m_indices, counts
+
+
+def expert_sort_masked(ids, experts: int, max_m: int, out=None, workspace=None):
+    """Rows of the masked layout for the experts ids (T, k): (pos int32 (T, k),
+    src int32 (experts * max_m), masked_m int32 (experts)).  A row is
+    e * max_m + rank; an expert's pairs from the max_m-th on have none."""
+    L = load_library()
+    size = _ids(ids)
+    n = ids.numel()
+    pos, src, masked_m = _sorted_out(out, (tuple(ids.shape), (experts * max_m,), (experts,)), ids)
+    ws, ws_bytes, held = _workspace(workspace, int(L.fp8_expert_sort_workspace_size(n, experts)), ids)
+    _check("fp8_expert_sort_masked", L.fp8_expert_sort_masked(
+        ids.data_ptr(), size, n, experts, max_m, pos.data_ptr(), src.data_ptr(), masked_m.data_ptr(), ws, ws_bytes,
+        _launch_stream(ids)))
+    return pos, src, masked_m
+
+
+def _pairs(pos, T: int, name: str = "pos") -> int:
+    _need(pos, name, _I32, 2)
+    if pos.shape[0] != T:
+        raise ValueError(f"{name} must have {T} rows, got {tuple(pos.shape)}")
+    return pos.shape[1]
+
+
+def expert_dispatch(x, pos, src, out=None) -> torch.Tensor:
+    """Tokens x (T, K) fp32 or bf16 to their experts' rows: xs (rows, K),
+    xs[pos[t, j]] = x[t].  src (rows) as the sort gives it: rows without a
+    pair become zeros.  Its gradient is expert_combine(dxs, pos)."""
+    L = load_library()
+    kind = _typed(x, "x", 2)
+    T, K = x.shape
+    k = _pairs(pos, T)
+    _need(src, "src", _I32, 1)
+    _same_device(x, pos, src)
+    rows = src.shape[0]
+    xs = x.new_empty((rows, K)) if out is None else _out(out, "out", x.dtype, (rows, K), x)
+    _check("fp8_expert_dispatch", L.fp8_expert_dispatch(x.data_ptr(), pos.data_ptr(), src.data_ptr(), xs.data_ptr(),
+                                                        T, k, rows, K, kind, _launch_stream(x)))
+    return xs
+
+
+def expert_dispatch_quant(x, pos, rows, ue8m0: bool = False, out=None):
+    """expert_dispatch with the rows quantized for a grouped GEMM: (xq uint8
+    (rows, K), sa fp32 (K/128, rows)), as quant_1x128 forms them.  rows: their
+    number, or (experts, max_m) for the masked layout, whose xq is (experts,
+    max_m, K).  Rows without a token stay as they are."""
+    L = load_library()
+    kind = _typed(x, "x", 2)
+    T, K = x.shape
+    k = _pairs(pos, T)
+    _same_device(x, pos)
+    shape = (rows, K) if isinstance(rows, int) else (*rows, K)
+    n = rows if isinstance(rows, int) else rows[0] * rows[1]
+    if out is None:
+        xq, sa = x.new_empty(shape, dtype=_U8), x.new_empty((K // 128, n), dtype=_F32)
+    else:
+        xq, sa = _out(out[0], "out[0]", _U8, shape, x), _out(out[1], "out[1]", _F32, (K // 128, n), x)
+    _check("fp8_expert_dispatch_quant", L.fp8_expert_dispatch_quant(
+        x.data_ptr(), pos.data_ptr(), xq.data_ptr(), sa.data_ptr(), T, k, n, K, kind, _flags(ue8m0),
+        _launch_stream(x)))
+    return xq, sa
+
+
+def _expert_rows_of(y, name: str):
+    """(type, rows, columns) of experts' rows: (rows, N), or (experts, max_m, N)."""
+    kind = _typed(y, name, 3 if isinstance(y, torch.Tensor) and y.dim() == 3 else 2)
+    return kind, y.shape[0] * (y.shape[1] if y.dim() == 3 else 1), y.shape[-1]
+
+
+def expert_combine(y, pos, weights=None, out=None) -> torch.Tensor:
+    """Experts' rows y ((rows, N), or (experts, max_m, N)) fp32 or bf16 back to
+    their tokens: out (T, N) = sum_j weights[t, j] * y[pos[t, j]] (weights fp32
+    (T, k), None: 1), in FP32 and rounded once.  Pairs without a row add
+    nothing."""
+    L = load_library()
+    kind, rows, N = _expert_rows_of(y, "y")
+    _need(pos, "pos", _I32, 2)
+    T, k = pos.shape
+    _same_device(y, pos)
+    if weights is not None:
+        _need(weights, "weights", _F32, 2)
+        _shape(weights, "weights", (T, k))
+        _same_device(y, weights)
+    o = y.new_empty((T, N)) if out is None else _out(out, "out", y.dtype, (T, N), y)
+    _check("fp8_expert_combine", L.fp8_expert_combine(y.data_ptr(), pos.data_ptr(), _optional(weights), o.data_ptr(),
+                                                      T, k, rows, N, kind, _launch_stream(y)))
+    return o
+
+
+def expert_combine_grad(dout, y, pos, weights=None, src=None, need_dy: bool = True, need_dw: bool = True, out=None):
+    """Gradient of expert_combine: (dy of y's shape and type, dweights fp32
+    (T, k)); None for what is not wanted.  dy[pos[t, j]] = weights[t, j] *
+    dout[t]; with src (rows) the rows without a pair are zeros, else they stay
+    as they are.  out: (dy, dweights) buffers."""
+    L = load_library()
+    kind, rows, N = _expert_rows_of(y, "y")
+    T, k = pos.shape if isinstance(pos, torch.Tensor) and pos.dim() == 2 else (-1, 0)
+    _need(pos, "pos", _I32, 2)
+    _need(dout, "dout", y.dtype, 2)
+    _shape(dout, "dout", (T, N))
+    _same_device(y, dout, pos)
+    if weights is not None:
+        _need(weights, "weights", _F32, 2)
+        _shape(weights, "weights", (T, k))
+        _same_device(y, weights)
+    if src is not None:
+        _need(src, "src", _I32, 1)
+        _shape(src, "src", (rows,))
+        _same_device(y, src)
+    if out is None:
+        dy = torch.empty_like(y) if need_dy else None
+        dw = pos.new_empty((T, k), dtype=_F32) if need_dw else None
+    else:
+        dy = _out(out[0], "out[0]", y.dtype, tuple(y.shape), y) if need_dy else None
+        dw = _out(out[1], "out[1]", _F32, (T, k), y) if need_dw else None
+    _check("fp8_expert_combine_grad", L.fp8_expert_combine_grad(
+        dout.data_ptr(), y.data_ptr(), pos.data_ptr(), _optional(weights), _optional(src), _optional(dy),
+        _optional(dw), T, k, rows, N, kind, _launch_stream(y)))
+    return dy, dw
+
+
+# ---------------------------------------------------------------------------
+# Adapters beside a shared projection.
+# ---------------------------------------------------------------------------
+class AdapterRows(NamedTuple):
+    """A batch's tokens sorted by adapter in tiles of 16 rows: src the token of
+    a row (-1: none), index its adapter (-1: none)."""
+    src: torch.Tensor
+    index: torch.Tensor
+
+
+def adapter_rows(ids, adapters: int, workspace=None) -> AdapterRows:
+    """The rows that add_adapters takes, once per batch for all its
+    projections: ids int32 or int64 (T), each token's adapter; one outside
+    [0, adapters) has none."""
+    _ids(ids)
+    if ids.dim() != 1:
+        raise ValueError(f"ids must have 1 dim, got {tuple(ids.shape)}")
+    _, src, index, _ = expert_sort(ids, adapters, align=16, keep=True, workspace=workspace)
+    return AdapterRows(src, index)
+
+
+def adapters_plan(rows: int, N: int, K: int, R: int, compute_units: int = 256) -> dict:
+    """The kernels add_adapters launches for this many rows (host-side
+    arithmetic only; no GPU needed)."""
+    plan = AdaptersPlan()
+    _check("fp8_adapters_plan", load_library().fp8_adapters_plan(rows, N, K, R, compute_units, ctypes.byref(plan)))
+    return plan.as_dict()
+
+
+def add_adapters(x, a, b, scale, rows: AdapterRows, y, out=None, workspace=None) -> torch.Tensor:
+    """A projection's result y (T, N) bf16 with each token's adapter added:
+    out[t] = y[t] + scale[i] * (x[t] a[i]^T) b[i]^T.  x (T, K), a (L, R, K),
+    b (L, N, R) bf16, scale fp32 (L), rows from adapter_rows(ids, L).  Tokens
+    without an adapter take y as it is.  out may be y."""
+    L = load_library()
+    _need(x, "x", _BF16, 2)
+    _need(a, "a", _BF16, 3)
+    _need(b, "b", _BF16, 3)
+    _need(scale, "scale", _F32, 1)
+    _need(y, "y", _BF16, 2)
+    src, index = rows
+    _need(src, "rows.src", _I32, 1)
+    _need(index, "rows.index", _I32, 1)
+    T, K = x.shape
+    n, R, _ = a.shape
+    N = y.shape[1]
+    if a.shape[2] != K or b.shape != (n, N, R) or scale.shape[0] != n or y.shape[0] != T or index.shape != src.shape:
+        raise ValueError("add_adapters: inconsistent operand shapes")
+    _same_device(x, a, b, scale, src, index, y)
+    o = torch.empty_like(y) if out is None else _out(out, "out", _BF16, (T, N), x)
+    nrows = src.shape[0]
+    ws, ws_bytes, held = _workspace(workspace, int(L.fp8_adapters_workspace_size(nrows, N, K, R)), x)
+    _check("fp8_add_adapters", L.fp8_add_adapters(
+        x.data_ptr(), a.data_ptr(), b.data_ptr(), scale.data_ptr(), src.data_ptr(), index.data_ptr(), y.data_ptr(),
+        o.data_ptr(), T, N, K, n, R, nrows, ws, ws_bytes, _launch_stream(x)))
+    return o

@@ -17,7 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8gemm.so")
-SOURCES = [os.path.join(CSRC, name) for name in ("fp8gemm_api.hip", "ffn_api.hip", "skinny_launch.hip")]
+SOURCES = [os.path.join(CSRC, name) for name in ("fp8gemm_api.hip", "ffn_api.hip", "skinny_launch.hip", "routing_api.hip")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

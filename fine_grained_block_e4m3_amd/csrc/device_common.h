@@ -65,6 +65,35 @@ __device__ __forceinline__ float group_scale(float amax, bool pow2) {
     return s;
 }
 
+// E4M3 codes of the correctly rounded quotients v[i] / s, with r the
+// correctly rounded 1 / s.  The product v[i] * r carries two roundings of
+// relative error at most 2^-24 each, so it lies within 2 units in the last
+// place of the exact quotient and within 2.5 of the correctly rounded one
+// (5 units of the lower binade where the two straddle a power of two).  The
+// conversion to E4M3 (round to nearest even, saturating) is monotone in the
+// magnitude: when the magnitudes 8 units below and 8 above the product take
+// the same code, every value between them does, the correctly rounded
+// quotient included, and the product's code (its sign is the quotient's) is
+// the answer.  Otherwise -- a product within 8 units of a rounding boundary,
+// about 2e-5 of random inputs -- the four quotients are divided.  With a
+// power-of-two scale the product is the quotient itself.
+template <bool POW2>
+__device__ __forceinline__ uint32_t cvt_e4m3x4_quot(f32x4 v, float s, float r) {
+    const float q0 = v[0] * r, q1 = v[1] * r, q2 = v[2] * r, q3 = v[3] * r;
+    if constexpr (POW2) {
+        return cvt_e4m3x4(q0, q1, q2, q3);
+    } else {
+        const uint32_t a0 = __float_as_uint(q0) & 0x7FFFFFFFu, a1 = __float_as_uint(q1) & 0x7FFFFFFFu;
+        const uint32_t a2 = __float_as_uint(q2) & 0x7FFFFFFFu, a3 = __float_as_uint(q3) & 0x7FFFFFFFu;
+        auto below = [](uint32_t a) { return __uint_as_float(a > 8u ? a - 8u : 0u); };
+        auto above = [](uint32_t a) { return __uint_as_float(a + 8u); };
+        const uint32_t lo = cvt_e4m3x4(below(a0), below(a1), below(a2), below(a3));
+        const uint32_t hi = cvt_e4m3x4(above(a0), above(a1), above(a2), above(a3));
+        if (lo == hi) return cvt_e4m3x4(q0, q1, q2, q3);
+        return cvt_e4m3x4(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
+    }
+}
+
 // Biased exponent byte of an FP32 scale: its E8M0 encoding when the scale is
 // a power of two.
 __device__ __forceinline__ int e8m0_of(float s) {

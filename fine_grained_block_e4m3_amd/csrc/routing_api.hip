@@ -1,0 +1,401 @@
+// routing_api.hip -- host side of the operators around the experts' products
+// and the shared projection (declared in include/fp8gemm.h): the router's
+// choice, tokens sorted by expert and back with their gradients, low-rank
+// adapters.
+//
+// As in fp8gemm_api.hip every entry point validates on the host, enqueues
+// nothing on an error, launches on the caller's stream, and neither
+// allocates, frees nor synchronizes.
+#include <algorithm>
+
+#include "host_common.h"
+#include "kernels_adapter.h"
+#include "kernels_expert.h"
+#include "kernels_route.h"
+
+namespace {
+
+using namespace fp8h;
+
+constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+
+bool row_type_ok(int32_t t) { return t == FP8_TYPE_F32 || t == FP8_TYPE_BF16; }
+size_t type_size(int32_t t) { return t == FP8_TYPE_F32 ? 4 : 2; }
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// ---------------------------------------------------------------------------
+// The router.
+// ---------------------------------------------------------------------------
+constexpr int kMaxRouteE = 1024, kMaxRouteK = 64;
+
+fp8_status check_route(int64_t T, int32_t E, int32_t k, int32_t type) {
+    if (!dims_ok(T) || E < 1 || k < 1 || !row_type_ok(type)) return FP8_ERR_INVALID_ARG;
+    if (k > E) return FP8_ERR_SHAPE;
+    if (E > kMaxRouteE || k > kMaxRouteK) return FP8_ERR_UNSUPPORTED;
+    return FP8_OK;
+}
+
+template <typename T, bool GRAD>
+void launch_route(fp8k::RouteParams& p, hipStream_t s) {
+    const dim3 grid((unsigned)cdiv(p.T, 4)), block(256);
+    auto go = [&](auto kernel, int per) {
+        // a lane's `per` logits in one load: rows and lanes at multiples of it
+        const size_t bytes = std::min<size_t>(per * sizeof(T), 16);
+        p.vec = p.E % per == 0 && aligned(p.logits, bytes) && (!GRAD || aligned(p.dlogits, bytes));
+        hipLaunchKernelGGL(kernel, grid, block, 0, s, p);
+    };
+    auto pick = [&](auto choice, auto grad, int per) {
+        if constexpr (GRAD) go(grad, per);
+        else go(choice, per);
+    };
+    if (p.E <= 64) pick(fp8k::route_topk_kernel<T, 1>, fp8k::route_grad_kernel<T, 1>, 1);
+    else if (p.E <= 128) pick(fp8k::route_topk_kernel<T, 2>, fp8k::route_grad_kernel<T, 2>, 2);
+    else if (p.E <= 256) pick(fp8k::route_topk_kernel<T, 4>, fp8k::route_grad_kernel<T, 4>, 4);
+    else if (p.E <= 512) pick(fp8k::route_topk_kernel<T, 8>, fp8k::route_grad_kernel<T, 8>, 8);
+    else pick(fp8k::route_topk_kernel<T, 16>, fp8k::route_grad_kernel<T, 16>, 16);
+}
+
+// ---------------------------------------------------------------------------
+// The sort.
+// ---------------------------------------------------------------------------
+// One workgroup counts and places alone while its pairs are few; then chunks
+// are counted by a first kernel, at most kMaxSortChunks, since every workgroup
+// adds up all chunks' counts.
+constexpr int64_t kSortAlone = 8192, kSortChunk = 2048, kMaxSortChunks = 256;
+
+int64_t sort_chunk(int64_t pairs) {
+    if (pairs <= kSortAlone) return std::max<int64_t>(pairs, 1);
+    return std::max(kSortChunk, cdiv(pairs, kMaxSortChunks));
+}
+int64_t sort_chunks(int64_t pairs) { return std::max<int64_t>(cdiv(pairs, sort_chunk(pairs)), 1); }
+
+fp8_status check_sort(int64_t pairs, int32_t E, int32_t id_bytes) {
+    if (!dims_ok(pairs) || E < 1 || !(id_bytes == 4 || id_bytes == 8)) return FP8_ERR_INVALID_ARG;
+    if (E > fp8k::kSortMaxExperts || pairs > kMaxDim / 2) return FP8_ERR_UNSUPPORTED;
+    return FP8_OK;
+}
+
+fp8_status run_sort(fp8k::SortParams& p, void* ws, size_t ws_bytes, hipStream_t s) {
+    const int64_t chunks = sort_chunks(p.pairs);
+    if (ws_bytes && !ws) return FP8_ERR_INVALID_ARG;
+    if (!aligned(ws, 4)) return FP8_ERR_ALIGNMENT;
+    if (chunks > 1 && ws_bytes < (size_t)(chunks * p.bins) * sizeof(int32_t)) return FP8_ERR_SCRATCH;
+    int cus = 0;
+    const fp8_status st = current_device_cus(&cus);
+    if (st != FP8_OK) return st;
+    p.chunk = sort_chunk(p.pairs);
+    p.hist = static_cast<int32_t*>(ws);
+    const dim3 grid((unsigned)chunks), block(fp8k::kSortThreads);
+    if (chunks > 1) {
+        hipLaunchKernelGGL(fp8k::expert_count_kernel, grid, block, 0, s, p);
+        const fp8_status run = launch_status();
+        if (run != FP8_OK) return run;
+    }
+    hipLaunchKernelGGL(fp8k::expert_place_kernel, grid, block, 0, s, p);
+    return launch_status();
+}
+
+// ---------------------------------------------------------------------------
+// Rows.
+// ---------------------------------------------------------------------------
+fp8_status check_rows(int64_t T, int32_t k, int64_t rows, int64_t W, int32_t type) {
+    if (!dims_ok(T) || !dims_ok(rows) || !dims_ok(W) || k < 1 || !row_type_ok(type)) return FP8_ERR_INVALID_ARG;
+    if (T * k >= kMaxDim) return FP8_ERR_UNSUPPORTED;
+    return FP8_OK;
+}
+
+// Waves (4 a workgroup) that move rows, and those that look for rows to clear.
+fp8_status rows_grid(fp8k::RowsParams& p, int64_t per_seg, dim3* grid) {
+    p.segs = cdiv(p.W, per_seg);
+    p.work = p.T * p.segs;
+    const int64_t waves = p.work + (p.src ? cdiv(p.rows, fp8k::kClearRows) : 0);
+    if (cdiv(waves, 4) > kMaxGrid) return FP8_ERR_UNSUPPORTED;
+    *grid = dim3((unsigned)cdiv(waves, 4));
+    return FP8_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Adapters.
+// ---------------------------------------------------------------------------
+struct AdapterPlan {
+    bool share;                 // a workgroup's waves take tiles of their own, else parts of one
+    int64_t tiles, splits, k_range, n_range;
+    size_t bytes(int64_t R) const { return (size_t)(splits * tiles * 16 * R) * sizeof(float); }
+};
+
+AdapterPlan adapter_plan(int64_t rows, int64_t N, int64_t K, int cus) {
+    AdapterPlan pl{};
+    pl.tiles = rows / 16;
+    pl.share = pl.tiles >= 8 * cus;
+    const int64_t wgs = std::max<int64_t>(pl.share ? cdiv(pl.tiles, 4) : pl.tiles, 1), step = pl.share ? 128 : 512;
+    pl.splits = std::clamp(cdiv(4 * cus, wgs), (int64_t)1, std::max<int64_t>(K / step, 1));
+    pl.k_range = cdiv(cdiv(K, pl.splits), step) * step;
+    pl.splits = cdiv(K, pl.k_range);
+    const int64_t cols = pl.share ? 64 : 256;
+    const int64_t parts = std::clamp(cdiv(4 * cus, wgs), (int64_t)1, std::max<int64_t>(cdiv(N, cols), 1));
+    pl.n_range = std::max(cdiv(cdiv(N, parts), cols), (int64_t)1) * cols;
+    return pl;
+}
+
+fp8_status check_adapters(int64_t T, int64_t N, int64_t K, int32_t L, int32_t R, int64_t rows) {
+    if (!dims_ok(T) || !dims_ok(N) || !dims_ok(K) || !dims_ok(rows) || L < 1 || R < 1) return FP8_ERR_INVALID_ARG;
+    if (K % 128 || K == 0 || R % 8 || rows % 16) return FP8_ERR_SHAPE;
+    if (R > fp8k::kAdapterMaxR || K > kMaxGemmK) return FP8_ERR_UNSUPPORTED;
+    return FP8_OK;
+}
+
+template <int RT>
+void launch_adapter_down(const fp8k::AdapterParams& p, bool share, hipStream_t s) {
+    if (share) hipLaunchKernelGGL((fp8k::adapter_down_kernel<RT, 1>), dim3((unsigned)cdiv(p.tiles, 4), (unsigned)p.splits), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((fp8k::adapter_down_kernel<RT, 4>), dim3((unsigned)p.tiles, (unsigned)p.splits), dim3(256), 0, s, p);
+}
+template <int RS>
+void launch_adapter_up(const fp8k::AdapterParams& p, bool share, hipStream_t s) {
+    const unsigned parts = (unsigned)cdiv(p.N, p.n_range);
+    if (share) hipLaunchKernelGGL((fp8k::adapter_up_kernel<RS, true>), dim3((unsigned)cdiv(p.tiles, 4), parts), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((fp8k::adapter_up_kernel<RS, false>), dim3((unsigned)p.tiles, parts), dim3(256), 0, s, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8_status fp8_route_topk(const void* logits, int64_t T, int32_t E, int32_t k, int32_t type, int32_t renormalize,
+                          float scale, float* weights, int32_t* ids, void* stream) {
+    const fp8_status st = check_route(T, E, k, type);
+    if (st != FP8_OK) return st;
+    if (T == 0) return FP8_OK;
+    if (!logits || !weights || !ids) return FP8_ERR_INVALID_ARG;
+    if (!aligned(logits, type_size(type)) || !aligned(weights, 4) || !aligned(ids, 4)) return FP8_ERR_ALIGNMENT;
+    int cus = 0;
+    const fp8_status dev = current_device_cus(&cus);
+    if (dev != FP8_OK) return dev;
+    fp8k::RouteParams p{};
+    p.logits = logits; p.w = weights; p.ids = ids;
+    p.T = T; p.E = E; p.k = k; p.scale = scale; p.renorm = renormalize != 0;
+    if (type == FP8_TYPE_F32) launch_route<float, false>(p, (hipStream_t)stream);
+    else launch_route<uint16_t, false>(p, (hipStream_t)stream);
+    return launch_status();
+}
+
+fp8_status fp8_route_topk_grad(const float* dweights, const void* logits, const int32_t* ids, int64_t T, int32_t E,
+                               int32_t k, int32_t type, int32_t renormalize, float scale, void* dlogits,
+                               void* stream) {
+    const fp8_status st = check_route(T, E, k, type);
+    if (st != FP8_OK) return st;
+    if (T == 0) return FP8_OK;
+    if (!dweights || !logits || !ids || !dlogits) return FP8_ERR_INVALID_ARG;
+    if (!aligned(logits, type_size(type)) || !aligned(dlogits, type_size(type)) || !aligned(dweights, 4) || !aligned(ids, 4))
+        return FP8_ERR_ALIGNMENT;
+    int cus = 0;
+    const fp8_status dev = current_device_cus(&cus);
+    if (dev != FP8_OK) return dev;
+    fp8k::RouteParams p{};
+    p.logits = logits; p.ids = const_cast<int32_t*>(ids); p.dw = dweights; p.dlogits = dlogits;
+    p.T = T; p.E = E; p.k = k; p.scale = scale; p.renorm = renormalize != 0;
+    if (type == FP8_TYPE_F32) launch_route<float, true>(p, (hipStream_t)stream);
+    else launch_route<uint16_t, true>(p, (hipStream_t)stream);
+    return launch_status();
+}
+
+int64_t fp8_expert_rows(int64_t pairs, int32_t E, int32_t align) {
+    if (pairs < 0 || pairs > kMaxDim / 2 || E < 1 || align < 1) return -1;
+    return (pairs + std::min<int64_t>(E, pairs) * (align - 1)) / align * align;
+}
+
+size_t fp8_expert_sort_workspace_size(int64_t pairs, int32_t E) {
+    if (check_sort(pairs, E, 4) != FP8_OK) return 0;
+    const int64_t chunks = sort_chunks(pairs);
+    return chunks > 1 ? (size_t)(chunks * (E + 1)) * sizeof(int32_t) : 0;
+}
+
+fp8_status fp8_expert_sort_contiguous(const void* ids, int32_t id_bytes, int64_t pairs, int32_t E, int32_t align,
+                                      int64_t rows, int32_t keep, int32_t* pos, int32_t* src, int32_t* m_indices,
+                                      int32_t* counts, void* workspace, size_t workspace_bytes, void* stream) {
+    const fp8_status st = check_sort(pairs, E, id_bytes);
+    if (st != FP8_OK) return st;
+    if (!dims_ok(rows) || align < 1 || align > 1024 || (align & (align - 1))) return FP8_ERR_INVALID_ARG;
+    if ((pairs && (!ids || !pos)) || (rows && (!src || !m_indices)) || !counts) return FP8_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)pos, (const void*)src, (const void*)m_indices, (const void*)counts})
+        if (!aligned(q, 4)) return FP8_ERR_ALIGNMENT;
+    if (!aligned(ids, id_bytes)) return FP8_ERR_ALIGNMENT;
+    fp8k::SortParams p{};
+    p.ids = ids; p.pos = pos; p.src = src; p.m_indices = m_indices; p.counts = counts; p.contiguous = true;
+    p.pairs = pairs; p.rows = rows; p.E = E; p.bins = keep ? E + 1 : E; p.align = align; p.wide = id_bytes == 8;
+    return run_sort(p, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+fp8_status fp8_expert_sort_masked(const void* ids, int32_t id_bytes, int64_t pairs, int32_t E, int64_t max_m,
+                                  int32_t* pos, int32_t* src, int32_t* masked_m, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    const fp8_status st = check_sort(pairs, E, id_bytes);
+    if (st != FP8_OK) return st;
+    if (!dims_ok(max_m)) return FP8_ERR_INVALID_ARG;
+    if (E * max_m > kMaxDim / 2) return FP8_ERR_UNSUPPORTED;
+    if ((pairs && (!ids || !pos)) || (max_m && !src) || !masked_m) return FP8_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)pos, (const void*)src, (const void*)masked_m})
+        if (!aligned(q, 4)) return FP8_ERR_ALIGNMENT;
+    if (!aligned(ids, id_bytes)) return FP8_ERR_ALIGNMENT;
+    fp8k::SortParams p{};
+    p.ids = ids; p.pos = pos; p.src = src; p.counts = masked_m;
+    p.pairs = pairs; p.rows = E * max_m; p.E = E; p.bins = E; p.align = 1; p.max_m = max_m; p.wide = id_bytes == 8;
+    return run_sort(p, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+fp8_status fp8_expert_dispatch(const void* x, const int32_t* pos, const int32_t* src, void* xs, int64_t T, int32_t k,
+                               int64_t rows, int64_t K, int32_t type, void* stream) {
+    const fp8_status st = check_rows(T, k, rows, K, type);
+    if (st != FP8_OK) return st;
+    if (rows == 0 || K == 0 || (T == 0 && !src)) return FP8_OK;
+    if ((T && (!x || !pos)) || !xs) return FP8_ERR_INVALID_ARG;
+    if (!aligned(x, type_size(type)) || !aligned(xs, type_size(type)) || !aligned(pos, 4) || !aligned(src, 4))
+        return FP8_ERR_ALIGNMENT;
+    int cus = 0;
+    const fp8_status dev = current_device_cus(&cus);
+    if (dev != FP8_OK) return dev;
+    fp8k::RowsParams p{};
+    p.x = x; p.out = xs; p.pos = pos; p.src = src; p.T = T; p.rows = rows; p.W = K; p.k = k;
+    dim3 grid;
+    const fp8_status g = rows_grid(p, 64 * fp8k::kRowVecs * 16 / (int64_t)type_size(type), &grid);
+    if (g != FP8_OK) return g;
+    if (type == FP8_TYPE_F32) hipLaunchKernelGGL(fp8k::expert_dispatch_kernel<float>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    else hipLaunchKernelGGL(fp8k::expert_dispatch_kernel<uint16_t>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    return launch_status();
+}
+
+fp8_status fp8_expert_dispatch_quant(const void* x, const int32_t* pos, uint8_t* xq, float* sa, int64_t T, int32_t k,
+                                     int64_t rows, int64_t K, int32_t type, uint32_t flags, void* stream) {
+    const fp8_status st = check_rows(T, k, rows, K, type);
+    if (st != FP8_OK) return st;
+    if (flags & ~FP8_FLAG_UE8M0) return FP8_ERR_INVALID_ARG;
+    if (K % 128) return FP8_ERR_SHAPE;
+    if (T == 0 || rows == 0 || K == 0) return FP8_OK;
+    if (!x || !pos || !xq || !sa) return FP8_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(xq) || !aligned16(sa) || !aligned(pos, 4)) return FP8_ERR_ALIGNMENT;
+    int cus = 0;
+    const fp8_status dev = current_device_cus(&cus);
+    if (dev != FP8_OK) return dev;
+    fp8k::RowsParams p{};
+    p.x = x; p.out = xq; p.sa = sa; p.pos = pos; p.T = T; p.rows = rows; p.W = K; p.k = k;
+    dim3 grid;
+    const fp8_status g = rows_grid(p, 1024, &grid);
+    if (g != FP8_OK) return g;
+    const hipStream_t s = (hipStream_t)stream;
+    const bool pow2 = flags & FP8_FLAG_UE8M0;
+    if (type == FP8_TYPE_F32) {
+        if (pow2) hipLaunchKernelGGL((fp8k::expert_dispatch_quant_kernel<float, true>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((fp8k::expert_dispatch_quant_kernel<float, false>), grid, dim3(256), 0, s, p);
+    } else {
+        if (pow2) hipLaunchKernelGGL((fp8k::expert_dispatch_quant_kernel<uint16_t, true>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((fp8k::expert_dispatch_quant_kernel<uint16_t, false>), grid, dim3(256), 0, s, p);
+    }
+    return launch_status();
+}
+
+fp8_status fp8_expert_combine(const void* y, const int32_t* pos, const float* weights, void* out, int64_t T,
+                              int32_t k, int64_t rows, int64_t N, int32_t type, void* stream) {
+    const fp8_status st = check_rows(T, k, rows, N, type);
+    if (st != FP8_OK) return st;
+    if (T == 0 || N == 0) return FP8_OK;
+    if ((rows && !y) || !pos || !out) return FP8_ERR_INVALID_ARG;
+    if (!aligned(y, type_size(type)) || !aligned(out, type_size(type)) || !aligned(pos, 4) || !aligned(weights, 4))
+        return FP8_ERR_ALIGNMENT;
+    int cus = 0;
+    const fp8_status dev = current_device_cus(&cus);
+    if (dev != FP8_OK) return dev;
+    fp8k::RowsParams p{};
+    p.x = y; p.out = out; p.pos = pos; p.w = weights; p.T = T; p.rows = rows; p.W = N; p.k = k;
+    dim3 grid;
+    const fp8_status g = rows_grid(p, 64 * fp8k::kCombineVecs * 16 / (int64_t)type_size(type), &grid);
+    if (g != FP8_OK) return g;
+    if (type == FP8_TYPE_F32) hipLaunchKernelGGL(fp8k::expert_combine_kernel<float>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    else hipLaunchKernelGGL(fp8k::expert_combine_kernel<uint16_t>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    return launch_status();
+}
+
+fp8_status fp8_expert_combine_grad(const void* dout, const void* y, const int32_t* pos, const float* weights,
+                                   const int32_t* src, void* dy, float* dweights, int64_t T, int32_t k, int64_t rows,
+                                   int64_t N, int32_t type, void* stream) {
+    const fp8_status st = check_rows(T, k, rows, N, type);
+    if (st != FP8_OK) return st;
+    if (!dy && !dweights) return FP8_OK;
+    if (T == 0 && (!dy || !src || rows == 0 || N == 0)) return FP8_OK;
+    if ((T && (!pos || (N && !dout))) || (T && rows && N && dweights && !y)) return FP8_ERR_INVALID_ARG;
+    for (const void* q : {dout, y, (const void*)dy})
+        if (!aligned(q, type_size(type))) return FP8_ERR_ALIGNMENT;
+    for (const void* q : {(const void*)pos, (const void*)weights, (const void*)src, (const void*)dweights})
+        if (!aligned(q, 4)) return FP8_ERR_ALIGNMENT;
+    int cus = 0;
+    const fp8_status dev = current_device_cus(&cus);
+    if (dev != FP8_OK) return dev;
+    fp8k::RowsParams p{};
+    p.x = dout; p.y = y; p.out = dy; p.dw = dweights; p.pos = pos; p.w = weights; p.src = dy ? src : nullptr;
+    p.T = T; p.rows = rows; p.W = N; p.k = k;
+    p.work = T;
+    const int64_t wgs = T + (p.src ? cdiv(rows, 4 * fp8k::kClearRows) : 0);
+    if (wgs > kMaxGrid) return FP8_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)wgs);
+    if (type == FP8_TYPE_F32) hipLaunchKernelGGL(fp8k::expert_combine_grad_kernel<float>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    else hipLaunchKernelGGL(fp8k::expert_combine_grad_kernel<uint16_t>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    return launch_status();
+}
+
+size_t fp8_adapters_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t R) {
+    if (check_adapters(0, N, K, 1, R, rows) != FP8_OK) return 0;
+    int cus = 0;
+    if (current_device_cus(&cus) != FP8_OK) return 0;
+    return adapter_plan(rows, N, K, cus).bytes(R);
+}
+
+fp8_status fp8_adapters_plan(int64_t rows, int64_t N, int64_t K, int32_t R, int32_t compute_units,
+                             fp8_adapters_plan_t* plan) {
+    if (!plan || compute_units <= 0) return FP8_ERR_INVALID_ARG;
+    const fp8_status st = check_adapters(0, N, K, 1, R, rows);
+    if (st != FP8_OK) return st;
+    const AdapterPlan pl = adapter_plan(rows, N, K, compute_units);
+    *plan = fp8_adapters_plan_t{};
+    plan->tiles = pl.tiles;
+    plan->shared = pl.share;
+    plan->k_splits = (int32_t)pl.splits;
+    plan->k_range = pl.k_range;
+    plan->n_range = pl.n_range;
+    plan->workspace_bytes = pl.bytes(R);
+    return FP8_OK;
+}
+
+fp8_status fp8_add_adapters(const uint16_t* x, const uint16_t* a, const uint16_t* b, const float* scale,
+                            const int32_t* src, const int32_t* index, const uint16_t* y, uint16_t* out, int64_t T,
+                            int64_t N, int64_t K, int32_t L, int32_t R, int64_t rows, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    const fp8_status st = check_adapters(T, N, K, L, R, rows);
+    if (st != FP8_OK) return st;
+    if (T == 0 || N == 0 || rows == 0) return FP8_OK;
+    if (!x || !a || !b || !scale || !src || !index || !y || !out || (workspace_bytes && !workspace)) return FP8_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(workspace)) return FP8_ERR_ALIGNMENT;
+    if (!aligned(scale, 4) || !aligned(src, 4) || !aligned(index, 4) || !aligned(y, 2) || !aligned(out, 2))
+        return FP8_ERR_ALIGNMENT;
+    int cus = 0;
+    const fp8_status dev = current_device_cus(&cus);
+    if (dev != FP8_OK) return dev;
+    const AdapterPlan pl = adapter_plan(rows, N, K, cus);
+    if (workspace_bytes < pl.bytes(R)) return FP8_ERR_SCRATCH;
+    if (cdiv(N, pl.n_range) > 65535 || pl.splits > 65535) return FP8_ERR_UNSUPPORTED;
+    fp8k::AdapterParams p{};
+    p.x = x; p.a = a; p.b = b; p.scale = scale; p.src = src; p.index = index; p.y = y; p.out = out;
+    p.z = static_cast<float*>(workspace);
+    p.T = T; p.N = N; p.K = K; p.tiles = pl.tiles; p.k_range = pl.k_range; p.n_range = pl.n_range;
+    p.L = L; p.R = R; p.splits = (int32_t)pl.splits;
+    const hipStream_t s = (hipStream_t)stream;
+    if (R <= 16) launch_adapter_down<1>(p, pl.share, s);
+    else if (R <= 32) launch_adapter_down<2>(p, pl.share, s);
+    else if (R <= 64) launch_adapter_down<4>(p, pl.share, s);
+    else launch_adapter_down<8>(p, pl.share, s);
+    const fp8_status run = launch_status();
+    if (run != FP8_OK) return run;
+    if (R <= 32) launch_adapter_up<1>(p, pl.share, s);
+    else if (R <= 64) launch_adapter_up<2>(p, pl.share, s);
+    else launch_adapter_up<4>(p, pl.share, s);
+    return launch_status();
+}
+
+}  // extern "C"

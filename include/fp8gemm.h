@@ -514,6 +514,155 @@ fp8_status fp8_clip_grad_norm(const void* const* grads, void* const* outs,
                               void* workspace, size_t workspace_bytes, void* stream);
 size_t fp8_clip_workspace_size(const int64_t* sizes, int32_t count);
 
+/* ---------------------------------------------------------------------------
+ * Around the experts' products: the router's choice, tokens sorted by expert
+ * and back.  Unlike the calls above these take pointers of any alignment that
+ * their elements have, except where a call says otherwise.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * The k experts of each row with the largest logits, and their weights.
+ *   logits  type FP8_TYPE_F32 or FP8_TYPE_BF16 (T,E); 1 <= k <= E <= 1024, k <= 64
+ *   ids     int32 (T,k): experts by falling logit, equal logits by rising
+ *           index.  An expert whose logit is -infinity is never chosen: where
+ *           too few are left, the last ids are -1 and their weights 0.
+ *   weights fp32 (T,k): scale * p[id], p = softmax(logits[t]); with
+ *           renormalize divided by the chosen p's sum.
+ * A NaN ranks above all numbers; a row with a NaN or +infinity among its
+ * chosen logits (without renormalize: among all) has NaN weights.
+ */
+fp8_status fp8_route_topk(const void* logits, int64_t T, int32_t E, int32_t k, int32_t type,
+                          int32_t renormalize, float scale, float* weights,
+                          int32_t* ids, void* stream);
+
+/*
+ * Its gradient, the choice held fixed: dlogits (T,E) in the logits' type from
+ * dweights fp32 (T,k), the same logits, ids, k, renormalize and scale:
+ *   G = sum_j p_j dw_j over the chosen (p renormalized if the weights were)
+ *   dlogits[e] = scale * (sum over j with ids_j = e of p_j dw_j - p_e G),
+ * p_e being 0 for experts not chosen with renormalize.  ids outside [0,E) add
+ * nothing (their dweights are not read into any sum).
+ */
+fp8_status fp8_route_topk_grad(const float* dweights, const void* logits, const int32_t* ids,
+                               int64_t T, int32_t E, int32_t k, int32_t type,
+                               int32_t renormalize, float scale, void* dlogits,
+                               void* stream);
+
+/*
+ * Rows of the experts' buffers for `pairs` (token, choice) pairs, pair
+ * t * k + j being token t's j-th expert: a stable sort by expert.
+ *   ids     int32 (id_bytes 4) or int64 (8), (pairs); one outside [0,E) has no
+ *           expert.  E <= 1024.
+ *   pos     int32 (pairs): the pair's row, or -1
+ *   src     int32 (rows): the row's pair, or -1
+ * Contiguous layout (fp8_grouped_gemm_contiguous): the experts' segments
+ * follow each other, each in whole `align` rows (a power of two up to 1024;
+ * 128 for the grouped GEMM, 16 for fp8_add_adapters).
+ *   m_indices int32 (rows): the row's expert, -1 on rows without a pair
+ *   counts  int32 (E): each expert's pairs
+ *   rows    fp8_expert_rows() always suffices; with fewer, pairs whose row
+ *           would lie behind have none (pos -1)
+ *   keep    nonzero: pairs without an expert get rows too, in a segment behind
+ *           the experts' whose m_indices are -1 (then one expert more counts
+ *           in fp8_expert_rows)
+ * Masked layout (fp8_grouped_gemm_masked): expert e's rows begin at e * max_m;
+ * its pairs from the max_m-th on have none.
+ *   src     int32 (E*max_m);  masked_m int32 (E): min(pairs, max_m) of each
+ * Every output is written whole.  workspace: fp8_expert_sort_workspace_size()
+ * bytes, 4-byte aligned, else FP8_ERR_SCRATCH (0 for few pairs); no clearing.
+ */
+int64_t fp8_expert_rows(int64_t pairs, int32_t E, int32_t align);
+size_t fp8_expert_sort_workspace_size(int64_t pairs, int32_t E);
+fp8_status fp8_expert_sort_contiguous(const void* ids, int32_t id_bytes, int64_t pairs,
+                                      int32_t E, int32_t align, int64_t rows, int32_t keep,
+                                      int32_t* pos, int32_t* src, int32_t* m_indices,
+                                      int32_t* counts, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+fp8_status fp8_expert_sort_masked(const void* ids, int32_t id_bytes, int64_t pairs,
+                                  int32_t E, int64_t max_m, int32_t* pos, int32_t* src,
+                                  int32_t* masked_m, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * Tokens to their experts' rows: xs[pos[t][j]] = x[t].
+ *   x (T,K) and xs (rows,K) of one type (FP8_TYPE_F32 or FP8_TYPE_BF16), pos
+ *   int32 (T,k), each row named at most once; a place outside [0,rows) is none.
+ *   src int32 (rows) or NULL: with it, rows whose src is negative become
+ *   zeros; without it they stay as they are.
+ * The gradient is fp8_expert_combine of dxs without weights.
+ */
+fp8_status fp8_expert_dispatch(const void* x, const int32_t* pos, const int32_t* src,
+                               void* xs, int64_t T, int32_t k, int64_t rows, int64_t K,
+                               int32_t type, void* stream);
+
+/*
+ * The same with the rows quantized as fp8_quant_1x128 does (from FP32 values):
+ *   xq u8 (rows,K), sa fp32 [K/128][rows]; K % 128 == 0.  Rows without a token
+ *   stay as they are (the grouped GEMMs do not use them).  x, xq and sa
+ *   16-byte aligned.  flags: FP8_FLAG_UE8M0.
+ */
+fp8_status fp8_expert_dispatch_quant(const void* x, const int32_t* pos, uint8_t* xq,
+                                     float* sa, int64_t T, int32_t k, int64_t rows,
+                                     int64_t K, int32_t type, uint32_t flags,
+                                     void* stream);
+
+/*
+ * Experts' rows back to their tokens: out[t] = sum_j weights[t][j] * y[pos[t][j]]
+ * over the pairs that have a row, in FP32 in the order of j, rounded once.
+ *   y (rows,N), out (T,N) of one type, weights fp32 (T,k) or NULL (1).
+ */
+fp8_status fp8_expert_combine(const void* y, const int32_t* pos, const float* weights,
+                              void* out, int64_t T, int32_t k, int64_t rows, int64_t N,
+                              int32_t type, void* stream);
+
+/*
+ * Its gradient: dy[pos[t][j]] = weights[t][j] * dout[t], and dweights[t][j] =
+ * <dout[t], y[pos[t][j]]> in FP32 (0 for a pair without a row).
+ *   dout (T,N), y and dy (rows,N) of one type; dy or dweights may be NULL (not
+ *   computed; y is read for dweights only).  src as for fp8_expert_dispatch.
+ */
+fp8_status fp8_expert_combine_grad(const void* dout, const void* y, const int32_t* pos,
+                                   const float* weights, const int32_t* src, void* dy,
+                                   float* dweights, int64_t T, int32_t k, int64_t rows,
+                                   int64_t N, int32_t type, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside one projection:
+ *   out[t] = y[t] + scale[a] * (x[t] A_a^T) B_a^T,  a the adapter of token t
+ * ------------------------------------------------------------------------- */
+/*
+ *   x bf16 bits (T,K), a bf16 bits (L,R,K), b bf16 bits (L,N,R), scale fp32 (L),
+ *   y and out bf16 bits (T,N), out may be y; any N, K % 128 == 0, R a multiple
+ *   of 8 up to 128 (smaller adapters: zeros in the rest of a or b).
+ *   src, index int32 (rows): src and m_indices of fp8_expert_sort_contiguous
+ *   over the tokens' adapters with align 16.  Rows whose src is outside [0,T)
+ *   have no token.  Tokens whose index is outside [0,L) take y as it is, and
+ *   tokens in no row are not written: sort with `keep` where out is not y.  A
+ *   row whose index differs from that of its tile of 16 (the first of its rows
+ *   that has a token) is not computed.  Each token stands in at most one row.
+ * The products' sums are FP32, x A^T is kept to 16 bits or more, and out is
+ * rounded once.  x, a, b and workspace 16-byte aligned; workspace:
+ * fp8_adapters_workspace_size() bytes, else FP8_ERR_SCRATCH; no clearing;
+ * calls that overlap in time need one each.
+ */
+fp8_status fp8_add_adapters(const uint16_t* x, const uint16_t* a, const uint16_t* b,
+                            const float* scale, const int32_t* src, const int32_t* index,
+                            const uint16_t* y, uint16_t* out, int64_t T, int64_t N,
+                            int64_t K, int32_t L, int32_t R, int64_t rows,
+                            void* workspace, size_t workspace_bytes, void* stream);
+size_t fp8_adapters_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t R);
+
+/* The kernels a fp8_add_adapters call launches (host arithmetic, no device needed). */
+typedef struct {
+    int64_t tiles;          /* of 16 rows */
+    int32_t shared;         /* 1: a workgroup takes four tiles; 0: one */
+    int32_t k_splits;       /* workgroups along K per tile */
+    int64_t k_range, n_range;   /* of a workgroup of the first and the second kernel */
+    size_t workspace_bytes;
+} fp8_adapters_plan_t;
+fp8_status fp8_adapters_plan(int64_t rows, int64_t N, int64_t K, int32_t R,
+                             int32_t compute_units, fp8_adapters_plan_t* plan);
+
 /* M alignment every expert segment of the contiguous layout must have
  * ([DG] "分组 GEMM 的两种布局": the alignment query).  Returns 128. */
 int32_t fp8_get_mk_alignment_for_contiguous_layout(void);

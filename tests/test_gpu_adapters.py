@@ -1,0 +1,122 @@
+"""Low-rank adapters of many requests against their 64-bit form: every rank's
+kernel, one token to long prompts, tokens without an adapter, in place and
+out of place, shared and split tiles."""
+import numpy as np
+import pytest
+import torch
+
+import fine_grained_block_e4m3_amd as fp8
+import routing_reference as ref
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+
+def _operands(rng, T, L, R, K, N):
+    def bf16(a):
+        return torch.from_numpy(np.asarray(a, np.float32)).bfloat16().cuda()
+    return (bf16(rng.normal(size=(T, K))), bf16(rng.normal(size=(L, R, K)) / K ** 0.5), bf16(rng.normal(size=(L, N, R)) * 0.3),
+            torch.from_numpy(rng.uniform(0.5, 2, L).astype(np.float32)).cuda(), bf16(rng.normal(size=(T, N))))
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+def _check(rng, T, L, R, K, N, idx, what):
+    x, a, b, s, y = _operands(rng, T, L, R, K, N)
+    rows = fp8.adapter_rows(torch.from_numpy(np.asarray(idx)).cuda(), L)
+    full = torch.full((T * N + 32,), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = fp8.add_adapters(x, a, b, s, rows, y, out=full[16:16 + T * N].view(T, N))
+    r, err = ref.adapters(_f64(x), _f64(a), _f64(b), _f64(s), idx, _f64(y))
+    ref.assert_near(_f64(out), r, ref.rounded(err, r, True), what)
+    assert bool((full[:16] == 9).all()) and bool((full[-16:] == 9).all())
+    none = torch.from_numpy((np.asarray(idx) < 0) | (np.asarray(idx) >= L)).cuda()
+    assert torch.equal(out[none].view(torch.int16), y[none].view(torch.int16))
+    again = fp8.add_adapters(x, a, b, s, rows, y)
+    assert torch.equal(again, out)
+    here = y.clone()
+    assert fp8.add_adapters(x, a, b, s, rows, here, out=here) is here
+    assert torch.equal(here, out)
+
+
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 72, 128])
+def test_ranks(R):
+    rng = np.random.default_rng(R)
+    for T, L, K, N in ((1, 1, 128, 1), (1, 3, 7168, 2048), (5, 2, 640, 77), (40, 6, 256, 300), (100, 64, 1536, 130)):
+        say("adapters", R, T, L, K, N)
+        _check(rng, T, L, R, K, N, rng.integers(-1, L + 1, T), f"{R} {T} {L} {K} {N}")
+
+
+@pytest.mark.parametrize("N", [1, 3, 8, 63, 64, 65, 255, 257, 1000])
+def test_widths(N):
+    rng = np.random.default_rng(N)
+    say("adapters width", N)
+    _check(rng, 33, 3, 16, 384, N, rng.integers(-1, 3, 33), f"width {N}")
+
+
+@pytest.mark.parametrize("dtype", [np.int32, np.int64])
+def test_orders(dtype):
+    """One adapter for all, runs, none at all, every token its own."""
+    rng = np.random.default_rng(1)
+    T, L = 150, 200
+    for name, idx in (("one", np.full(T, 7)), ("runs", np.arange(T) // 40), ("none", np.full(T, -1)),
+                      ("own", rng.permutation(L)[:T]), ("far", rng.choice([-2 ** 31, 2 ** 31 - 1, 5], T))):
+        say("adapters order", name)
+        _check(rng, T, L, 16, 256, 200, idx.astype(dtype), name)
+
+
+def test_many_tiles():
+    """So many tiles that a workgroup takes several (a device of 256 compute units: 2048 tiles)."""
+    rng = np.random.default_rng(2)
+    T, L, R, K, N = 33001, 5, 16, 128, 72
+    idx = rng.integers(-1, L, T)
+    rows = fp8.expert_rows(T, L + 1, 16)
+    assert fp8.adapters_plan(rows, N, K, R)["shared"] == 1
+    say("adapters many tiles")
+    _check(rng, T, L, R, K, N, idx, "many tiles")
+
+
+def test_given_tables():
+    """Rows outside the tokens, tiles of mixed indices, tiles without a row."""
+    say("adapters given tables")
+    rng = np.random.default_rng(3)
+    T, L, R, K, N = 20, 3, 16, 256, 100
+    x, a, b, s, y = _operands(rng, T, L, R, K, N)
+    src = torch.full((64,), -1, dtype=torch.int32, device="cuda")
+    index = torch.full((64,), 1, dtype=torch.int32, device="cuda")
+    src[3], src[5], src[7] = 4, T, 9            # T: no token
+    index[3], index[7] = 2, 0                   # token 9 is not computed: the tile is token 4's
+    src[33], src[34], index[33], index[34] = 0, 19, 1, 1
+    out = fp8.add_adapters(x, a, b, s, fp8.AdapterRows(src, index), y, out=torch.full_like(y, 5.0))
+    idx = np.full(T, -1)
+    idx[[4, 0, 19]] = 2, 1, 1
+    r, err = ref.adapters(_f64(x), _f64(a), _f64(b), _f64(s), idx, _f64(y))
+    done = [0, 4, 19]
+    ref.assert_near(_f64(out)[done], r[done], ref.rounded(err, r, True)[done], "given")
+    assert bool((out[[i for i in range(T) if i not in done]] == 5).all())
+
+
+def test_workspace_and_refusals():
+    say("adapters refusals")
+    rng = np.random.default_rng(4)
+    x, a, b, s, y = _operands(rng, 10, 3, 16, 256, 100)
+    rows = fp8.adapter_rows(torch.zeros(10, dtype=torch.int32, device="cuda"), 3)
+    size = fp8.adapters_plan(rows.src.shape[0], 100, 256, 16)["workspace_bytes"]
+    want = fp8.add_adapters(x, a, b, s, rows, y)
+    ws = torch.full((size + 16,), 0xFF, dtype=torch.uint8, device="cuda")
+    assert torch.equal(fp8.add_adapters(x, a, b, s, rows, y, workspace=ws[:size]), want)
+    assert bool((ws[size:] == 0xFF).all())
+    with pytest.raises(fp8.Fp8GemmError):
+        fp8.add_adapters(x, a, b, s, rows, y, workspace=ws[:size - 16])
+    for bad in ((x[:9], a, b, s, rows, y), (x, a[:2], b, s, rows, y), (x, a, b[:, :99].contiguous(), s, rows, y),
+                (x, a, b, s[:2], rows, y), (x, a, b, s, (rows.src, rows.index[:16]), y), (x.t(), a, b, s, rows, y),
+                (x, a, b, s, rows, y.cpu())):
+        with pytest.raises(ValueError):
+            fp8.add_adapters(*bad)
+    with pytest.raises(TypeError):
+        fp8.add_adapters(x.float(), a, b, s, rows, y)
+    with pytest.raises(fp8.Fp8GemmError):          # a rank that is no multiple of 8
+        fp8.add_adapters(x, a[:, :12].contiguous(), b[:, :, :12].contiguous(), s, rows, y)
+    assert fp8.add_adapters(x[:0], a, b, s, fp8.adapter_rows(torch.zeros(0, dtype=torch.int32, device="cuda"), 3),
+                            y[:0]).shape == (0, 100)
