@@ -128,8 +128,8 @@ class GatedGradPlan(ctypes.Structure):
 
 class AdaptersPlan(ctypes.Structure):
     """fp8_adapters_plan_t: the kernels a call of add_adapters launches."""
-    _fields_ = [("tiles", ctypes.c_int64), ("shared", ctypes.c_int32), ("k_splits", ctypes.c_int32),
-                ("k_range", ctypes.c_int64), ("n_range", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
+    _fields_ = [("tiles", ctypes.c_int64), ("k_splits", ctypes.c_int64), ("k_range", ctypes.c_int64),
+                ("n_range", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t), ("group", ctypes.c_int32)]
     as_dict = GemmPlan.as_dict
 
 
@@ -198,9 +198,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fp8_expert_combine.argtypes = [P, P, P, P, I64, I32, I64, I64, I32, P]
     L.fp8_expert_combine_grad.argtypes = [P] * 7 + [I64, I32, I64, I64, I32, P]
     L.fp8_add_adapters.argtypes = [P] * 8 + [I64, I64, I64, I32, I32, I64, P, SIZE, P]
-    L.fp8_adapters_workspace_size.argtypes = [I64, I64, I64, I32]
+    L.fp8_adapters_workspace_size.argtypes = [I64, I32, I64, I64, I64, I32]
     L.fp8_adapters_workspace_size.restype = SIZE
-    L.fp8_adapters_plan.argtypes = [I64, I64, I64, I32, I32, ctypes.POINTER(AdaptersPlan)]
+    L.fp8_adapters_plan.argtypes = [I64, I32, I64, I64, I64, I32, I32, ctypes.POINTER(AdaptersPlan)]
     for fn in ("fp8_quant_1x128", "fp8_quant_128x128", "fp8_gemm_nt", "fp8_gemm_nt_ws", "fp8_gemm_nt_noalloc",
                "fp8_gemm_plan",
                "fp8_gemm_nt_qout",
@@ -1102,11 +1102,13 @@ def adapter_rows(ids, adapters: int, workspace=None) -> AdapterRows:
     return AdapterRows(src, index)
 
 
-def adapters_plan(rows: int, N: int, K: int, R: int, compute_units: int = 256) -> dict:
-    """The kernels add_adapters launches for this many rows (host-side
-    arithmetic only; no GPU needed)."""
+def adapters_plan(T: int, adapters: int, N: int, K: int, R: int, compute_units: int = 256) -> dict:
+    """The kernels add_adapters launches for T tokens (host-side arithmetic
+    only; no GPU needed)."""
     plan = AdaptersPlan()
-    _check("fp8_adapters_plan", load_library().fp8_adapters_plan(rows, N, K, R, compute_units, ctypes.byref(plan)))
+    rows = expert_rows(T, adapters + 1, 16)
+    _check("fp8_adapters_plan", load_library().fp8_adapters_plan(T, adapters, rows, N, K, R, compute_units,
+                                                                 ctypes.byref(plan)))
     return plan.as_dict()
 
 
@@ -1132,7 +1134,7 @@ def add_adapters(x, a, b, scale, rows: AdapterRows, y, out=None, workspace=None)
     _same_device(x, a, b, scale, src, index, y)
     o = torch.empty_like(y) if out is None else _out(out, "out", _BF16, (T, N), x)
     nrows = src.shape[0]
-    ws, ws_bytes, held = _workspace(workspace, int(L.fp8_adapters_workspace_size(nrows, N, K, R)), x)
+    ws, ws_bytes, held = _workspace(workspace, int(L.fp8_adapters_workspace_size(T, n, nrows, N, K, R)), x)
     _check("fp8_add_adapters", L.fp8_add_adapters(
         x.data_ptr(), a.data_ptr(), b.data_ptr(), scale.data_ptr(), src.data_ptr(), index.data_ptr(), y.data_ptr(),
         o.data_ptr(), T, N, K, n, R, nrows, ws, ws_bytes, _launch_stream(x)))

@@ -4,20 +4,27 @@
 //
 // The tokens come sorted by adapter in tiles of 16 rows (src: the token of a
 // row or -1, index: its adapter), which is one dimension of the matrix
-// instruction.  Two kernels:
-//   down  z[row] = x[src[row]] A_a^T, K split over waves and workgroups where
-//         the tiles are few; FP32 sums, one buffer per workgroup along K
-//   up    the sums of z, scaled, times B_a^T, added to y and rounded once
-// Both are bounded by memory: x, y and the adapters that occur are read once
-// from memory (tiles of one adapter share them through the caches); the
-// products are a few operations per byte.  z enters the second product as the
-// sum of two BF16 values, which keeps 16 bits of it (one part would cost 2^-9
-// of the added term) and costs only instructions that wait anyway.
+// instruction.  Two kernels: the first forms z = x A^T, K split over waves and
+// workgroups, the second adds z's sums, multiplies by B^T and adds y, N split.
+// Each has two forms:
+//   tiles   a workgroup per tile: few tokens per adapter, A and B are most of
+//           what is read, and the operands come straight into registers
+//   groups  a workgroup per four tiles, which mostly share an adapter: x and y
+//           are most of what is read, in whole 128-byte pieces of their rows
+//           through LDS.  (The matrix instruction's layout, 16 rows of 64 bytes
+//           per load, comes at 36 GB/s per compute unit from L2, pieces of 128
+//           bytes at 80, whole kilobytes at 105, measured: with many tokens
+//           that is the bound.)
+// Both are bounded by memory otherwise; the products are a few operations per
+// byte.  z enters the second product as the sum of two BF16 values, which keeps
+// 16 bits of it (one part would cost 2^-9 of the added term) and costs only
+// instructions that wait anyway.
 //
 // The index of a tile is that of its first row with a token; a row of another
 // index is not computed.  Rows of an index outside the adapters take y as it is.
 #pragma once
 
+#include "gemm_common.h"
 #include "rows_common.h"
 
 namespace fp8k {
@@ -33,9 +40,10 @@ struct AdapterParams {
     uint16_t* out;              // (T, N), may be y
     float* z;                   // [splits][16 tiles][R]
     int64_t T, N, K, tiles;
-    int64_t k_range;            // elements of K per workgroup, a multiple of 128
-    int64_t n_range;            // columns per workgroup of the second kernel
-    int32_t L, R, splits;
+    int64_t k_range;            // elements of K per workgroup of the first kernel, a multiple of 128
+    int64_t n_range;            // columns per workgroup of the second kernel, a multiple of 256
+    int32_t L, R;
+    int32_t splits, parts;      // workgroups along K and along N
 };
 
 constexpr int kAdapterMaxR = 128;
@@ -44,160 +52,435 @@ constexpr int kAdapterMaxR = 128;
 struct AdapterTile {
     int64_t token;              // of the lane's row, or of a row that has one
     int32_t index;              // of the tile
-    bool any, valid;            // the tile has a token; the lane's row is one of the tile's index
+    bool any;                   // the tile has a token
+    bool adds;                  // and its index is an adapter
+    bool valid;                 // the lane's row is one of the tile's index
 };
 __device__ __forceinline__ AdapterTile adapter_tile(const AdapterParams& p, int64_t tile, int lane) {
     AdapterTile t;
-    const int64_t row = tile * 16 + (lane & 15);
-    const int32_t src = tile < p.tiles ? p.src[row] : -1;
-    const bool has = src >= 0 && src < p.T;
-    const int32_t idx = has ? p.index[row] : -1;
+    const int64_t row = (tile < p.tiles ? tile : 0) * 16 + (lane & 15);
+    const int32_t src = p.src[row], idx = p.index[row];
+    const bool has = tile < p.tiles && src >= 0 && src < p.T;
     const uint64_t m = __ballot(has);
     t.any = m != 0;
     const int first = t.any ? __builtin_ctzll(m) : 0;
     t.index = __builtin_amdgcn_readlane(idx, first);
+    t.adds = t.any && t.index >= 0 && t.index < p.L;
     t.valid = has && idx == t.index;
     const int32_t safe = __builtin_amdgcn_readlane(src, first);
     t.token = t.valid ? src : safe;
     return t;
 }
 
-// First kernel.  WK waves of a workgroup share a tile's K range, 4 / WK tiles.
-// A step is 32 of K: lane l reads 16 bytes of token l % 16 (or of row l % 16
-// of A) from element 8 (l / 16) on, four steps in flight.  Rows without a
-// token read another row's and are not stored, rows of A behind R the last one's.
-template <int RT, int WK>
-__global__ __launch_bounds__(256) void adapter_down_kernel(AdapterParams p) {
-    __shared__ float part[WK > 1 ? 3 : 1][RT][64][4];
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int64_t tile = WK > 1 ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
-    const AdapterTile t = adapter_tile(p, tile, lane);
-    const bool work = t.any && t.index >= 0 && t.index < p.L;
-    if (WK > 1 && !work) return;            // (the whole workgroup)
-    f32x4 acc[RT] = {};
-    if (work) {
-        const int64_t k0 = (int64_t)blockIdx.y * p.k_range, k1 = k0 + p.k_range < p.K ? k0 + p.k_range : p.K;
-        const uint16_t* x = p.x + t.token * p.K + 8 * (lane >> 4);
-        const uint16_t* a[RT];
+// First product.  A step is 32 of K: lane l reads 16 bytes of token l % 16 (and
+// of row l % 16 of each 16 of A) from element 8 (l / 16) on.  Lanes whose row
+// has no token read another row's and are not used, rows of A behind R the
+// last one's.  The lane's results are elements 16 r + 4 (l / 16) + i of token
+// l % 16.
+__device__ __forceinline__ const uint16_t* adapter_x(const AdapterParams& p, const AdapterTile& t, int lane) {
+    return p.x + t.token * p.K + 8 * (lane >> 4);
+}
+__device__ __forceinline__ const uint16_t* adapter_a(const AdapterParams& p, const AdapterTile& t, int r, int lane) {
+    const int row = 16 * r + (lane & 15);
+    return p.a + ((int64_t)t.index * p.R + (row < p.R ? row : p.R - 1)) * p.K + 8 * (lane >> 4);
+}
+__device__ __forceinline__ bf16x8 load_bf16x8(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
+
+// z over the chunks of 32 G elements c, c + step, ..., below `end`; the next
+// chunk's loads are under way while one is multiplied.
+template <int RT, int G>
+__device__ __forceinline__ void adapter_down(const uint16_t* x, const uint16_t* const (&a)[RT], int64_t c, int64_t step,
+                                             int64_t end, f32x4 (&acc)[RT]) {
+    bf16x8 xv[2][G], av[2][G][RT];
+    auto load = [&](int h, int64_t at) FP8K_INLINE {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int row = 16 * r + (lane & 15);
-            a[r] = p.a + ((int64_t)t.index * p.R + (row < p.R ? row : p.R - 1)) * p.K + 8 * (lane >> 4);
+        for (int i = 0; i < G; ++i) {
+            const int64_t k = at * (32 * G) + 32 * i;
+            xv[h][i] = load_bf16x8(x + k);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) av[h][i][r] = load_bf16x8(a[r] + k);
         }
-        for (int64_t k = k0 + (WK > 1 ? wave * 128 : 0); k < k1; k += WK * 128) {
-            bf16x8 xv[4], av[RT][4];
+    };
+    auto multiply = [&](int h) FP8K_INLINE {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                xv[i] = *reinterpret_cast<const bf16x8*>(x + k + 32 * i);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) av[r][i] = *reinterpret_cast<const bf16x8*>(a[r] + k + 32 * i);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[r][i], xv[i], acc[r], 0, 0, 0);
-        }
-    }
-    if constexpr (WK > 1) {
-        if (wave > 0) {
+        for (int i = 0; i < G; ++i)
 #pragma unroll
             for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[wave - 1][r][lane][i] = acc[r][i];
+                acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[h][i][r], xv[h][i], acc[r], 0, 0, 0);
+    };
+    if (c >= end) return;
+    load(0, c);
+    for (;;) {
+        if (c + step >= end) {
+            multiply(0);
+            return;
         }
-        __syncthreads();
-        if (wave > 0) return;
-#pragma unroll
-        for (int w = 0; w < 3; ++w)
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][i] += part[w][r][lane][i];
+        load(1, c + step);
+        multiply(0);
+        c += 2 * step;
+        if (c >= end) {
+            multiply(1);
+            return;
+        }
+        load(0, c);
+        multiply(1);
     }
-    // lane l: token l % 16, elements 16 r + 4 (l / 16) + i
-    if (!work || !t.valid) return;
-    float* z = p.z + ((int64_t)blockIdx.y * p.tiles * 16 + tile * 16 + (lane & 15)) * p.R + 4 * (lane >> 4);
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-        if (16 * r + 4 * (lane >> 4) < p.R) *reinterpret_cast<f32x4*>(z + 16 * r) = acc[r];
 }
 
-// Second kernel.  A wave forms 64 columns of a tile at a time: four products
-// whose rows are the columns 16 (i / 4) + 4 j + i % 4 (i the row, j the
-// product), so that a lane ends with 16 columns of one token in a row.
-// RS: 32s of R.
-template <int RS, bool SHARE>
+// Second product.  B's rows are the columns col(j), j = 0..3, of the lane's row
+// of each of four products.  RS: 32s of R.
+template <int RS, typename F>
+__device__ __forceinline__ void adapter_b_load(const AdapterParams& p, int32_t index, F col, int g, bf16x8 (&w)[4][RS]) {
+    const uint16_t* b = p.b + (int64_t)index * p.N * p.R;
+    int at[RS];                             // (lanes whose elements lie behind R load others, times a z of 0 ...)
+#pragma unroll
+    for (int s = 0; s < RS; ++s) at[s] = 32 * s + 8 * g < p.R ? 32 * s + 8 * g : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t c = col(j) < p.N ? col(j) : p.N - 1;      // (not stored)
+#pragma unroll
+        for (int s = 0; s < RS; ++s) w[j][s] = load_bf16x8(b + c * p.R + at[s]);
+    }
+    // ... which an infinity there would make a NaN
+#pragma unroll
+    for (int s = 0; s < RS; ++s)
+        if (32 * s + 32 > p.R) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (32 * s + 8 * g >= p.R) w[j][s] = bf16x8{};
+        }
+}
+template <int RS>
+__device__ __forceinline__ void adapter_multiply(const bf16x8 (&w)[4][RS], const bf16x8 (&hi)[RS], const bf16x8 (&lo)[RS],
+                                                 f32x4 (&acc)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < RS; ++s) {
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j][s], hi[s], acc[j], 0, 0, 0);
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j][s], lo[s], acc[j], 0, 0, 0);
+        }
+}
+
+// The scaled z of the lane's token, elements 32 s + 8 (l / 16) + 0..7, as two
+// BF16 parts.
+__device__ __forceinline__ void adapter_parts(const float (&f)[8], float scale, bf16x8& hi, bf16x8& lo) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float v = scale * f[e];
+        hi[e] = (__bf16)v;
+        lo[e] = (__bf16)(v - (float)hi[e]);
+    }
+}
+
+template <int RT, int G>
+__global__ __launch_bounds__(256) void adapter_down_kernel(AdapterParams p) {
+    __shared__ __attribute__((aligned(16))) float part[3][RT][64][4];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int64_t tile = blockIdx.x / p.splits, split = blockIdx.x - tile * p.splits;
+    const AdapterTile t = adapter_tile(p, tile, lane);
+    if (!t.adds) return;                    // (the whole workgroup)
+    f32x4 acc[RT] = {};
+    const int64_t k0 = split * p.k_range, k1 = k0 + p.k_range < p.K ? k0 + p.k_range : p.K;
+    const uint16_t* a[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) a[r] = adapter_a(p, t, r, lane);
+    adapter_down<RT, G>(adapter_x(p, t, lane), a, k0 / (32 * G) + wave, 4, k1 / (32 * G), acc);
+    if (wave > 0) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(part[wave - 1][r][lane]) = acc[r];
+    }
+    __syncthreads();
+    if (wave > 0 || !t.valid) return;
+    float* z = p.z + (split * p.tiles * 16 + tile * 16 + (lane & 15)) * p.R + 4 * (lane >> 4);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+        for (int w = 0; w < 3; ++w) acc[r] += *reinterpret_cast<const f32x4*>(part[w][r][lane]);
+        if (16 * r + 4 * (lane >> 4) < p.R) *reinterpret_cast<f32x4*>(z + 16 * r) = acc[r];
+    }
+}
+
+// z of groups of four tiles: a product of 64 rows of x with A's R rows, K in
+// stages of 64 elements.  Each wave loads whole 128-byte pieces of rows into
+// LDS; one wave's 16 rows and all of A are read back as operands.  A group of
+// several adapters goes through K once for each.
+// LDS row of 128 bytes: its eight 16-byte chunks at slot chunk ^ lds_swz(row).
+__device__ __forceinline__ void dma_lds16_from(uint32_t m0, const void* p) {
+    int saved;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %2, off\n\t"
+                 "s_mov_b32 m0, %0"
+                 : "=&s"(saved) : "s"(m0), "v"(p));
+}
+
+template <int RT, int STAGES>
+__global__ __launch_bounds__(256) void adapter_down_group_kernel(AdapterParams p, int64_t groups) {
+    constexpr int AROWS = (RT + 1) / 2 * 32, ROWS = 64 + AROWS, PER = ROWS / 32;     // 1 KB loads of a wave per stage
+    constexpr int STAGE = ROWS * 128;
+    static_assert((STAGES - 1) * PER <= 63, "vmcnt range");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int64_t per = (groups * p.splits + 7) / 8, work = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int64_t)(blockIdx.x >> 3) >= per || work >= groups * p.splits) return;
+    const int64_t group = work / p.splits, split = work - group * p.splits;
+    const uint32_t lds0 = (uint32_t)uniform((int)lds_addr(smem));
+    FP8K_LDS const uint8_t* lds = (FP8K_LDS const uint8_t*)smem;
+    AdapterTile t[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) t[m] = adapter_tile(p, group * 4 + m, lane);
+    const int64_t k0 = split * p.k_range, k1 = k0 + p.k_range < p.K ? k0 + p.k_range : p.K;
+    const int blocks = (int)((k1 - k0) / 64);
+    // the lane's place in a 1 KB load: row of 8, and the chunk that its slot holds
+    const int lrow = lane >> 3;
+    const uint16_t* from[PER];
+    f32x4 acc[RT] = {};
+    uint32_t todo = 0;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) todo |= t[m].adds ? 1u << m : 0u;
+    while (todo) {
+        int index = 0, mine = 0;            // this pass's adapter; whether the wave's tile is one of its
+#pragma unroll
+        for (int m = 3; m >= 0; --m)
+            if (todo >> m & 1) index = t[m].index;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            if ((todo >> m & 1) && t[m].index == index) {
+                todo &= ~(1u << m);
+                mine |= wave == m;
+            }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int row = 8 * (wave * PER + i) + lrow, chunk = (lane & 7) ^ lds_swz(row);
+            if (row < 64) {
+                // (a row without a token: another's values, not used)
+                const int64_t at = group * 64 + row;
+                const int src = at < p.tiles * 16 ? p.src[at] : -1;
+                from[i] = p.x + (int64_t)(src >= 0 && src < p.T ? src : 0) * p.K + k0 + 8 * chunk;
+            } else {
+                const int r = row - 64 < p.R ? row - 64 : p.R - 1;
+                from[i] = p.a + ((int64_t)index * p.R + r) * p.K + k0 + 8 * chunk;
+            }
+        }
+        // (every address is at hand: the compiler's own loads do not count among the stages')
+        auto issue = [&](int kb) FP8K_INLINE {
+            const uint32_t dst = lds0 + (uint32_t)(kb % STAGES * STAGE + wave * PER * 1024);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) dma_lds16_from(dst + i * 1024, from[i] + (int64_t)kb * 64);
+        };
+        for (int kb = 0; kb < STAGES - 1 && kb < blocks; ++kb) issue(kb);
+        for (int kb = 0; kb < blocks; ++kb) {
+            // block kb has landed; the blocks behind it, if there are enough, are under way
+            if (kb + STAGES - 2 < blocks) wait_vmcnt<(STAGES - 2) * PER>();
+            else wait_vmcnt<0>();
+            lds_barrier();
+            // (its stage was read in the last round, which every wave has left)
+            if (kb + STAGES - 1 < blocks) issue(kb + STAGES - 1);
+            if (mine) {
+                FP8K_LDS const uint8_t* base = lds + kb % STAGES * STAGE;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    auto read = [&](int row) FP8K_INLINE {
+                        const int slot = (4 * s + (lane >> 4)) ^ lds_swz(row);
+                        return __builtin_bit_cast(bf16x8, *(FP8K_LDS const i32x4*)(base + row * 128 + 16 * slot));
+                    };
+                    const bf16x8 xv = read(16 * wave + (lane & 15));
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(read(64 + 16 * r + (lane & 15)), xv, acc[r], 0, 0, 0);
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        lds_barrier();                      // (before another pass's first stages)
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        if (wave != m || !t[m].adds || !t[m].valid) continue;
+        float* z = p.z + (split * p.tiles * 16 + (group * 4 + m) * 16 + (lane & 15)) * p.R + 4 * (lane >> 4);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+            if (16 * r + 4 * (lane >> 4) < p.R) *reinterpret_cast<f32x4*>(z + 16 * r) = acc[r];
+    }
+}
+
+// The sum of eight elements of z over the splits.
+__device__ __forceinline__ void adapter_z_sum(const AdapterParams& p, int64_t row, int e0, float (&f)[8]) {
+    const float* z = p.z + row * p.R + e0;
+    const int64_t next = p.tiles * 16 * p.R;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    // (eight splits' loads at a time)
+    for (int i0 = 0; i0 < p.splits; i0 += 8) {
+        f32x4 u[8][2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u[i][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (i0 + i < p.splits) u[i][h] = *reinterpret_cast<const f32x4*>(z + (i0 + i) * next + 4 * h);
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] += u[i][e >> 2][e & 3];
+    }
+}
+
+// Second kernel for a tile: 64 columns at a time, by four products whose rows
+// are the columns 16 (i / 4) + 4 j + i % 4 (i the row, j the product), so that a
+// lane ends with 16 columns in a row of token l % 16.
+template <int RS>
 __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterParams p) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int64_t tile = SHARE ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+    const int g = lane >> 4, i = lane & 15;
+    const int64_t tile = blockIdx.x / p.parts, n_lo = (blockIdx.x - tile * p.parts) * p.n_range;
+    const int64_t n_end = n_lo + p.n_range < p.N ? n_lo + p.n_range : p.N, n0 = n_lo + wave * 64;
+    if (n0 >= n_end) return;
     const AdapterTile t = adapter_tile(p, tile, lane);
-    if (!t.any) return;
-    const bool adds = t.index >= 0 && t.index < p.L;
-    if (!adds && p.out == p.y) return;
-    const int g = lane >> 4;
-    // z of the lane's token, elements 32 s + 8 g + 0..7, as two BF16 parts
+    if (!t.any || (!t.adds && p.out == p.y)) return;
+    bf16x8 w[4][RS];
+    i32x4 base[2];
+    auto load = [&](int64_t n) FP8K_INLINE {
+        if (t.adds) adapter_b_load<RS>(p, t.index, [&](int j) FP8K_INLINE { return n + 16 * (i >> 2) + 4 * j + (i & 3); }, g, w);
+        const int64_t c0 = n + 16 * g;
+        const uint16_t* y = p.y + t.token * p.N + c0;
+        if (n + 64 <= p.N) {                // (lanes without a token of their own read another's)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) __builtin_memcpy(&base[h], y + 8 * h, 16);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                base[h] = i32x4{0, 0, 0, 0};
+                if (c0 + 8 * h < p.N) base[h] = load_row16<uint16_t>(y + 8 * h, p.N - c0 - 8 * h);
+            }
+        }
+    };
+    load(n0);
     bf16x8 hi[RS], lo[RS];
-    if (adds) {
+    if (t.adds) {
         const float c = p.scale[t.index];
-        const float* z = p.z + (tile * 16 + (lane & 15)) * p.R + 8 * g;
 #pragma unroll
         for (int s = 0; s < RS; ++s) {
             float f[8] = {};
-            if (t.valid && 32 * s + 8 * g < p.R) {
-                for (int i = 0; i < p.splits; ++i) {
-                    const float* zi = z + (int64_t)i * p.tiles * 16 * p.R + 32 * s;
-                    const f32x4 u = *reinterpret_cast<const f32x4*>(zi), v = *reinterpret_cast<const f32x4*>(zi + 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[e] += u[e];
-                        f[4 + e] += v[e];
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float v = c * f[e];
-                hi[s][e] = (__bf16)v;
-                lo[s][e] = (__bf16)(v - (float)hi[s][e]);
-            }
+            if (t.valid && 32 * s + 8 * g < p.R) adapter_z_sum(p, tile * 16 + i, 32 * s + 8 * g, f);
+            adapter_parts(f, c, hi[s], lo[s]);
         }
     }
-    const int64_t n_lo = (int64_t)blockIdx.y * p.n_range, n_end = n_lo + p.n_range < p.N ? n_lo + p.n_range : p.N;
-    const int i0 = lane & 15;
-    const uint16_t* b = p.b + (int64_t)(adds ? t.index : 0) * p.N * p.R + 8 * g;
-    const uint16_t* y = p.y + t.token * p.N;
-    uint16_t* out = p.out + t.token * p.N;
-    for (int64_t n = n_lo + (SHARE ? 0 : wave * 64); n < n_end; n += SHARE ? 64 : 256) {
+    for (int64_t n = n0; n < n_end; n += 256) {
+        if (n > n0) load(n);
         f32x4 acc[4] = {};
-        const int64_t c0 = n + 16 * g;      // the lane's first column
-        i32x4 base[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (t.valid && c0 + 8 * h < p.N) base[h] = load_row16<uint16_t>(y + c0 + 8 * h, p.N - c0 - 8 * h);
-        if (adds) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                int64_t col = n + 16 * (i0 >> 2) + 4 * j + (i0 & 3);
-                col = col < p.N ? col : p.N - 1;        // (not stored)
-#pragma unroll
-                for (int s = 0; s < RS; ++s) {
-                    bf16x8 w{};
-                    if (32 * s + 8 * g < p.R) w = *reinterpret_cast<const bf16x8*>(b + col * p.R + 32 * s);
-                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, hi[s], acc[j], 0, 0, 0);
-                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, lo[s], acc[j], 0, 0, 0);
-                }
-            }
-        }
+        if (t.adds) adapter_multiply<RS>(w, hi, lo, acc);
+        if (!t.valid) continue;
+        const int64_t c0 = n + 16 * g;
+        uint16_t* out = p.out + t.token * p.N + c0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (t.valid && c0 + 8 * h < p.N) {
-                float f[8];
+            float f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = RowElem<uint16_t>::get(base[h], e) + acc[2 * h + (e >> 2)][e & 3];
-                // (without an adapter y goes through as it is, the sign of a zero too)
-                store_row16<uint16_t>(out + c0 + 8 * h, p.N - c0 - 8 * h, adds ? RowElem<uint16_t>::pack(f) : base[h]);
+            for (int e = 0; e < 8; ++e) f[e] = RowElem<uint16_t>::get(base[h], e) + acc[2 * h + (e >> 2)][e & 3];
+            // (without an adapter y goes through as it is, the sign of a zero too)
+            const i32x4 v = t.adds ? RowElem<uint16_t>::pack(f) : base[h];
+            if (n + 64 <= p.N) __builtin_memcpy(out + 8 * h, &v, 16);
+            else if (c0 + 8 * h < p.N) store_row16<uint16_t>(out + 8 * h, p.N - c0 - 8 * h, v);
+        }
+    }
+}
+
+// Second kernel for a group: z's parts of its 64 rows lie in LDS; a wave forms
+// 64 columns of the four tiles, B's loads shared by tiles of one adapter, and
+// each tile's results change places in LDS so that 8 lanes hold 64 columns of a
+// row and y is read and written in whole 128-byte pieces.
+template <int RS>
+__global__ __launch_bounds__(256) void adapter_up_group_kernel(AdapterParams p, int64_t groups) {
+    constexpr int ZROW = 32 * RS + 8;       // elements; 16 rows at one place cover all banks
+    constexpr int DROW = 68;
+    __shared__ __attribute__((aligned(16))) uint16_t zp[2][64][ZROW];
+    __shared__ __attribute__((aligned(16))) float ds[4][16][DROW];
+    __shared__ int32_t token[64], adapter[4];       // -1: none
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int g = lane >> 4, i = lane & 15;
+    const int64_t per = (groups * p.parts + 7) / 8, work = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int64_t)(blockIdx.x >> 3) >= per || work >= groups * p.parts) return;
+    const int64_t group = work / p.parts, n_lo = (work - group * p.parts) * p.n_range;
+    const int64_t n_end = n_lo + p.n_range < p.N ? n_lo + p.n_range : p.N;
+    {
+        const AdapterTile t = adapter_tile(p, group * 4 + wave, lane);
+        if (lane < 16) token[16 * wave + lane] = t.valid ? (int32_t)t.token : -1;
+        if (lane == 0) adapter[wave] = t.adds ? t.index : -1;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < 64 * 4 * RS; k += 256) {
+        const int row = k / (4 * RS), e0 = 8 * (k % (4 * RS)), a = adapter[row >> 4];
+        float f[8] = {};
+        bf16x8 hi, lo;
+        if (a >= 0 && token[row] >= 0 && e0 < p.R) adapter_z_sum(p, group * 64 + row, e0, f);
+        adapter_parts(f, a >= 0 ? p.scale[a] : 0.f, hi, lo);
+        *reinterpret_cast<bf16x8*>(&zp[0][row][e0]) = hi;
+        *reinterpret_cast<bf16x8*>(&zp[1][row][e0]) = lo;
+    }
+    __syncthreads();
+    const int r8 = lane >> 3, c8 = 8 * (lane & 7);      // the lane's rows r8 and r8 + 8, and its columns
+    for (int64_t n = n_lo + wave * 64; n < n_end; n += 256) {
+        const bool full = n + 64 <= p.N;
+        i32x4 base[4][2];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // (a row without a token reads another's)
+                const uint16_t* y = p.y + (int64_t)max(token[16 * m + 8 * h + r8], 0) * p.N + n + c8;
+                if (full) {
+                    __builtin_memcpy(&base[m][h], y, 16);
+                } else {
+                    base[m][h] = i32x4{0, 0, 0, 0};
+                    if (n + c8 < p.N) base[m][h] = load_row16<uint16_t>(y, p.N - n - c8);
+                }
             }
+        bf16x8 w[4][RS];
+        int held = -1;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int a = uniform(adapter[m]);
+            if (a >= 0) {
+                if (a != held) {
+                    adapter_b_load<RS>(p, a, [&](int j) FP8K_INLINE { return n + 16 * j + i; }, g, w);
+                    held = a;
+                }
+                bf16x8 hi[RS], lo[RS];
+#pragma unroll
+                for (int s = 0; s < RS; ++s) {
+                    hi[s] = *reinterpret_cast<const bf16x8*>(&zp[0][16 * m + i][32 * s + 8 * g]);
+                    lo[s] = *reinterpret_cast<const bf16x8*>(&zp[1][16 * m + i][32 * s + 8 * g]);
+                }
+                f32x4 acc[4] = {};
+                adapter_multiply<RS>(w, hi, lo, acc);
+                // (the wave's own buffer: its LDS operations run in order)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4*>(&ds[wave][i][16 * j + 4 * g]) = acc[j];
+                __builtin_amdgcn_wave_barrier();
+            } else if (p.out == p.y) {
+                continue;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t = token[16 * m + 8 * h + r8];
+                i32x4 v = base[m][h];
+                if (a >= 0) {
+                    const f32x4 d0 = *reinterpret_cast<const f32x4*>(&ds[wave][8 * h + r8][c8]);
+                    const f32x4 d1 = *reinterpret_cast<const f32x4*>(&ds[wave][8 * h + r8][c8 + 4]);
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = RowElem<uint16_t>::get(base[m][h], e) + (e < 4 ? d0[e] : d1[e - 4]);
+                    v = RowElem<uint16_t>::pack(f);
+                }
+                uint16_t* out = p.out + (int64_t)t * p.N + n + c8;
+                if (t >= 0) {
+                    if (full) __builtin_memcpy(out, &v, 16);
+                    else if (n + c8 < p.N) store_row16<uint16_t>(out, p.N - n - c8, v);
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
         }
     }
 }

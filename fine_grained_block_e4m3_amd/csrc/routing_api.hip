@@ -118,22 +118,31 @@ fp8_status rows_grid(fp8k::RowsParams& p, int64_t per_seg, dim3* grid) {
 // Adapters.
 // ---------------------------------------------------------------------------
 struct AdapterPlan {
-    bool share;                 // a workgroup's waves take tiles of their own, else parts of one
-    int64_t tiles, splits, k_range, n_range;
+    int group;                  // tiles per workgroup: 1 or 4
+    int64_t tiles, groups, splits, k_range, n_range;
     size_t bytes(int64_t R) const { return (size_t)(splits * tiles * 16 * R) * sizeof(float); }
 };
 
-AdapterPlan adapter_plan(int64_t rows, int64_t N, int64_t K, int cus) {
+// Groups of four tiles where adapters have tokens enough to fill them and the
+// work outweighs the longer way of a workgroup.  One MI355X, K 7168, N 2048,
+// tiles / groups, us: 8 adapters, 1000 tokens, R 16 13 / 17; 4000, R 16 25 / 28;
+// 2000, R 64 35 / 30; 8192, R 16 67 / 48 and R 64 136 / 65; 100 adapters, 4000
+// tokens, R 32 52 / 50; 200 adapters 53 / 72.
+// Workgroups per compute unit: along K two (tiles) or four (groups: one more
+// than fit, so that the last round is short), along N four or eight; parts of K
+// of 512 and parts of N of 256 at least.
+AdapterPlan adapter_plan(int64_t T, int64_t L, int64_t rows, int64_t N, int64_t K, int64_t R, int cus) {
     AdapterPlan pl{};
     pl.tiles = rows / 16;
-    pl.share = pl.tiles >= 8 * cus;
-    const int64_t wgs = std::max<int64_t>(pl.share ? cdiv(pl.tiles, 4) : pl.tiles, 1), step = pl.share ? 128 : 512;
-    pl.splits = std::clamp(cdiv(4 * cus, wgs), (int64_t)1, std::max<int64_t>(K / step, 1));
-    pl.k_range = cdiv(cdiv(K, pl.splits), step) * step;
+    pl.group = T >= 64 * (L + 1) && T * R >= 96 << 10 ? 4 : 1;
+    pl.groups = std::max<int64_t>(cdiv(pl.tiles, pl.group), 1);
+    auto share = [&](int64_t len, int64_t least, int64_t step, int64_t wgs) {
+        const int64_t parts = std::clamp(wgs / pl.groups, (int64_t)1, std::max<int64_t>(cdiv(len, least), 1));
+        return std::max(cdiv(cdiv(len, parts), step), (int64_t)1) * step;
+    };
+    pl.k_range = share(K, 512, 128, (pl.group == 1 ? 2 : 4) * cus);
     pl.splits = cdiv(K, pl.k_range);
-    const int64_t cols = pl.share ? 64 : 256;
-    const int64_t parts = std::clamp(cdiv(4 * cus, wgs), (int64_t)1, std::max<int64_t>(cdiv(N, cols), 1));
-    pl.n_range = std::max(cdiv(cdiv(N, parts), cols), (int64_t)1) * cols;
+    pl.n_range = share(N, 256, 256, (pl.group == 1 ? 4 : 8) * cus);
     return pl;
 }
 
@@ -144,16 +153,18 @@ fp8_status check_adapters(int64_t T, int64_t N, int64_t K, int32_t L, int32_t R,
     return FP8_OK;
 }
 
-template <int RT>
-void launch_adapter_down(const fp8k::AdapterParams& p, bool share, hipStream_t s) {
-    if (share) hipLaunchKernelGGL((fp8k::adapter_down_kernel<RT, 1>), dim3((unsigned)cdiv(p.tiles, 4), (unsigned)p.splits), dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((fp8k::adapter_down_kernel<RT, 4>), dim3((unsigned)p.tiles, (unsigned)p.splits), dim3(256), 0, s, p);
+// Grids of groups in whole 8s: a workgroup's die is its index modulo 8.
+template <int RT, int G>
+void launch_adapter_down(const fp8k::AdapterParams& p, const AdapterPlan& pl, hipStream_t s) {
+    const int64_t wgs = pl.groups * p.splits;
+    if (pl.group == 1) hipLaunchKernelGGL((fp8k::adapter_down_kernel<RT, G>), dim3((unsigned)wgs), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((fp8k::adapter_down_group_kernel<RT, 3>), dim3((unsigned)(cdiv(wgs, 8) * 8)), dim3(256), 0, s, p, pl.groups);
 }
 template <int RS>
-void launch_adapter_up(const fp8k::AdapterParams& p, bool share, hipStream_t s) {
-    const unsigned parts = (unsigned)cdiv(p.N, p.n_range);
-    if (share) hipLaunchKernelGGL((fp8k::adapter_up_kernel<RS, true>), dim3((unsigned)cdiv(p.tiles, 4), parts), dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((fp8k::adapter_up_kernel<RS, false>), dim3((unsigned)p.tiles, parts), dim3(256), 0, s, p);
+void launch_adapter_up(const fp8k::AdapterParams& p, const AdapterPlan& pl, hipStream_t s) {
+    const int64_t wgs = pl.groups * p.parts;
+    if (pl.group == 1) hipLaunchKernelGGL((fp8k::adapter_up_kernel<RS>), dim3((unsigned)wgs), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((fp8k::adapter_up_group_kernel<RS>), dim3((unsigned)(cdiv(wgs, 8) * 8)), dim3(256), 0, s, p, pl.groups);
 }
 
 }  // namespace
@@ -340,23 +351,23 @@ fp8_status fp8_expert_combine_grad(const void* dout, const void* y, const int32_
     return launch_status();
 }
 
-size_t fp8_adapters_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t R) {
-    if (check_adapters(0, N, K, 1, R, rows) != FP8_OK) return 0;
+size_t fp8_adapters_workspace_size(int64_t T, int32_t L, int64_t rows, int64_t N, int64_t K, int32_t R) {
+    if (check_adapters(T, N, K, L, R, rows) != FP8_OK) return 0;
     int cus = 0;
     if (current_device_cus(&cus) != FP8_OK) return 0;
-    return adapter_plan(rows, N, K, cus).bytes(R);
+    return adapter_plan(T, L, rows, N, K, R, cus).bytes(R);
 }
 
-fp8_status fp8_adapters_plan(int64_t rows, int64_t N, int64_t K, int32_t R, int32_t compute_units,
+fp8_status fp8_adapters_plan(int64_t T, int32_t L, int64_t rows, int64_t N, int64_t K, int32_t R, int32_t compute_units,
                              fp8_adapters_plan_t* plan) {
     if (!plan || compute_units <= 0) return FP8_ERR_INVALID_ARG;
-    const fp8_status st = check_adapters(0, N, K, 1, R, rows);
+    const fp8_status st = check_adapters(T, N, K, L, R, rows);
     if (st != FP8_OK) return st;
-    const AdapterPlan pl = adapter_plan(rows, N, K, compute_units);
+    const AdapterPlan pl = adapter_plan(T, L, rows, N, K, R, compute_units);
     *plan = fp8_adapters_plan_t{};
     plan->tiles = pl.tiles;
-    plan->shared = pl.share;
-    plan->k_splits = (int32_t)pl.splits;
+    plan->group = pl.group;
+    plan->k_splits = pl.splits;
     plan->k_range = pl.k_range;
     plan->n_range = pl.n_range;
     plan->workspace_bytes = pl.bytes(R);
@@ -377,24 +388,25 @@ fp8_status fp8_add_adapters(const uint16_t* x, const uint16_t* a, const uint16_t
     int cus = 0;
     const fp8_status dev = current_device_cus(&cus);
     if (dev != FP8_OK) return dev;
-    const AdapterPlan pl = adapter_plan(rows, N, K, cus);
+    const AdapterPlan pl = adapter_plan(T, L, rows, N, K, R, cus);
     if (workspace_bytes < pl.bytes(R)) return FP8_ERR_SCRATCH;
-    if (cdiv(N, pl.n_range) > 65535 || pl.splits > 65535) return FP8_ERR_UNSUPPORTED;
+    if ((pl.tiles + 8) * std::max(pl.splits, cdiv(N, pl.n_range)) > kMaxGrid) return FP8_ERR_UNSUPPORTED;
     fp8k::AdapterParams p{};
     p.x = x; p.a = a; p.b = b; p.scale = scale; p.src = src; p.index = index; p.y = y; p.out = out;
     p.z = static_cast<float*>(workspace);
     p.T = T; p.N = N; p.K = K; p.tiles = pl.tiles; p.k_range = pl.k_range; p.n_range = pl.n_range;
-    p.L = L; p.R = R; p.splits = (int32_t)pl.splits;
+    p.L = L; p.R = R; p.splits = (int32_t)pl.splits; p.parts = (int32_t)cdiv(N, pl.n_range);
     const hipStream_t s = (hipStream_t)stream;
-    if (R <= 16) launch_adapter_down<1>(p, pl.share, s);
-    else if (R <= 32) launch_adapter_down<2>(p, pl.share, s);
-    else if (R <= 64) launch_adapter_down<4>(p, pl.share, s);
-    else launch_adapter_down<8>(p, pl.share, s);
+    // (one tile: as many steps of K in flight as two chunks leave registers for)
+    if (R <= 16) launch_adapter_down<1, 4>(p, pl, s);
+    else if (R <= 32) launch_adapter_down<2, 4>(p, pl, s);
+    else if (R <= 64) launch_adapter_down<4, 2>(p, pl, s);
+    else launch_adapter_down<8, 1>(p, pl, s);
     const fp8_status run = launch_status();
     if (run != FP8_OK) return run;
-    if (R <= 32) launch_adapter_up<1>(p, pl.share, s);
-    else if (R <= 64) launch_adapter_up<2>(p, pl.share, s);
-    else launch_adapter_up<4>(p, pl.share, s);
+    if (R <= 32) launch_adapter_up<1>(p, pl, s);
+    else if (R <= 64) launch_adapter_up<2>(p, pl, s);
+    else launch_adapter_up<4>(p, pl, s);
     return launch_status();
 }
 

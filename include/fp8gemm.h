@@ -650,18 +650,19 @@ fp8_status fp8_add_adapters(const uint16_t* x, const uint16_t* a, const uint16_t
                             const uint16_t* y, uint16_t* out, int64_t T, int64_t N,
                             int64_t K, int32_t L, int32_t R, int64_t rows,
                             void* workspace, size_t workspace_bytes, void* stream);
-size_t fp8_adapters_workspace_size(int64_t rows, int64_t N, int64_t K, int32_t R);
+size_t fp8_adapters_workspace_size(int64_t T, int32_t L, int64_t rows, int64_t N,
+                                   int64_t K, int32_t R);
 
 /* The kernels a fp8_add_adapters call launches (host arithmetic, no device needed). */
 typedef struct {
     int64_t tiles;          /* of 16 rows */
-    int32_t shared;         /* 1: a workgroup takes four tiles; 0: one */
-    int32_t k_splits;       /* workgroups along K per tile */
+    int64_t k_splits;       /* workgroups along K of the first kernel */
     int64_t k_range, n_range;   /* of a workgroup of the first and the second kernel */
     size_t workspace_bytes;
+    int32_t group;          /* tiles per workgroup: 1 or 4 */
 } fp8_adapters_plan_t;
-fp8_status fp8_adapters_plan(int64_t rows, int64_t N, int64_t K, int32_t R,
-                             int32_t compute_units, fp8_adapters_plan_t* plan);
+fp8_status fp8_adapters_plan(int64_t T, int32_t L, int64_t rows, int64_t N, int64_t K,
+                             int32_t R, int32_t compute_units, fp8_adapters_plan_t* plan);
 
 /* M alignment every expert segment of the contiguous layout must have
  * ([DG] "分组 GEMM 的两种布局": the alignment query).  Returns 128. */

@@ -67,14 +67,14 @@ def test_orders(dtype):
 
 
 def test_many_tiles():
-    """So many tiles that a workgroup takes several (a device of 256 compute units: 2048 tiles)."""
+    """So many tokens per adapter that a workgroup takes four tiles, of one adapter, of two, of one and none."""
     rng = np.random.default_rng(2)
-    T, L, R, K, N = 33001, 5, 16, 128, 72
-    idx = rng.integers(-1, L, T)
-    rows = fp8.expert_rows(T, L + 1, 16)
-    assert fp8.adapters_plan(rows, N, K, R)["shared"] == 1
-    say("adapters many tiles")
-    _check(rng, T, L, R, K, N, idx, "many tiles")
+    for T, L, R, K, N, group in ((8301, 5, 16, 128, 72, 4), (4000, 300, 24, 256, 130, 1), (2700, 40, 64, 384, 65, 4),
+                                 (3080, 12, 32, 2048, 600, 4), (1000, 3, 128, 1152, 340, 4), (1400, 5, 72, 640, 128, 4)):
+        idx = rng.integers(-1, L, T)
+        assert fp8.adapters_plan(T, L, N, K, R)["group"] == group
+        say("adapters many tiles", T, L, R)
+        _check(rng, T, L, R, K, N, idx, "many tiles")
 
 
 def test_given_tables():
@@ -100,16 +100,18 @@ def test_given_tables():
 def test_workspace_and_refusals():
     say("adapters refusals")
     rng = np.random.default_rng(4)
-    x, a, b, s, y = _operands(rng, 10, 3, 16, 256, 100)
+    x, a, b, s, y = _operands(rng, 10, 3, 128, 2048, 1200)
     rows = fp8.adapter_rows(torch.zeros(10, dtype=torch.int32, device="cuda"), 3)
-    size = fp8.adapters_plan(rows.src.shape[0], 100, 256, 16)["workspace_bytes"]
+    plan = fp8.adapters_plan(10, 3, 1200, 2048, 128)
+    assert plan["group"] == 1 and plan["k_splits"] > 1
+    size = plan["workspace_bytes"]
     want = fp8.add_adapters(x, a, b, s, rows, y)
     ws = torch.full((size + 16,), 0xFF, dtype=torch.uint8, device="cuda")
     assert torch.equal(fp8.add_adapters(x, a, b, s, rows, y, workspace=ws[:size]), want)
     assert bool((ws[size:] == 0xFF).all())
     with pytest.raises(fp8.Fp8GemmError):
         fp8.add_adapters(x, a, b, s, rows, y, workspace=ws[:size - 16])
-    for bad in ((x[:9], a, b, s, rows, y), (x, a[:2], b, s, rows, y), (x, a, b[:, :99].contiguous(), s, rows, y),
+    for bad in ((x[:9], a, b, s, rows, y), (x, a[:2], b, s, rows, y), (x, a, b[:, :1199].contiguous(), s, rows, y),
                 (x, a, b, s[:2], rows, y), (x, a, b, s, (rows.src, rows.index[:16]), y), (x.t(), a, b, s, rows, y),
                 (x, a, b, s, rows, y.cpu())):
         with pytest.raises(ValueError):
@@ -119,4 +121,4 @@ def test_workspace_and_refusals():
     with pytest.raises(fp8.Fp8GemmError):          # a rank that is no multiple of 8
         fp8.add_adapters(x, a[:, :12].contiguous(), b[:, :, :12].contiguous(), s, rows, y)
     assert fp8.add_adapters(x[:0], a, b, s, fp8.adapter_rows(torch.zeros(0, dtype=torch.int32, device="cuda"), 3),
-                            y[:0]).shape == (0, 100)
+                            y[:0]).shape == (0, 1200)

@@ -141,17 +141,19 @@ def test_adapter_validation(L):
         assert call(**{name: P(4104)}) == ALIGN, name
     assert call(scale=P(4098)) == ALIGN and call(y=P(4097)) == ALIGN
     assert call(T=0, x=None) == OK and call(N=0) == OK and call(rows=0) == OK
-    assert L.fp8_adapters_workspace_size(48, 20, 100, 16) == 0
+    assert L.fp8_adapters_workspace_size(3, 2, 48, 20, 100, 16) == 0
 
 
-@pytest.mark.parametrize("rows", [16, 32, 1024, 8320, 40000, 1 << 20])
+@pytest.mark.parametrize("T,adapters", [(1, 1), (1, 1000), (100, 64), (320, 9), (8192, 8), (8192, 300), (1 << 20, 16)])
 @pytest.mark.parametrize("N,K", [(1, 128), (300, 1536), (7168, 7168), (24576, 128), (2112, 28672)])
-def test_adapter_plan_covers_the_problem(rows, N, K):
+def test_adapter_plan_covers_the_problem(T, adapters, N, K):
     for cus in (256, 64):
-        p = fp8.adapters_plan(rows, N, K, 16, compute_units=cus)
+        p = fp8.adapters_plan(T, adapters, N, K, 16, compute_units=cus)
+        rows = fp8.expert_rows(T, adapters + 1, 16)
         assert p["tiles"] * 16 == rows
+        assert p["group"] == (4 if T >= 64 * (adapters + 1) and T * 16 >= 96 << 10 else 1)
         assert p["k_range"] % 128 == 0 and (p["k_splits"] - 1) * p["k_range"] < K <= p["k_splits"] * p["k_range"]
-        assert p["n_range"] % 64 == 0 and p["n_range"] > 0 and -(-N // p["n_range"]) <= 65535
+        assert p["n_range"] % 256 == 0 and p["n_range"] > 0
         assert p["workspace_bytes"] == p["k_splits"] * rows * 16 * 4
 
 
