@@ -22,8 +22,6 @@ import ctypes
 import os
 from array import array
 
-from typing import NamedTuple
-
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -859,6 +857,10 @@ _I32 = torch.int32
 
 def _typed(t, name: str, ndim: int) -> int:
     """Checks rows of fp32 or bf16 and returns their FP8_TYPE_*."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == ndim and t.is_contiguous():
+        kind = ROW_TYPES.get(t.dtype)
+        if kind is not None:
+            return kind
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     kind = ROW_TYPES.get(t.dtype)
@@ -871,6 +873,11 @@ def _typed(t, name: str, ndim: int) -> int:
 def _shape(t, name: str, shape) -> None:
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _ints(like, *shape) -> torch.Tensor:
+    """New int32 entries (without a type to convert where `like` has it: half a microsecond)."""
+    return like.new_empty(*shape) if like.dtype is _I32 else like.new_empty(shape, dtype=_I32)
 
 
 def _optional(t):
@@ -887,7 +894,8 @@ def route_topk(logits, k: int, renormalize: bool = True, scale: float = 1.0, out
     kind = _typed(logits, "logits", 2)
     T, E = logits.shape
     if out is None:
-        w, ids = logits.new_empty((T, k), dtype=_F32), logits.new_empty((T, k), dtype=_I32)
+        w = logits.new_empty(T, k) if kind == 0 else logits.new_empty((T, k), dtype=_F32)
+        ids = logits.new_empty((T, k), dtype=_I32)
     else:
         w, ids = _out(out[0], "out[0]", _F32, (T, k), logits), _out(out[1], "out[1]", _I32, (T, k), logits)
     _check("fp8_route_topk", L.fp8_route_topk(logits.data_ptr(), T, E, k, kind, renormalize, scale, w.data_ptr(),
@@ -916,6 +924,8 @@ def route_topk_grad(dweights, logits, ids, renormalize: bool = True, scale: floa
 
 def _ids(ids) -> int:
     """Checks expert (or adapter) indices of any shape and returns their bytes."""
+    if isinstance(ids, torch.Tensor) and ids.dtype is _I32 and ids.is_cuda and ids.is_contiguous():
+        return 4
     if not isinstance(ids, torch.Tensor):
         raise TypeError("ids must be a torch.Tensor")
     if ids.dtype not in (torch.int32, torch.int64):
@@ -934,7 +944,7 @@ def expert_rows(pairs: int, experts: int, align: int = 128) -> int:
 
 def _sorted_out(out, shapes, like):
     if out is None:
-        return [like.new_empty(shape, dtype=_I32) for shape in shapes]
+        return [_ints(like, *shape) for shape in shapes]
     if len(out) != len(shapes):
         raise ValueError(f"out must hold {len(shapes)} tensors")
     return [_out(t, f"out[{i}]", _I32, shape, like) for i, (t, shape) in enumerate(zip(out, shapes))]
@@ -954,7 +964,7 @@ def expert_sort(ids, experts: int, align: int = 128, rows: int | None = None, ke
     n = ids.numel()
     if rows is None:
         rows = expert_rows(n, experts + 1 if keep else experts, align)
-    pos, src, m_indices, counts = _sorted_out(out, (tuple(ids.shape), (rows,), (rows,), (experts,)), ids)
+    pos, src, m_indices, counts = _sorted_out(out, (ids.shape, (rows,), (rows,), (experts,)), ids)
     ws, ws_bytes, held = _workspace(workspace, int(L.fp8_expert_sort_workspace_size(n, experts)), ids)
     _check("fp8_expert_sort_contiguous", L.fp8_expert_sort_contiguous(
         ids.data_ptr(), size, n, experts, align, rows, keep, pos.data_ptr(), src.data_ptr(), m_indices.data_ptr(),
@@ -969,7 +979,7 @@ def expert_sort_masked(ids, experts: int, max_m: int, out=None, workspace=None):
     L = load_library()
     size = _ids(ids)
     n = ids.numel()
-    pos, src, masked_m = _sorted_out(out, (tuple(ids.shape), (experts * max_m,), (experts,)), ids)
+    pos, src, masked_m = _sorted_out(out, (ids.shape, (experts * max_m,), (experts,)), ids)
     ws, ws_bytes, held = _workspace(workspace, int(L.fp8_expert_sort_workspace_size(n, experts)), ids)
     _check("fp8_expert_sort_masked", L.fp8_expert_sort_masked(
         ids.data_ptr(), size, n, experts, max_m, pos.data_ptr(), src.data_ptr(), masked_m.data_ptr(), ws, ws_bytes,
@@ -995,7 +1005,7 @@ def expert_dispatch(x, pos, src, out=None) -> torch.Tensor:
     _need(src, "src", _I32, 1)
     _same_device(x, pos, src)
     rows = src.shape[0]
-    xs = x.new_empty((rows, K)) if out is None else _out(out, "out", x.dtype, (rows, K), x)
+    xs = x.new_empty(rows, K) if out is None else _out(out, "out", x.dtype, (rows, K), x)
     _check("fp8_expert_dispatch", L.fp8_expert_dispatch(x.data_ptr(), pos.data_ptr(), src.data_ptr(), xs.data_ptr(),
                                                         T, k, rows, K, kind, _launch_stream(x)))
     return xs
@@ -1043,7 +1053,7 @@ def expert_combine(y, pos, weights=None, out=None) -> torch.Tensor:
         _need(weights, "weights", _F32, 2)
         _shape(weights, "weights", (T, k))
         _same_device(y, weights)
-    o = y.new_empty((T, N)) if out is None else _out(out, "out", y.dtype, (T, N), y)
+    o = y.new_empty(T, N) if out is None else _out(out, "out", y.dtype, (T, N), y)
     _check("fp8_expert_combine", L.fp8_expert_combine(y.data_ptr(), pos.data_ptr(), _optional(weights), o.data_ptr(),
                                                       T, k, rows, N, kind, _launch_stream(y)))
     return o
@@ -1084,22 +1094,25 @@ def expert_combine_grad(dout, y, pos, weights=None, src=None, need_dy: bool = Tr
 # ---------------------------------------------------------------------------
 # Adapters beside a shared projection.
 # ---------------------------------------------------------------------------
-class AdapterRows(NamedTuple):
-    """A batch's tokens sorted by adapter in tiles of 16 rows: src the token of
-    a row (-1: none), index its adapter (-1: none)."""
-    src: torch.Tensor
-    index: torch.Tensor
-
-
-def adapter_rows(ids, adapters: int, workspace=None) -> AdapterRows:
-    """The rows that add_adapters takes, once per batch for all its
-    projections: ids int32 or int64 (T), each token's adapter; one outside
-    [0, adapters) has none."""
-    _ids(ids)
+def adapter_rows(ids, adapters: int, workspace=None) -> torch.Tensor:
+    """A batch's tokens sorted by adapter in tiles of 16 rows, as add_adapters
+    takes them, once per batch for all its projections: ids int32 or int64 (T),
+    each token's adapter; one outside [0, adapters) has none.  Returns int32
+    (2, rows): the token of each row (-1: none) and its adapter (-1: none)."""
+    L = load_library()
+    size = _ids(ids)
     if ids.dim() != 1:
         raise ValueError(f"ids must have 1 dim, got {tuple(ids.shape)}")
-    _, src, index, _ = expert_sort(ids, adapters, align=16, keep=True, workspace=workspace)
-    return AdapterRows(src, index)
+    n = len(ids)
+    # (fp8_expert_rows(n, adapters + 1, 16))
+    rows = n + 15 * min(adapters + 1, n) & -16
+    table = _ints(ids, 2, rows)
+    ws, ws_bytes, held = _workspace(workspace, int(L.fp8_expert_sort_workspace_size(n, adapters)), ids)
+    at = table.data_ptr()
+    _check("fp8_expert_sort_contiguous", L.fp8_expert_sort_contiguous(
+        ids.data_ptr(), size, n, adapters, 16, rows, 1, None, at, at + 4 * rows, None, ws, ws_bytes,
+        _launch_stream(ids)))
+    return table
 
 
 def adapters_plan(T: int, adapters: int, N: int, K: int, R: int, compute_units: int = 256) -> dict:
@@ -1112,30 +1125,40 @@ def adapters_plan(T: int, adapters: int, N: int, K: int, R: int, compute_units: 
     return plan.as_dict()
 
 
-def add_adapters(x, a, b, scale, rows: AdapterRows, y, out=None, workspace=None) -> torch.Tensor:
+def _adapter_operands(x, a, b, scale, rows, y):
+    # (one expression for operands that fit, as in _gated_operands)
+    try:
+        T, K = x.shape
+        n, R, _ = a.shape
+        N = y.shape[1]
+        two, nrows = rows.shape
+        if (x.dtype is _BF16 and a.dtype is _BF16 and b.dtype is _BF16 and y.dtype is _BF16 and scale.dtype is _F32
+                and rows.dtype is _I32 and two == 2 and y.shape[0] == T and a.shape[2] == K and b.shape == (n, N, R)
+                and scale.shape == (n,) and x.is_contiguous() and a.is_contiguous() and b.is_contiguous()
+                and scale.is_contiguous() and rows.is_contiguous() and y.is_contiguous() and y.dim() == 2
+                and (0 <= x.get_device() == a.get_device() == b.get_device() == scale.get_device()
+                     == rows.get_device() == y.get_device())):
+            return T, N, K, n, R, nrows
+    except (AttributeError, TypeError, ValueError, IndexError):
+        pass
+    for t, name, dtype, dims in ((x, "x", _BF16, 2), (a, "a", _BF16, 3), (b, "b", _BF16, 3), (scale, "scale", _F32, 1),
+                                 (rows, "rows", _I32, 2), (y, "y", _BF16, 2)):
+        _need(t, name, dtype, dims)
+    _same_device(x, a, b, scale, rows, y)
+    raise ValueError("add_adapters: inconsistent operand shapes")
+
+
+def add_adapters(x, a, b, scale, rows, y, out=None, workspace=None) -> torch.Tensor:
     """A projection's result y (T, N) bf16 with each token's adapter added:
     out[t] = y[t] + scale[i] * (x[t] a[i]^T) b[i]^T.  x (T, K), a (L, R, K),
     b (L, N, R) bf16, scale fp32 (L), rows from adapter_rows(ids, L).  Tokens
     without an adapter take y as it is.  out may be y."""
     L = load_library()
-    _need(x, "x", _BF16, 2)
-    _need(a, "a", _BF16, 3)
-    _need(b, "b", _BF16, 3)
-    _need(scale, "scale", _F32, 1)
-    _need(y, "y", _BF16, 2)
-    src, index = rows
-    _need(src, "rows.src", _I32, 1)
-    _need(index, "rows.index", _I32, 1)
-    T, K = x.shape
-    n, R, _ = a.shape
-    N = y.shape[1]
-    if a.shape[2] != K or b.shape != (n, N, R) or scale.shape[0] != n or y.shape[0] != T or index.shape != src.shape:
-        raise ValueError("add_adapters: inconsistent operand shapes")
-    _same_device(x, a, b, scale, src, index, y)
-    o = torch.empty_like(y) if out is None else _out(out, "out", _BF16, (T, N), x)
-    nrows = src.shape[0]
+    T, N, K, n, R, nrows = _adapter_operands(x, a, b, scale, rows, y)
+    o = torch.empty_like(y) if out is None else out if out is y else _out(out, "out", _BF16, (T, N), x)
     ws, ws_bytes, held = _workspace(workspace, int(L.fp8_adapters_workspace_size(T, n, nrows, N, K, R)), x)
+    table = rows.data_ptr()
     _check("fp8_add_adapters", L.fp8_add_adapters(
-        x.data_ptr(), a.data_ptr(), b.data_ptr(), scale.data_ptr(), src.data_ptr(), index.data_ptr(), y.data_ptr(),
+        x.data_ptr(), a.data_ptr(), b.data_ptr(), scale.data_ptr(), table, table + 4 * nrows, y.data_ptr(),
         o.data_ptr(), T, N, K, n, R, nrows, ws, ws_bytes, _launch_stream(x)))
     return o

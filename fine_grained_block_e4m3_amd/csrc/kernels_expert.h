@@ -23,21 +23,20 @@ namespace fp8k {
 // ---------------------------------------------------------------------------
 // The sort.
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortMaxExperts = 1024;
 constexpr int kSortBins = kSortMaxExperts + 1;      // and one for pairs kept without an expert
 
 struct SortParams {
     const void* ids;            // int32, or int64
-    int32_t* pos;
+    int32_t* pos;               // may be NULL
     int32_t* src;
     int32_t* m_indices;         // contiguous layout
-    int32_t* counts;            // of each expert; masked layout: at most max_m
-    int32_t* hist;              // [chunks][bins], with more than one chunk
+    int32_t* counts;            // of each expert; masked layout: at most max_m; may be NULL
+    int32_t* hist;              // [bins][chunks4], with more than one chunk
     int64_t pairs, rows;
     int64_t chunk;              // pairs of a workgroup
     int32_t E, bins;            // bins: E, or E + 1 where pairs without an expert get rows too
+    int32_t chunks, chunks4;    // chunks4: rounded up to a multiple of 4
     int32_t align;              // contiguous
     int64_t max_m;              // masked
     bool contiguous;            // else masked
@@ -51,18 +50,44 @@ __device__ __forceinline__ int sort_bin(const SortParams& p, int64_t i) {
     return p.bins > p.E ? p.E : -1;
 }
 
-// Pairs per bin of one chunk.
-__global__ __launch_bounds__(kSortThreads) void expert_count_kernel(SortParams p) {
+// -1 to every row's entries, by all threads of `groups` workgroups; the rows of
+// pairs are written after it.
+template <int THREADS>
+__device__ __forceinline__ void sort_clear(const SortParams& p, int group, int groups) {
+    const i32x4 none{-1, -1, -1, -1};
+    for (int64_t r = 4 * ((int64_t)group * THREADS + threadIdx.x); r < p.rows; r += (int64_t)4 * groups * THREADS) {
+        if (r + 4 <= p.rows) {              // (at any alignment)
+            __builtin_memcpy(p.src + r, &none, 16);
+            if (p.contiguous) __builtin_memcpy(p.m_indices + r, &none, 16);
+        } else {
+            for (int64_t i = r; i < p.rows; ++i) {
+                p.src[i] = -1;
+                if (p.contiguous) p.m_indices[i] = -1;
+            }
+        }
+    }
+}
+
+// Pairs per bin of one chunk; and all rows cleared.
+__global__ __launch_bounds__(1024) void expert_count_kernel(SortParams p) {
     __shared__ int32_t hist[kSortBins];
-    for (int b = threadIdx.x; b < p.bins; b += kSortThreads) hist[b] = 0;
-    __syncthreads();
     const int64_t lo = blockIdx.x * p.chunk, end = lo + p.chunk < p.pairs ? lo + p.chunk : p.pairs;
-    for (int64_t i = lo + threadIdx.x; i < end; i += kSortThreads) {
+    const int64_t i0 = lo + threadIdx.x;
+    const int first = i0 < end ? sort_bin(p, i0) : -1;      // (its load runs while the counts are cleared)
+    for (int b = threadIdx.x; b < p.bins; b += 1024) hist[b] = 0;
+    sort_clear<1024>(p, blockIdx.x, gridDim.x);
+    __syncthreads();
+    if (first >= 0) atomicAdd(&hist[first], 1);
+    for (int64_t i = i0 + 1024; i < end; i += 1024) {
         const int b = sort_bin(p, i);
         if (b >= 0) atomicAdd(&hist[b], 1);
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < p.bins; b += kSortThreads) p.hist[(int64_t)blockIdx.x * p.bins + b] = hist[b];
+    for (int b = threadIdx.x; b < p.bins; b += 1024) p.hist[(int64_t)b * p.chunks4 + blockIdx.x] = hist[b];
+    if (blockIdx.x == 0) {                  // (what a row of four is filled up with)
+        for (int b = threadIdx.x; b < p.bins; b += 1024)
+            for (int c = p.chunks; c < p.chunks4; ++c) p.hist[(int64_t)b * p.chunks4 + c] = 0;
+    }
 }
 
 // Inclusive sum over the 64 lanes.
@@ -75,46 +100,110 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
     return v;
 }
 
-// Rows of one chunk's pairs.  Each wave counts and then places a run of the
-// chunk's pairs: the bins' counts of the waves before it and of the chunks
-// before this one make the first row of its own, and within 64 pairs a lane's
-// rank is the number of lower lanes with its bin (a mask that one ballot per
-// bit of the bin narrows).  No result depends on the order of the counting
-// atomics.
-__global__ __launch_bounds__(kSortThreads) void expert_place_kernel(SortParams p) {
-    __shared__ int32_t next[kSortWaves][kSortBins];     // per wave: counts, then the next row
-    __shared__ int32_t total[kSortBins];
-    __shared__ int32_t start[kSortBins + 1];
-    __shared__ int32_t sums[kSortWaves];
+// Lanes whose key (of `bits` bits) is the lane's own.
+__device__ __forceinline__ uint64_t same_key(uint32_t key, int bits) {
+    uint64_t same = ~0ull;
+    for (int k = 0; k < bits; ++k) {
+        const bool bit = key >> k & 1u;
+        const uint64_t m = __ballot(bit);
+        same &= bit ? m : ~m;
+    }
+    return same;
+}
+
+// Rows of one chunk's pairs.  Each wave takes a run of the chunk, 64 pairs at a
+// time; a lane's rank among them is the number of lower lanes with its bin, and
+// a count per wave and bin numbers the pairs of a run.  The counts of the waves
+// before it and of the chunks before this one then make the first row of a
+// wave's bin.  ROUNDS: times 64 pairs that a wave keeps in registers between
+// the two passes, or 0 (any number, formed twice).  No result depends on the
+// order of atomics.
+template <int WAVES, int ROUNDS>
+__global__ __launch_bounds__(64 * WAVES) void expert_place_kernel(SortParams p) {
+    constexpr int THREADS = 64 * WAVES;
+    __shared__ int32_t next[WAVES][kSortBins];  // per wave: counts, then the first row
+    __shared__ int32_t total[kSortBins];        // per bin: all chunks' pairs
+    __shared__ int32_t earlier[kSortBins];      // ... and those of the chunks before this one
+    __shared__ int32_t sums[WAVES];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int chunks = gridDim.x, c = blockIdx.x;
-    for (int b = lane; b < p.bins; b += 64) next[wave][b] = 0;
+    const int c = blockIdx.x;
+    const int bits = 32 - __builtin_clz(p.bins);        // a bin and "none" (= bins) fit
     const int64_t lo = c * p.chunk, end = lo + p.chunk < p.pairs ? lo + p.chunk : p.pairs;
-    const int64_t run = ((end - lo + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
+    const int64_t run = ((end - lo + WAVES - 1) / WAVES + 63) / 64 * 64;
     const int64_t w_lo = lo + wave * run, w_end = w_lo + run < end ? w_lo + run : end;
-    for (int64_t i = w_lo + lane; i < w_end; i += 64) {
-        const int b = sort_bin(p, i);
-        if (b >= 0) atomicAdd(&next[wave][b], 1);
+    int bin[ROUNDS > 0 ? ROUNDS : 1], at[ROUNDS > 0 ? ROUNDS : 1];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int64_t i = w_lo + 64 * r + lane;
+        bin[r] = i < w_end ? sort_bin(p, i) : -1;
+    }
+    if (p.chunks == 1) sort_clear<THREADS>(p, 0, 1);    // (else the first kernel has)
+    // (a wave clears and counts its own bins; LDS operations of a wave run in order)
+    for (int b = lane; b < p.bins; b += 64) next[wave][b] = 0;
+    // Numbers of 64 pairs within the wave's run.
+    auto number = [&](int b) FP8K_INLINE {
+        const uint64_t same = same_key(b >= 0 ? (uint32_t)b : (uint32_t)p.bins, bits);
+        const int rank = __popcll(same & ((1ull << lane) - 1)), n = __popcll(same);
+        int k = 0;
+        if (b >= 0) k = next[wave][b] + rank;
+        __builtin_amdgcn_wave_barrier();        // (every lane has read before the last one of its bin writes)
+        if (b >= 0 && rank == n - 1) next[wave][b] = k + 1;
+        __builtin_amdgcn_wave_barrier();
+        return k;
+    };
+    if constexpr (ROUNDS > 0) {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) at[r] = number(bin[r]);
+    } else {
+        for (int64_t i = w_lo + lane; i < w_end; i += 64) {
+            const int b = sort_bin(p, i);
+            if (b >= 0) atomicAdd(&next[wave][b], 1);
+        }
+    }
+    if (p.chunks > 1) {
+        // all chunks' pairs of a bin, and those of the chunks before this one, by 2^k threads a bin
+        int per = 1;
+        while (per < 16 && per * 2 * p.bins <= THREADS) per *= 2;
+        for (int b0 = 0; b0 < p.bins; b0 += THREADS / per) {
+            const int b = b0 + threadIdx.x / per;
+            int all = 0, before = 0;
+            if (b < p.bins) {
+                const i32x4* h = reinterpret_cast<const i32x4*>(p.hist + (int64_t)b * p.chunks4);
+#pragma unroll 4
+                for (int k = threadIdx.x % per; k < p.chunks4 / 4; k += per) {
+                    const i32x4 n = h[k];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        all += n[e];
+                        before += 4 * k + e < c ? n[e] : 0;
+                    }
+                }
+            }
+            for (int o = per / 2; o >= 1; o /= 2) {
+                all += __shfl_xor(all, o);
+                before += __shfl_xor(before, o);
+            }
+            if (b < p.bins && threadIdx.x % per == 0) {
+                total[b] = all;
+                earlier[b] = before;
+            }
+        }
     }
     __syncthreads();
-    // totals, and the rows that a bin's segment takes
+    // the rows that each bin's segment takes
     int carry = 0;
-    for (int b0 = 0; b0 < p.bins; b0 += kSortThreads) {
+    for (int b0 = 0; b0 < p.bins; b0 += THREADS) {
         const int b = b0 + threadIdx.x;
         int before = 0, all = 0, take = 0;
         if (b < p.bins) {
-            if (chunks > 1) {
-#pragma unroll 8
-                for (int i = 0; i < chunks; ++i) {
-                    const int n = p.hist[(int64_t)i * p.bins + b];
-                    all += n;
-                    before += i < c ? n : 0;
-                }
+            if (p.chunks > 1) {
+                all = total[b];
+                before = earlier[b];
             } else {
 #pragma unroll
-                for (int w = 0; w < kSortWaves; ++w) all += next[w][b];
+                for (int w = 0; w < WAVES; ++w) all += next[w][b];
             }
-            total[b] = all;
+            if (c == 0 && b < p.E && p.counts) p.counts[b] = p.contiguous || all < p.max_m ? all : (int)p.max_m;
             take = p.contiguous ? (all + p.align - 1) / p.align * p.align : 0;
         }
         const int upto = wave_scan(take, lane);
@@ -122,69 +211,43 @@ __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(SortParams p
         __syncthreads();
         int first = carry + upto - take;
 #pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             first += w < wave ? sums[w] : 0;
             carry += sums[w];
         }
         if (b < p.bins) {
-            // (rows past 2^31 do not exist: a masked buffer has fewer, and so has a contiguous one)
+            // (rows and pairs together stay below 2^31)
             if (!p.contiguous) first = (int)(b * p.max_m);
-            start[b] = first;
-            int at = first + before;
+            int row = first + before;
 #pragma unroll
-            for (int w = 0; w < kSortWaves; ++w) {
+            for (int w = 0; w < WAVES; ++w) {
                 const int n = next[w][b];
-                next[w][b] = at;
-                at += n;
+                next[w][b] = row;
+                row += n;
             }
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0) start[p.bins] = carry;
-    __syncthreads();
-    const int bits = 32 - __builtin_clz(p.bins);        // a bin and "none" (= bins) fit
-    for (int64_t i0 = w_lo; i0 < w_end; i0 += 64) {
-        const int64_t i = i0 + lane;
-        const bool in = i < w_end;
-        const int b = in ? sort_bin(p, i) : -1;
-        const uint32_t key = b >= 0 ? (uint32_t)b : (uint32_t)p.bins;
-        uint64_t same = ~0ull;
-        for (int k = 0; k < bits; ++k) {
-            const bool bit = key >> k & 1u;
-            const uint64_t m = __ballot(bit);
-            same &= bit ? m : ~m;
+    auto place = [&](int64_t i, int b, int row) FP8K_INLINE {
+        const bool held = b >= 0 && row < p.rows && (p.contiguous || row < (b + 1) * p.max_m);
+        if (p.pos) p.pos[i] = held ? row : -1;
+        if (held) {
+            p.src[row] = (int32_t)i;
+            if (p.contiguous) p.m_indices[row] = b < p.E ? b : -1;
         }
-        const int rank = __popcll(same & ((1ull << lane) - 1)), n = __popcll(same);
-        int at = 0;
-        if (b >= 0) at = next[wave][b] + rank;
-        __builtin_amdgcn_wave_barrier();                // (every lane has read before the last one of its bin writes)
-        if (b >= 0 && rank == n - 1) next[wave][b] = at + 1;
-        __builtin_amdgcn_wave_barrier();
-        if (in) {
-            const bool held = b >= 0 && at < p.rows && (p.contiguous || at < (b + 1) * p.max_m);
-            p.pos[i] = held ? at : -1;
-            if (held) {
-                p.src[at] = (int32_t)i;
-                if (p.contiguous) p.m_indices[at] = b < p.E ? b : -1;
-            }
+    };
+    if constexpr (ROUNDS > 0) {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int64_t i = w_lo + 64 * r + lane;
+            if (i < w_end) place(i, bin[r], (bin[r] >= 0 ? next[wave][bin[r]] : 0) + at[r]);
         }
-    }
-    // what no pair has: counts, and the rows behind a segment's pairs
-    for (int b = c * kSortWaves + wave; b < p.bins; b += chunks * kSortWaves) {
-        const int n = total[b];
-        if (lane == 0 && b < p.E) p.counts[b] = p.contiguous || n < p.max_m ? n : (int)p.max_m;
-        const int64_t s = start[b];
-        int64_t to = p.contiguous ? s + (int64_t)(n + p.align - 1) / p.align * p.align : s + p.max_m;
-        to = to < p.rows ? to : p.rows;
-        for (int64_t r = s + n + lane; r < to; r += 64) {
-            p.src[r] = -1;
-            if (p.contiguous) p.m_indices[r] = -1;
-        }
-    }
-    if (p.contiguous) {
-        for (int64_t r = start[p.bins] + (int64_t)c * kSortThreads + threadIdx.x; r < p.rows; r += (int64_t)chunks * kSortThreads) {
-            p.src[r] = -1;
-            p.m_indices[r] = -1;
+    } else {
+        for (int64_t i0 = w_lo; i0 < w_end; i0 += 64) {
+            const int64_t i = i0 + lane;
+            const int b = i < w_end ? sort_bin(p, i) : -1;
+            const int row = number(b);
+            if (i < w_end) place(i, b, row);
         }
     }
 }

@@ -553,13 +553,13 @@ fp8_status fp8_route_topk_grad(const float* dweights, const void* logits, const 
  * t * k + j being token t's j-th expert: a stable sort by expert.
  *   ids     int32 (id_bytes 4) or int64 (8), (pairs); one outside [0,E) has no
  *           expert.  E <= 1024.
- *   pos     int32 (pairs): the pair's row, or -1
+ *   pos     int32 (pairs): the pair's row, or -1; may be NULL
  *   src     int32 (rows): the row's pair, or -1
  * Contiguous layout (fp8_grouped_gemm_contiguous): the experts' segments
  * follow each other, each in whole `align` rows (a power of two up to 1024;
  * 128 for the grouped GEMM, 16 for fp8_add_adapters).
  *   m_indices int32 (rows): the row's expert, -1 on rows without a pair
- *   counts  int32 (E): each expert's pairs
+ *   counts  int32 (E): each expert's pairs; may be NULL
  *   rows    fp8_expert_rows() always suffices; with fewer, pairs whose row
  *           would lie behind have none (pos -1)
  *   keep    nonzero: pairs without an expert get rows too, in a segment behind
@@ -569,7 +569,8 @@ fp8_status fp8_route_topk_grad(const float* dweights, const void* logits, const 
  * its pairs from the max_m-th on have none.
  *   src     int32 (E*max_m);  masked_m int32 (E): min(pairs, max_m) of each
  * Every output is written whole.  workspace: fp8_expert_sort_workspace_size()
- * bytes, 4-byte aligned, else FP8_ERR_SCRATCH (0 for few pairs); no clearing.
+ * bytes, 16-byte aligned, else FP8_ERR_SCRATCH (0 for few pairs); no clearing;
+ * calls that overlap in time need one each.
  */
 int64_t fp8_expert_rows(int64_t pairs, int32_t E, int32_t align);
 size_t fp8_expert_sort_workspace_size(int64_t pairs, int32_t E);

@@ -88,7 +88,7 @@ def test_given_tables():
     src[3], src[5], src[7] = 4, T, 9            # T: no token
     index[3], index[7] = 2, 0                   # token 9 is not computed: the tile is token 4's
     src[33], src[34], index[33], index[34] = 0, 19, 1, 1
-    out = fp8.add_adapters(x, a, b, s, fp8.AdapterRows(src, index), y, out=torch.full_like(y, 5.0))
+    out = fp8.add_adapters(x, a, b, s, torch.stack((src, index)), y, out=torch.full_like(y, 5.0))
     idx = np.full(T, -1)
     idx[[4, 0, 19]] = 2, 1, 1
     r, err = ref.adapters(_f64(x), _f64(a), _f64(b), _f64(s), idx, _f64(y))
@@ -112,7 +112,7 @@ def test_workspace_and_refusals():
     with pytest.raises(fp8.Fp8GemmError):
         fp8.add_adapters(x, a, b, s, rows, y, workspace=ws[:size - 16])
     for bad in ((x[:9], a, b, s, rows, y), (x, a[:2], b, s, rows, y), (x, a, b[:, :1199].contiguous(), s, rows, y),
-                (x, a, b, s[:2], rows, y), (x, a, b, s, (rows.src, rows.index[:16]), y), (x.t(), a, b, s, rows, y),
+                (x, a, b, s[:2], rows, y), (x, a, b, s, rows[:1], y), (x.t(), a, b, s, rows, y),
                 (x, a, b, s, rows, y.cpu())):
         with pytest.raises(ValueError):
             fp8.add_adapters(*bad)

@@ -37,7 +37,7 @@ def _ids(rng, shape, E, kind):
 
 
 @pytest.mark.parametrize("E", [1, 3, 16, 64, 255, 256, 1000, 1024])
-@pytest.mark.parametrize("shape", [(0, 2), (1, 1), (1, 8), (63, 1), (65, 1), (300, 5), (1024, 8), (2731, 3), (5000, 4)])
+@pytest.mark.parametrize("shape", [(0, 2), (1, 1), (1, 8), (63, 1), (65, 1), (300, 5), (1024, 2), (1025, 2), (2731, 3), (5000, 4)])
 def test_sort_contiguous(E, shape):
     rng = np.random.default_rng(E + shape[0])
     for kind, dtype, align, keep in (("even", torch.int32, 128, False), ("outside", torch.int64, 16, True),
@@ -70,9 +70,9 @@ def test_sort_masked(E, max_m):
 
 
 def test_sort_of_many_pairs():
-    """As many chunks as there can be, larger than the smallest."""
+    """As many chunks as there can be, of each kernel's size."""
     rng = np.random.default_rng(9)
-    for n, E in ((700000, 40), (530000, 1024)):
+    for n, E in ((262145, 256), (700000, 40), (530000, 1024), (1200001, 17)):
         say("sort", n, E)
         a = _ids(rng, (n,), E, "outside")
         most = fp8.expert_rows(n, E)

@@ -46,21 +46,20 @@ def test_route_validation(L):
 def test_sort_validation(L):
     def call(ids=A, size=4, n=10, E=4, align=128, rows=640, pos=A, src=A, idx=A, counts=A, ws=None, ws_bytes=0):
         return L.fp8_expert_sort_contiguous(ids, size, n, E, align, rows, 0, pos, src, idx, counts, ws, ws_bytes, None)
-    assert call(ids=None) == INVALID and call(pos=None) == INVALID and call(src=None) == INVALID
-    assert call(idx=None) == INVALID and call(counts=None) == INVALID
+    assert call(ids=None) == INVALID and call(src=None) == INVALID and call(idx=None) == INVALID
     assert call(size=2) == INVALID and call(n=-1) == INVALID and call(E=0) == INVALID and call(rows=-1) == INVALID
     assert call(align=0) == INVALID and call(align=48) == INVALID and call(align=2048) == INVALID
     assert call(ws_bytes=4) == INVALID
     assert call(E=1025) == UNSUP and call(n=(1 << 30) + 1) == UNSUP
-    assert call(ids=P(4100), size=8) == ALIGN and call(pos=P(4098)) == ALIGN and call(ws=P(4098), ws_bytes=400) == ALIGN
-    assert call(n=8193) == SCRATCH and call(n=100000, ws=A, ws_bytes=16) == SCRATCH
+    assert call(ids=P(4100), size=8) == ALIGN and call(pos=P(4098)) == ALIGN and call(ws=P(4104), ws_bytes=400) == ALIGN
+    assert call(n=2049) == SCRATCH and call(n=100000, ws=A, ws_bytes=16) == SCRATCH
 
     def masked(ids=A, E=4, max_m=16, src=A, m=A):
         return L.fp8_expert_sort_masked(ids, 4, 10, E, max_m, A, src, m, None, 0, None)
     assert masked(ids=None) == INVALID and masked(src=None) == INVALID and masked(m=None) == INVALID
     assert masked(max_m=-1) == INVALID and masked(E=1024, max_m=1 << 21) == UNSUP
-    assert L.fp8_expert_sort_workspace_size(8192, 256) == 0
-    assert L.fp8_expert_sort_workspace_size(8193, 256) == 5 * 257 * 4
+    assert L.fp8_expert_sort_workspace_size(2048, 256) == 0
+    assert L.fp8_expert_sort_workspace_size(2049, 256) == 4 * 257 * 4       # three chunks, a multiple of 4
     assert L.fp8_expert_sort_workspace_size(-1, 256) == 0 and L.fp8_expert_sort_workspace_size(10, 2000) == 0
     for n in (8193, 1 << 20, 1 << 30):       # at most 256 chunks
         assert L.fp8_expert_sort_workspace_size(n, 1024) <= 256 * 1025 * 4
