@@ -300,6 +300,7 @@ fp8_status fp8_expert_dispatch_quant(const void* x, const int32_t* pos, uint8_t*
     p.x = x; p.out = xq; p.sa = sa; p.pos = pos; p.T = T; p.rows = rows; p.W = K; p.k = k;
     dim3 grid;
     const fp8_status g = rows_grid(p, 1024, &grid);
+    grid.x = (grid.x + 7) / 8 * 8;
     if (g != FP8_OK) return g;
     const hipStream_t s = (hipStream_t)stream;
     const bool pow2 = flags & FP8_FLAG_UE8M0;
