@@ -274,7 +274,7 @@ struct RowsParams {
 constexpr int kClearRows = 8;
 
 // Zeros to the rows of a group of kClearRows that no pair has.
-template <typename T>
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ void clear_rows(const RowsParams& p, int64_t group, int lane) {
     const int64_t r0 = group * kClearRows;
     const bool none = lane < kClearRows && r0 + lane < p.rows && p.src[r0 + lane] < 0;
@@ -284,7 +284,7 @@ __device__ __forceinline__ void clear_rows(const RowsParams& p, int64_t group, i
         left &= left - 1;
         T* row = static_cast<T*>(p.out) + r * p.W;
         for (int64_t n = lane * RowElem<T>::VN; n < p.W; n += 64 * RowElem<T>::VN)
-            store_row16<T>(row + n, p.W - n, i32x4{0, 0, 0, 0});
+            store_row16<T, STREAM>(row + n, p.W - n, i32x4{0, 0, 0, 0});
     }
 }
 
@@ -323,9 +323,12 @@ __global__ __launch_bounds__(256) void expert_dispatch_kernel(RowsParams p) {
 // group) and stores them at the token's k places.  The scales of one K block
 // lie beside those of the expert's neighbouring tokens, 4 bytes each: every die
 // takes a run of consecutive tokens, whose pieces of a line then meet in its
-// cache (8192 x 8 of 256 experts, K 7168: tokens dealt out to the dies in turn
-// 139 us, so 127; 1024 x 8 of 64 17.7, 14.6).
-template <typename T, bool POW2>
+// cache (1024 x 8 of 64 experts, K 7168: tokens dealt out to the dies in turn
+// 17.7 us, so 14.6).  STREAM: codes that do not fit the last-level cache are
+// stored past the caches, which then keep those lines (8192 x 8 of 256 experts,
+// 470 MB of codes: 150 us, so 120, as long as without any scales; 67 MB: no
+// difference).
+template <typename T, bool POW2, bool STREAM>
 __global__ __launch_bounds__(256) void expert_dispatch_quant_kernel(RowsParams p) {
     constexpr int VN = RowElem<T>::VN;
     // (a grid of whole 8s: block b runs on die b % 8)
@@ -356,14 +359,19 @@ __global__ __launch_bounds__(256) void expert_dispatch_quant_kernel(RowsParams p
     for (int j = 0; j < p.k; ++j) {
         const int64_t row = uniform(p.pos[t * p.k + j]);
         if (row < 0 || row >= p.rows || !in) continue;
-        *reinterpret_cast<i32x4*>(static_cast<uint8_t*>(p.out) + row * p.W + n) = q;
+        i32x4* out = reinterpret_cast<i32x4*>(static_cast<uint8_t*>(p.out) + row * p.W + n);
+        if constexpr (STREAM) __builtin_nontemporal_store(q, out);
+        else *out = q;
         if ((lane & 7) == 0) p.sa[kb * p.rows + row] = s;
     }
 }
 
 constexpr int kCombineVecs = 2; // 16-byte vectors of a lane per row and run
 
-template <typename T>
+// STREAM: rows of whole cache lines are read with the nontemporal hint, each
+// once (8192 x 8, N 7168: 209 us without, 195 with it; 4096 x 2 35.5, 30.9; rows
+// of 3060 bytes, which share lines, 11.1, 12.6).
+template <typename T, bool STREAM>
 __global__ __launch_bounds__(256) void expert_combine_kernel(RowsParams p) {
     constexpr int VN = RowElem<T>::VN;
     const int64_t u = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
@@ -384,7 +392,7 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(RowsParams p) {
             for (int i = 0; i < kCombineVecs; ++i) {
                 const int64_t n = n0 + i * 64 * VN;
                 v[j][i] = i32x4{0, 0, 0, 0};
-                if (held && n < p.W) v[j][i] = load_row16<T>(static_cast<const T*>(p.x) + row * p.W + n, p.W - n);
+                if (held && n < p.W) v[j][i] = load_row16<T, STREAM>(static_cast<const T*>(p.x) + row * p.W + n, p.W - n);
             }
         }
 #pragma unroll
@@ -401,26 +409,27 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(RowsParams p) {
     }
 }
 
-// A workgroup takes a token: dout is read once per 4 of its pairs, each row of
-// y once.
-constexpr int kGradPairs = 4;
-
-template <typename T>
+// A workgroup takes a token: dout is read once per PAIRS of its pairs, each row
+// of y once.  STREAM: rows of whole cache lines are read and written with the
+// nontemporal hint (4096 x 2, N 7168: 66 us without, 55 with it, and 117, 115
+// with a pass that reads dy; 1024 x 8 86, 76; 8192 x 8 510, 496; rows of 3060
+// bytes 26.4, 26.9).
+template <typename T, int PAIRS, bool STREAM>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(RowsParams p) {
     constexpr int VN = RowElem<T>::VN;
-    __shared__ float part[4][kGradPairs];
+    __shared__ float part[4][PAIRS];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t t = blockIdx.x;
     if (t >= p.work) {
-        if (p.src) clear_rows<T>(p, (t - p.work) * 4 + wave, lane);
+        if (p.src) clear_rows<T, STREAM>(p, (t - p.work) * 4 + wave, lane);
         return;
     }
     const T* dout = static_cast<const T*>(p.x) + t * p.W;
-    for (int j0 = 0; j0 < p.k; j0 += kGradPairs) {
-        int64_t row[kGradPairs];
-        float w[kGradPairs], acc[kGradPairs] = {};
+    for (int j0 = 0; j0 < p.k; j0 += PAIRS) {
+        int64_t row[PAIRS];
+        float w[PAIRS], acc[PAIRS] = {};
 #pragma unroll
-        for (int j = 0; j < kGradPairs; ++j) {
+        for (int j = 0; j < PAIRS; ++j) {
             const int64_t at = t * p.k + j0 + j;
             row[j] = j0 + j < p.k ? (int64_t)uniform(p.pos[at]) : -1;
             if (row[j] >= p.rows) row[j] = -1;
@@ -428,14 +437,14 @@ __global__ __launch_bounds__(256) void expert_combine_grad_kernel(RowsParams p) 
         }
         for (int64_t n = threadIdx.x * VN; n < p.W; n += 256 * VN) {
             const i32x4 d = load_row16<T>(dout + n, p.W - n);
-            i32x4 v[kGradPairs];
+            i32x4 v[PAIRS];
 #pragma unroll
-            for (int j = 0; j < kGradPairs; ++j) {
+            for (int j = 0; j < PAIRS; ++j) {
                 v[j] = i32x4{0, 0, 0, 0};
-                if (p.dw && row[j] >= 0) v[j] = load_row16<T>(static_cast<const T*>(p.y) + row[j] * p.W + n, p.W - n);
+                if (p.dw && row[j] >= 0) v[j] = load_row16<T, STREAM>(static_cast<const T*>(p.y) + row[j] * p.W + n, p.W - n);
             }
 #pragma unroll
-            for (int j = 0; j < kGradPairs; ++j) {
+            for (int j = 0; j < PAIRS; ++j) {
                 float s[VN];
 #pragma unroll
                 for (int e = 0; e < VN; ++e) {
@@ -444,19 +453,19 @@ __global__ __launch_bounds__(256) void expert_combine_grad_kernel(RowsParams p) 
                     s[e] = w[j] * g;
                 }
                 if (p.out && row[j] >= 0)
-                    store_row16<T>(static_cast<T*>(p.out) + row[j] * p.W + n, p.W - n, RowElem<T>::pack(s));
+                    store_row16<T, STREAM>(static_cast<T*>(p.out) + row[j] * p.W + n, p.W - n, RowElem<T>::pack(s));
             }
         }
         if (p.dw) {
 #pragma unroll
-            for (int j = 0; j < kGradPairs; ++j) {
+            for (int j = 0; j < PAIRS; ++j) {
                 // (a pair without a row has no product, even of an infinite dout)
                 const float s = wave_sum(acc[j]);
                 if (lane == 0) part[wave][j] = row[j] >= 0 ? s : 0.f;
             }
             __syncthreads();
             const int j = threadIdx.x;
-            if (j < kGradPairs && j0 + j < p.k)
+            if (j < PAIRS && j0 + j < p.k)
                 p.dw[t * p.k + j0 + j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
             __syncthreads();
         }

@@ -115,6 +115,12 @@ fp8_status check_rows(int64_t T, int32_t k, int64_t rows, int64_t W, int32_t typ
     return FP8_OK;
 }
 
+// Codes of more bytes than the last-level cache holds are stored past the caches.
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
+// Rows of whole cache lines, which no other row shares.
+constexpr size_t kLine = 128;
+bool whole_lines(int64_t W, int32_t type, const void* p) { return W * (int64_t)type_size(type) % kLine == 0 && aligned(p, kLine); }
+
 // Waves (4 a workgroup) that move rows, and those that look for rows to clear.
 fp8_status rows_grid(fp8k::RowsParams& p, int64_t per_seg, dim3* grid) {
     p.segs = cdiv(p.W, per_seg);
@@ -304,12 +310,14 @@ fp8_status fp8_expert_dispatch_quant(const void* x, const int32_t* pos, uint8_t*
     if (g != FP8_OK) return g;
     const hipStream_t s = (hipStream_t)stream;
     const bool pow2 = flags & FP8_FLAG_UE8M0;
+    const bool past = T * k * K > kCacheBytes;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p); };
     if (type == FP8_TYPE_F32) {
-        if (pow2) hipLaunchKernelGGL((fp8k::expert_dispatch_quant_kernel<float, true>), grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((fp8k::expert_dispatch_quant_kernel<float, false>), grid, dim3(256), 0, s, p);
+        if (past) pow2 ? go(fp8k::expert_dispatch_quant_kernel<float, true, true>) : go(fp8k::expert_dispatch_quant_kernel<float, false, true>);
+        else pow2 ? go(fp8k::expert_dispatch_quant_kernel<float, true, false>) : go(fp8k::expert_dispatch_quant_kernel<float, false, false>);
     } else {
-        if (pow2) hipLaunchKernelGGL((fp8k::expert_dispatch_quant_kernel<uint16_t, true>), grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((fp8k::expert_dispatch_quant_kernel<uint16_t, false>), grid, dim3(256), 0, s, p);
+        if (past) pow2 ? go(fp8k::expert_dispatch_quant_kernel<uint16_t, true, true>) : go(fp8k::expert_dispatch_quant_kernel<uint16_t, false, true>);
+        else pow2 ? go(fp8k::expert_dispatch_quant_kernel<uint16_t, true, false>) : go(fp8k::expert_dispatch_quant_kernel<uint16_t, false, false>);
     }
     return launch_status();
 }
@@ -330,8 +338,10 @@ fp8_status fp8_expert_combine(const void* y, const int32_t* pos, const float* we
     dim3 grid;
     const fp8_status g = rows_grid(p, 64 * fp8k::kCombineVecs * 16 / (int64_t)type_size(type), &grid);
     if (g != FP8_OK) return g;
-    if (type == FP8_TYPE_F32) hipLaunchKernelGGL(fp8k::expert_combine_kernel<float>, grid, dim3(256), 0, (hipStream_t)stream, p);
-    else hipLaunchKernelGGL(fp8k::expert_combine_kernel<uint16_t>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    const bool lines = whole_lines(N, type, y);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)stream, p); };
+    if (type == FP8_TYPE_F32) lines ? go(fp8k::expert_combine_kernel<float, true>) : go(fp8k::expert_combine_kernel<float, false>);
+    else lines ? go(fp8k::expert_combine_kernel<uint16_t, true>) : go(fp8k::expert_combine_kernel<uint16_t, false>);
     return launch_status();
 }
 
@@ -357,8 +367,15 @@ fp8_status fp8_expert_combine_grad(const void* dout, const void* y, const int32_
     const int64_t wgs = T + (p.src ? cdiv(rows, 4 * fp8k::kClearRows) : 0);
     if (wgs > kMaxGrid) return FP8_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)wgs);
-    if (type == FP8_TYPE_F32) hipLaunchKernelGGL(fp8k::expert_combine_grad_kernel<float>, grid, dim3(256), 0, (hipStream_t)stream, p);
-    else hipLaunchKernelGGL(fp8k::expert_combine_grad_kernel<uint16_t>, grid, dim3(256), 0, (hipStream_t)stream, p);
+    const bool few = k <= 4, lines = whole_lines(N, type, y) && aligned(dy, kLine);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)stream, p); };
+    if (type == FP8_TYPE_F32) {
+        if (lines) few ? go(fp8k::expert_combine_grad_kernel<float, 4, true>) : go(fp8k::expert_combine_grad_kernel<float, 8, true>);
+        else few ? go(fp8k::expert_combine_grad_kernel<float, 4, false>) : go(fp8k::expert_combine_grad_kernel<float, 8, false>);
+    } else {
+        if (lines) few ? go(fp8k::expert_combine_grad_kernel<uint16_t, 4, true>) : go(fp8k::expert_combine_grad_kernel<uint16_t, 8, true>);
+        else few ? go(fp8k::expert_combine_grad_kernel<uint16_t, 4, false>) : go(fp8k::expert_combine_grad_kernel<uint16_t, 8, false>);
+    }
     return launch_status();
 }
 

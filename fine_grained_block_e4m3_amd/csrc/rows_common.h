@@ -37,11 +37,16 @@ struct RowElem<uint16_t> {      // BF16 bits
 
 // The 16 bytes at p, of which `left` elements (more than none) belong to the
 // row: whole vectors at any alignment, a row's last ones element by element.
-template <typename T>
+// STREAM: with the nontemporal hint, for what is read once or does not fit the
+// caches.
+typedef i32x4 i32x4_any __attribute__((aligned(2)));
+
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ i32x4 load_row16(const T* p, int64_t left) {
     i32x4 v{0, 0, 0, 0};
     if (left >= RowElem<T>::VN) {
-        __builtin_memcpy(&v, p, 16);
+        if constexpr (STREAM) v = __builtin_nontemporal_load(reinterpret_cast<const i32x4_any*>(p));
+        else __builtin_memcpy(&v, p, 16);
     } else {
 #pragma unroll
         for (int i = 0; i < RowElem<T>::VN - 1; ++i) {
@@ -53,10 +58,11 @@ __device__ __forceinline__ i32x4 load_row16(const T* p, int64_t left) {
     }
     return v;
 }
-template <typename T>
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ void store_row16(T* p, int64_t left, i32x4 v) {
     if (left >= RowElem<T>::VN) {
-        __builtin_memcpy(p, &v, 16);
+        if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<i32x4_any*>(p));
+        else __builtin_memcpy(p, &v, 16);
     } else {
 #pragma unroll
         for (int i = 0; i < RowElem<T>::VN - 1; ++i) {
