@@ -181,7 +181,12 @@ template <int RS>
 void launch_adapter_up(const fp8k::AdapterParams& p, const AdapterPlan& pl, hipStream_t s) {
     const int64_t wgs = pl.groups * p.parts;
     if (pl.group == 1) hipLaunchKernelGGL((fp8k::adapter_up_kernel<RS>), dim3((unsigned)wgs), dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((fp8k::adapter_up_group_kernel<RS>), dim3((unsigned)(cdiv(wgs, 8) * 8)), dim3(256), 0, s, p, pl.groups);
+    else {
+        const dim3 grid((unsigned)(cdiv(wgs, 8) * 8));
+        const bool lines = whole_lines(p.N, FP8_TYPE_BF16, p.y) && aligned(p.out, kLine);
+        if (lines) hipLaunchKernelGGL((fp8k::adapter_up_group_kernel<RS, true>), grid, dim3(256), 0, s, p, pl.groups);
+        else hipLaunchKernelGGL((fp8k::adapter_up_group_kernel<RS, false>), grid, dim3(256), 0, s, p, pl.groups);
+    }
 }
 
 }  // namespace
