@@ -146,20 +146,24 @@ struct AdapterPlan {
 // 2000, R 64 35 / 30; 8192, R 16 67 / 48 and R 64 136 / 65; 100 adapters, 4000
 // tokens, R 32 52 / 50; 200 adapters 53 / 72.
 // Workgroups per compute unit: along K two (tiles) or four (groups: one more
-// than fit, so that the last round is short), along N four or eight; parts of K
-// of 512 and parts of N of 256 at least.
+// than fit, so that the last round is short; 8192 tokens, R 64: 4 splits 65 us,
+// 5 64, 7 62, 10 70), along N four or eight; parts of K of 512 and parts of N of
+// 256 at least.  A single tile has 8 splits at most, whose sums are loaded at
+// once (one token, R 16, 14 splits of 512 3.2 + 5.7 us, 8 of 896 3.6 + 4.7; R 64
+// 4.9 + 8.8, 6.2 + 6.3).
 AdapterPlan adapter_plan(int64_t T, int64_t L, int64_t rows, int64_t N, int64_t K, int64_t R, int cus) {
     AdapterPlan pl{};
     pl.tiles = rows / 16;
     pl.group = T >= 64 * (L + 1) && T * R >= 96 << 10 ? 4 : 1;
     pl.groups = std::max<int64_t>(cdiv(pl.tiles, pl.group), 1);
-    auto share = [&](int64_t len, int64_t least, int64_t step, int64_t wgs) {
-        const int64_t parts = std::clamp(wgs / pl.groups, (int64_t)1, std::max<int64_t>(cdiv(len, least), 1));
+    auto share = [&](int64_t len, int64_t most, int64_t step, int64_t wgs) {
+        const int64_t parts = std::clamp(wgs / pl.groups, (int64_t)1, std::max<int64_t>(most, 1));
         return std::max(cdiv(cdiv(len, parts), step), (int64_t)1) * step;
     };
-    pl.k_range = share(K, 512, 128, (pl.group == 1 ? 2 : 4) * cus);
+    const int64_t k_most = cdiv(K, 512);
+    pl.k_range = share(K, pl.group == 1 ? std::min<int64_t>(k_most, 8) : k_most, 128, (pl.group == 1 ? 2 : 4) * cus);
     pl.splits = cdiv(K, pl.k_range);
-    pl.n_range = share(N, 256, 256, (pl.group == 1 ? 4 : 8) * cus);
+    pl.n_range = share(N, cdiv(N, 256), 256, (pl.group == 1 ? 4 : 8) * cus);
     return pl;
 }
 
