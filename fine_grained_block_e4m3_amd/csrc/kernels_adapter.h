@@ -395,7 +395,7 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterParams p) {
 // N 2048, both kernels: R 64 69 us without, 62 with it, R 16 55, 47; 3000 tokens
 // whose y stays cached 34.7, 35.6).
 template <int RS, bool STREAM>
-__global__ __launch_bounds__(256) void adapter_up_group_kernel(AdapterParams p, int64_t groups) {
+__global__ __launch_bounds__(256, RS <= 2 ? 4 : 2) void adapter_up_group_kernel(AdapterParams p, int64_t groups) {
     constexpr int ZROW = 32 * RS + 8;       // elements; 16 rows at one place cover all banks
     constexpr int DROW = 68;
     __shared__ __attribute__((aligned(16))) uint16_t zp[2][64][ZROW];
