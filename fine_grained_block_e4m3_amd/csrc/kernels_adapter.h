@@ -20,6 +20,10 @@
 // 16 bits of it (one part would cost 2^-9 of the added term) and costs only
 // instructions that wait anyway.
 //
+// Measured (one MI355X, the two kernels, K 7168): 1 token, R 16, N 2048 3.7 + 5.0
+// us; 100 tokens of 64 adapters, N 2112 5.8 + 5.2; 8192 tokens of 8, R 64, N
+// 2048 30 + 27 (4.3 and 3.1 TB/s).
+//
 // The index of a tile is that of its first row with a token; a row of another
 // index is not computed.  Rows of an index outside the adapters take y as it is.
 #pragma once

