@@ -17,7 +17,7 @@
 //           that is the bound.)
 // Both are bounded by memory otherwise; the products are a few operations per
 // byte.  z enters the second product as the sum of two BF16 values, which keeps
-// 16 bits of it (one part would cost 2^-9 of the added term) and costs only
+// 16 bits of it (one part could cost 2^-8 of the added term) and costs only
 // instructions that wait anyway.
 //
 // Measured (one MI355X, the two kernels, K 7168): 1 token, R 16, N 2048 3.7 + 5.0
