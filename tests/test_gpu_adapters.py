@@ -70,7 +70,8 @@ def test_many_tiles():
     """So many tokens per adapter that a workgroup takes four tiles, of one adapter, of two, of one and none."""
     rng = np.random.default_rng(2)
     for T, L, R, K, N, group in ((8301, 5, 16, 128, 72, 4), (4000, 300, 24, 256, 130, 1), (2700, 40, 64, 384, 65, 4),
-                                 (3080, 12, 32, 2048, 600, 4), (1000, 3, 128, 1152, 340, 4), (1400, 5, 72, 640, 128, 4)):
+                                 (3080, 12, 32, 2048, 600, 4), (3080, 12, 32, 512, 640, 4), (2000, 3, 64, 256, 192, 4),
+                                 (1000, 3, 128, 1152, 340, 4), (1400, 5, 72, 640, 128, 4)):
         idx = rng.integers(-1, L, T)
         assert fp8.adapters_plan(T, L, N, K, R)["group"] == group
         say("adapters many tiles", T, L, R)

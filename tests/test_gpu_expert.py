@@ -142,6 +142,52 @@ def test_rows_there_and_back(W, kind):
             assert dw_full[0] == 9 and dw_full[-1] == 9
 
 
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("k", [1, 4, 5, 8, 9, 17])
+def test_rows_of_whole_lines(kind, k):
+    """Buffers at line boundaries and beside them take different loads and
+    stores: one result, the 64-bit form's."""
+    rng = np.random.default_rng(k)
+    dtype = TYPES[kind]
+    for T, rows, W in ((3, 20, 64), (30, 300, 1024), (9, 64, 7168)):
+        say("whole lines", kind, k, T, W)
+        pos, src = _places(rng, T, k, rows)
+        dpos, dsrc = torch.from_numpy(pos).cuda(), torch.from_numpy(src).cuda()
+        y = torch.from_numpy(rng.normal(size=(rows, W)).astype(np.float32)).to(dtype).cuda()
+        dout = torch.from_numpy(rng.normal(size=(T, W)).astype(np.float32)).to(dtype).cuda()
+        w = torch.from_numpy(rng.normal(size=(T, k)).astype(np.float32)).cuda()
+        beside = torch.empty(rows * W + 8, dtype=dtype, device="cuda")[8:].view(rows, W)
+        beside.copy_(y)
+        assert y.data_ptr() % 128 == 0 and beside.data_ptr() % 128 != 0
+        out = fp8.expert_combine(y, dpos, w)
+        assert torch.equal(out, fp8.expert_combine(beside, dpos, w))
+        r, mag = ref.combine(y.double().cpu().numpy(), pos, w.double().cpu().numpy())
+        ref.assert_near(out.double().cpu().numpy(), r, ref.rounded((k + 1) * ref.U * mag, r, kind == "bf16"), "combine")
+        dy, dw = fp8.expert_combine_grad(dout, y, dpos, w, dsrc)
+        dy2, dw2 = fp8.expert_combine_grad(dout, beside, dpos, w, dsrc)
+        assert torch.equal(dy, dy2) and torch.equal(dw, dw2)
+        rdy, rdw, mag = ref.combine_grad(dout.double().cpu().numpy(), y.double().cpu().numpy(), pos, w.double().cpu().numpy(),
+                                         np.zeros((rows, W)))
+        ref.assert_near(dy.double().cpu().numpy(), rdy, ref.rounded(ref.U * np.abs(rdy), rdy, kind == "bf16"), "dy")
+        ref.assert_near(dw.double().cpu().numpy(), rdw, (W / 64 + 24) * ref.U * mag + 1e-300, "dw")
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_codes_larger_than_the_caches(kind, pow2):
+    """Over 256 MB of codes, against the quantizer's."""
+    say("large codes", kind, pow2)
+    T, K = 40000, 7168
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn((T, K), generator=gen, device="cuda").to(TYPES[kind])
+    ids = torch.randint(0, 7, (T, 1), generator=gen, device="cuda", dtype=torch.int32)
+    pos, src, _, _ = fp8.expert_sort(ids, 7)
+    xq, sa = fp8.expert_dispatch_quant(x, pos, src.shape[0], ue8m0=pow2)
+    q, s = fp8.quant_1x128(x.float(), ue8m0=pow2)
+    at = pos[:, 0].long()
+    assert torch.equal(xq[at], q) and torch.equal(sa[:, at], s)
+
+
 def test_gradients_alone():
     """Each of the two gradients without the other; y is not read for dy."""
     say("gradients alone")

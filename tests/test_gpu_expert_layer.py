@@ -104,6 +104,33 @@ def test_chain_against_the_oracle(layout, max_m, T, E, k):
     ref.assert_near(out.double().cpu().numpy(), want, ref.rounded(mag, want, True), "chain")
 
 
+@pytest.mark.parametrize("layout", ["contiguous", "masked"])
+@pytest.mark.parametrize("fast", [False, True])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_unused_rows_may_hold_anything(layout, fast, pow2):
+    """Every grouped path: rows without a token as NaN codes and scales, or as zeros."""
+    say("unused rows", layout, fast, pow2)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    T, E, k, K, N, max_m = 333, 7, 3, 512, 384, 256
+    wq, sb = fp8.quant_128x128(torch.randn((E * N, K), generator=gen, device="cuda") * 0.05, ue8m0=pow2)
+    wq, sb = wq.view(E, N, K), sb.view(E, N // 128, K // 128)
+    x = torch.randn((T, K), generator=gen, device="cuda").bfloat16()
+    w, ids = fp8.route_topk(torch.randn((T, E), generator=gen, device="cuda"), k)
+    got = []
+    for code, scale in ((0, 0.0), (0x7F, float("nan"))):
+        if layout == "masked":
+            pos, src, m = fp8.expert_sort_masked(ids, E, max_m)
+        else:
+            pos, src, m, _ = fp8.expert_sort(ids, E)
+        shape = (E, max_m) if layout == "masked" else src.shape[0]
+        xq = torch.full((E, max_m, K) if layout == "masked" else (shape, K), code, dtype=torch.uint8, device="cuda")
+        sa = torch.full((K // 128, src.shape[0]), scale, device="cuda")
+        fp8.expert_dispatch_quant(x, pos, shape, ue8m0=pow2, out=(xq, sa))
+        product = fp8.grouped_gemm_masked if layout == "masked" else fp8.grouped_gemm_contiguous
+        got.append(fp8.expert_combine(product(xq, sa, wq, sb, m, ue8m0=pow2, fast_accum=fast), pos, w))
+    assert bool(torch.isfinite(got[0].float()).all()) and torch.equal(got[0], got[1])
+
+
 @pytest.mark.parametrize("layout,max_m", [("contiguous", 0), ("masked", 64)])
 def test_chain_in_a_graph(layout, max_m):
     """Captured once, replayed on changing tokens and choices, against eager."""
