@@ -127,7 +127,8 @@ class GatedGradPlan(ctypes.Structure):
 class AdaptersPlan(ctypes.Structure):
     """fp8_adapters_plan_t: the kernels a call of add_adapters launches."""
     _fields_ = [("tiles", ctypes.c_int64), ("k_splits", ctypes.c_int64), ("k_range", ctypes.c_int64),
-                ("n_range", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t), ("group", ctypes.c_int32)]
+                ("n_range", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t), ("group", ctypes.c_int32),
+                ("whole", ctypes.c_int32)]
     as_dict = GemmPlan.as_dict
 
 

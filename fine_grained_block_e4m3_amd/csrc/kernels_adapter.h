@@ -4,25 +4,28 @@
 //
 // The tokens come sorted by adapter in tiles of 16 rows (src: the token of a
 // row or -1, index: its adapter), which is one dimension of the matrix
-// instruction.  Two kernels: the first forms z = x A^T, K split over waves and
-// workgroups, the second adds z's sums, multiplies by B^T and adds y, N split.
-// Each has two forms:
-//   tiles   a workgroup per tile: few tokens per adapter, A and B are most of
-//           what is read, and the operands come straight into registers
-//   groups  a workgroup per four tiles, which mostly share an adapter: x and y
-//           are most of what is read, in whole 128-byte pieces of their rows
-//           through LDS.  (The matrix instruction's layout, 16 rows of 64 bytes
-//           per load, comes at 36 GB/s per compute unit from L2, pieces of 128
-//           bytes at 80, whole kilobytes at 105, measured: with many tokens
-//           that is the bound.)
-// Both are bounded by memory otherwise; the products are a few operations per
+// instruction.  Three forms:
+//   whole   one kernel, a few workgroups per tile that each form z = x A^T of
+//           their tokens by dot products: a token or two per adapter
+//   tiles   two kernels: the first forms z, K split over waves and workgroups,
+//           the second adds z's sums, multiplies by B^T and adds y, N split; a
+//           workgroup per tile and split.  Few tokens per adapter: A and B are
+//           most of what is read, and the operands come straight into registers
+//   groups  the two kernels with a workgroup per four tiles, which mostly share
+//           an adapter: x and y are most of what is read, in whole 128-byte
+//           pieces of their rows through LDS.
+// (The matrix instruction's layout, 16 rows of 64 bytes per load, comes at 36
+// GB/s per compute unit from L2, pieces of 128 bytes at 80, whole kilobytes at
+// 105, measured: that is why whole multiplies by rows, and why many tokens go
+// through LDS.)
+// All are bounded by memory otherwise; the products are a few operations per
 // byte.  z enters the second product as the sum of two BF16 values, which keeps
 // 16 bits of it (one part could cost 2^-8 of the added term) and costs only
 // instructions that wait anyway.
 //
-// Measured (one MI355X, the two kernels, K 7168): 1 token, R 16, N 2048 3.7 + 5.0
-// us; 100 tokens of 64 adapters, N 2112 5.8 + 5.2; 8192 tokens of 8, R 64, N
-// 2048 30 + 27 (4.3 and 3.1 TB/s).
+// Measured (one MI355X, K 7168): 1 token, R 16, N 2048 6.0 us (one kernel); 100
+// tokens of 64 adapters, N 2112 9.6 (one kernel); 8192 tokens of 8, R 64, N 2048 30 + 27
+// (two; 4.3 and 3.1 TB/s).
 //
 // The index of a tile is that of its first row with a token; a row of another
 // index is not computed.  Rows of an index outside the adapters take y as it is.
@@ -335,6 +338,45 @@ __device__ __forceinline__ void adapter_z_sum(const AdapterParams& p, int64_t ro
 // are the columns 16 (i / 4) + 4 j + i % 4 (i the row, j the product), so that a
 // lane ends with 16 columns in a row of token l % 16.
 template <int RS>
+__device__ __forceinline__ void adapter_up_load(const AdapterParams& p, const AdapterTile& t, int64_t n, int lane,
+                                                bf16x8 (&w)[4][RS], i32x4 (&base)[2]) {
+    const int g = lane >> 4, i = lane & 15;
+    if (t.adds) adapter_b_load<RS>(p, t.index, [&](int j) FP8K_INLINE { return n + 16 * (i >> 2) + 4 * j + (i & 3); }, g, w);
+    const int64_t c0 = n + 16 * g;
+    const uint16_t* y = p.y + t.token * p.N + c0;
+    if (n + 64 <= p.N) {                    // (lanes without a token of their own read another's)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) __builtin_memcpy(&base[h], y + 8 * h, 16);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            base[h] = i32x4{0, 0, 0, 0};
+            if (c0 + 8 * h < p.N) base[h] = load_row16<uint16_t>(y + 8 * h, p.N - c0 - 8 * h);
+        }
+    }
+}
+template <int RS>
+__device__ __forceinline__ void adapter_up_store(const AdapterParams& p, const AdapterTile& t, int64_t n, int lane,
+                                                 const bf16x8 (&w)[4][RS], const bf16x8 (&hi)[RS], const bf16x8 (&lo)[RS],
+                                                 const i32x4 (&base)[2]) {
+    f32x4 acc[4] = {};
+    if (t.adds) adapter_multiply<RS>(w, hi, lo, acc);
+    if (!t.valid) return;
+    const int64_t c0 = n + 16 * (lane >> 4);
+    uint16_t* out = p.out + t.token * p.N + c0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = RowElem<uint16_t>::get(base[h], e) + acc[2 * h + (e >> 2)][e & 3];
+        // (without an adapter y goes through as it is, the sign of a zero too)
+        const i32x4 v = t.adds ? RowElem<uint16_t>::pack(f) : base[h];
+        if (n + 64 <= p.N) __builtin_memcpy(out + 8 * h, &v, 16);
+        else if (c0 + 8 * h < p.N) store_row16<uint16_t>(out + 8 * h, p.N - c0 - 8 * h, v);
+    }
+}
+
+template <int RS>
 __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterParams p) {
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int g = lane >> 4, i = lane & 15;
@@ -343,25 +385,9 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterParams p) {
     if (n0 >= n_end) return;
     const AdapterTile t = adapter_tile(p, tile, lane);
     if (!t.any || (!t.adds && p.out == p.y)) return;
-    bf16x8 w[4][RS];
+    bf16x8 w[4][RS], hi[RS], lo[RS];
     i32x4 base[2];
-    auto load = [&](int64_t n) FP8K_INLINE {
-        if (t.adds) adapter_b_load<RS>(p, t.index, [&](int j) FP8K_INLINE { return n + 16 * (i >> 2) + 4 * j + (i & 3); }, g, w);
-        const int64_t c0 = n + 16 * g;
-        const uint16_t* y = p.y + t.token * p.N + c0;
-        if (n + 64 <= p.N) {                // (lanes without a token of their own read another's)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) __builtin_memcpy(&base[h], y + 8 * h, 16);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                base[h] = i32x4{0, 0, 0, 0};
-                if (c0 + 8 * h < p.N) base[h] = load_row16<uint16_t>(y + 8 * h, p.N - c0 - 8 * h);
-            }
-        }
-    };
-    load(n0);
-    bf16x8 hi[RS], lo[RS];
+    adapter_up_load<RS>(p, t, n0, lane, w, base);
     if (t.adds) {
         const float c = p.scale[t.index];
 #pragma unroll
@@ -372,22 +398,169 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterParams p) {
         }
     }
     for (int64_t n = n0; n < n_end; n += 256) {
-        if (n > n0) load(n);
-        f32x4 acc[4] = {};
-        if (t.adds) adapter_multiply<RS>(w, hi, lo, acc);
-        if (!t.valid) continue;
-        const int64_t c0 = n + 16 * g;
-        uint16_t* out = p.out + t.token * p.N + c0;
+        if (n > n0) adapter_up_load<RS>(p, t, n, lane, w, base);
+        adapter_up_store<RS>(p, t, n, lane, w, hi, lo, base);
+    }
+}
+
+// One kernel for few tokens per adapter: `parts` workgroups per tile (a power of
+// two) share its tokens, then N, and each forms z of its tokens for itself: A is
+// read as often, but from its die's L2, and no z goes through memory, which
+// costs a second launch and 2 us.  16 waves, one workgroup per compute unit.
+//
+// z by dot products over whole kilobytes of A's rows: a wave takes eight rows
+// and every KP-th 512 elements, NT tokens at a time, and leaves its sums in
+// zs[kp][row of the tile][R].
+__device__ __forceinline__ float add_across(float a, float b, bool half) {
+    // lanes below: a of both halves; lanes above: b (of 64 lanes, or of each 32)
+    const auto s = half ? __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false)
+                        : __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+template <int CTRL>
+__device__ __forceinline__ float lane_shift(float f) {
+    return __uint_as_float(lane_shift0<CTRL, 0xF>(__float_as_uint(f)));
+}
+template <int NT>
+__device__ __forceinline__ void adapter_dots(const AdapterParams& p, const uint16_t* a, const int (&row)[NT],
+                                             const int (&token)[NT], int kp, int KP, int r0, int lane, float* zs) {
+    float acc[NT][8] = {};
+    for (int64_t c = (int64_t)kp * 512; c < p.K; c += (int64_t)KP * 512) {
+        const bool in = c + 8 * lane < p.K;
+        const int64_t k = in ? c + 8 * lane : 0;
+        bf16x8 av[8], xv[NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float f[8];
+        for (int r = 0; r < 8; ++r) av[r] = load_bf16x8(a + r * p.K + k);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = RowElem<uint16_t>::get(base[h], e) + acc[2 * h + (e >> 2)][e & 3];
-            // (without an adapter y goes through as it is, the sign of a zero too)
-            const i32x4 v = t.adds ? RowElem<uint16_t>::pack(f) : base[h];
-            if (n + 64 <= p.N) __builtin_memcpy(out + 8 * h, &v, 16);
-            else if (c0 + 8 * h < p.N) store_row16<uint16_t>(out + 8 * h, p.N - c0 - 8 * h, v);
+        for (int q = 0; q < NT; ++q) xv[q] = load_bf16x8(p.x + (int64_t)token[q] * p.K + k);
+        if (!in) {                          // (both: zero times an infinity is no zero)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) av[r] = bf16x8{};
+#pragma unroll
+            for (int q = 0; q < NT; ++q) xv[q] = bf16x8{};
         }
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; e += 2)
+                    acc[q][r] = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{av[r][e], av[r][e + 1]}, bf16x2{xv[q][e], xv[q][e + 1]},
+                                                                acc[q][r], false);
+    }
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+        // sums over the lanes, halving the rows that a lane holds: row lane / 8 in the end
+        float u[4], v[2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[r] = add_across(acc[q][r], acc[q][r + 4], true);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) v[r] = add_across(u[r], u[r + 2], false);
+        const bool upper = lane & 8;
+        float f = (upper ? v[1] : v[0]) + lane_shift<0x128>(upper ? v[0] : v[1]);   // lane ^ 8
+        f += lane_shift<0x141>(f);          // mirrored in 8 lanes
+        f += lane_shift<0x4E>(f);           // lane ^ 2
+        f += lane_shift<0xB1>(f);           // lane ^ 1
+        if ((lane & 7) == 0) zs[(kp * 16 + row[q]) * p.R + r0 + (lane >> 3)] = f;
+    }
+}
+
+constexpr int kWholeWaves = 16;
+
+template <int RS>
+__global__ __launch_bounds__(64 * kWholeWaves) void adapter_whole_kernel(AdapterParams p) {
+    __shared__ __attribute__((aligned(16))) float zs[kWholeWaves * 16 * 8];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int g = lane >> 4, i = lane & 15;
+    // (a tile's workgroups on one die, whose L2 then holds the adapter)
+    const int part = (int)(blockIdx.x >> 3) & (p.parts - 1);
+    const int64_t tile = (int64_t)((blockIdx.x >> 3) >> __builtin_ctz(p.parts)) * 8 + (blockIdx.x & 7);
+    AdapterTile t = adapter_tile(p, tile, lane);
+    if (!t.any || (!t.adds && p.out == p.y)) return;
+    // Shares of the tokens, each over parts / shares parts of N: the cheapest of
+    // the powers of two.  Cost of a compute unit (measured, in units of R / 8.6 ps):
+    // 28 per 1024 columns times 1024, and per element of K 12 for four tokens,
+    // 7, 9 and 12 for one to three.
+    const uint32_t all = (uint32_t)__ballot(t.valid) & 0xFFFFu;
+    const int log_parts = __builtin_ctz(p.parts), count = __builtin_popcount(all);
+    int log_shares = 0;
+    float least = INFINITY;
+    for (int l = 0; l <= log_parts; ++l) {
+        const int each = (count + (1 << l) - 1) >> l, rest = each & 3;
+        const int columns = 10 + log_parts - l;         // log2 of those that a share's parts do at once
+        const float cost = (float)p.K * (float)(each / 4 * 12 + (rest ? (5 + 2 * rest + rest / 3) : 0)) +
+                           (float)((p.N + (1ll << columns) - 1) >> columns) * (28.f * 1024.f);
+        if (cost < least) {
+            least = cost;
+            log_shares = l;
+        }
+    }
+    const int shares = 1 << log_shares;
+    t.valid = t.valid && ((__builtin_popcount(all & ((1u << i) - 1)) ^ part) & (shares - 1)) == 0;
+    uint32_t left = (uint32_t)__ballot(t.valid) & 0xFFFFu;
+    if (!left) return;
+    const int log_range = 6 + log_parts - log_shares;
+    const int64_t n_range = (p.N + (1ll << log_range) - 1) >> log_range << 6, n_lo = (part >> log_shares) * n_range;
+    const int64_t n_end = n_lo + n_range < p.N ? n_lo + n_range : p.N;
+    const int blocks = p.R / 8, KP = kWholeWaves / blocks;
+    if (t.adds && wave < KP * blocks) {
+        const int kp = wave / blocks, r0 = 8 * (wave - kp * blocks);
+        const uint16_t* a = p.a + ((int64_t)t.index * p.R + r0) * p.K;
+        auto next = [&](int& row, int& token) FP8K_INLINE {
+            if (left) {                     // (the last one twice)
+                row = __builtin_ctz(left);
+                token = __builtin_amdgcn_readlane((int)t.token, row);
+                left &= left - 1;
+            }
+        };
+        while (left) {
+            const int n = __builtin_popcount(left);
+            int row[4] = {}, token[4] = {};
+            if (n == 1) {
+                next(row[0], token[0]);
+                adapter_dots<1>(p, a, {row[0]}, {token[0]}, kp, KP, r0, lane, zs);
+            } else if (n == 2) {
+                next(row[0], token[0]);
+                next(row[1], token[1]);
+                adapter_dots<2>(p, a, {row[0], row[1]}, {token[0], token[1]}, kp, KP, r0, lane, zs);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q > 0) row[q] = row[q - 1], token[q] = token[q - 1];
+                    next(row[q], token[q]);
+                }
+                adapter_dots<4>(p, a, row, token, kp, KP, r0, lane, zs);
+            }
+        }
+    }
+    bf16x8 w[4][RS], hi[RS], lo[RS];
+    i32x4 base[2];
+    int64_t n = n_lo + 64 * wave;
+    if (n < n_end) adapter_up_load<RS>(p, t, n, lane, w, base);
+    __syncthreads();
+    if (n >= n_end) return;
+    if (t.adds) {
+        const float c = p.scale[t.index];
+#pragma unroll
+        for (int s = 0; s < RS; ++s) {
+            float f[8] = {};
+            const int e0 = 32 * s + 8 * g;
+            if (e0 < p.R && t.valid) {
+#pragma unroll 4
+                for (int k = 0; k < KP; ++k) {
+                    const float* z = zs + (k * 16 + i) * p.R + e0;
+                    const f32x4 u = *reinterpret_cast<const f32x4*>(z), v = *reinterpret_cast<const f32x4*>(z + 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] += e < 4 ? u[e] : v[e - 4];
+                }
+            }
+            adapter_parts(f, c, hi[s], lo[s]);
+        }
+    }
+    while (n < n_end) {
+        adapter_up_store<RS>(p, t, n, lane, w, hi, lo, base);
+        n += 64 * kWholeWaves;
+        if (n < n_end) adapter_up_load<RS>(p, t, n, lane, w, base);
     }
 }
 

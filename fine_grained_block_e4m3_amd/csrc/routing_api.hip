@@ -135,10 +135,28 @@ fp8_status rows_grid(fp8k::RowsParams& p, int64_t per_seg, dim3* grid) {
 // Adapters.
 // ---------------------------------------------------------------------------
 struct AdapterPlan {
-    int group;                  // tiles per workgroup: 1 or 4
+    int whole;                  // one kernel, with as many workgroups per tile; 0: two kernels
+    int group;                  // tiles per workgroup of the two: 1 or 4
     int64_t tiles, groups, splits, k_range, n_range;
-    size_t bytes(int64_t R) const { return (size_t)(splits * tiles * 16 * R) * sizeof(float); }
+    size_t bytes(int64_t R) const { return whole ? 0 : (size_t)(splits * tiles * 16 * R) * sizeof(float); }
 };
+
+// One kernel where tiles hold few tokens (tokens times R up to 64 per tile of the
+// table) and four workgroups per tile are about one per compute unit: a table's
+// tiles are those it has room for, of which a quarter or more is empty in most
+// batches.  One MI355X, one kernel / two, us, tiles in use x tokens of each:
+// K 7168, N 2048: 1 x 1 R 16 6.0 / 7.6, R 64 11.8 / 11.9; 64 x 1 R 16 6.4 / 8.7, R 64
+// 17.1 / 18.9; 64 x 4 R 16 8.8 / 9.4; K 2048, N 7168: 1 x 1 R 16 6.6 / 7.1; 64 x 1 7.2 /
+// 10.8; and a launch less.  The other side, K 7168, N 2048: 24 x 16 R 16 9.9 / 8.4, R 64
+// 20.7 / 15.7; 96 x 1 with four workgroups each 11.9 / 10.4, with two 7.8, but
+// with two a tile of 16 tokens takes 13.8 / 8.1.  Parts of N of 256 columns or more (1 x 1,
+// N 2048, R 16: 8 parts 6.0, 16 6.2, N 300: 2 4.8, 16 6.4).
+int adapter_whole_parts(int64_t T, int64_t tiles, int64_t N, int64_t R, int cus) {
+    if (R > 64 || T * R > 64 * tiles || 3 * tiles > cus) return 0;
+    int parts = 1;
+    while (parts < 16 && 2 * parts * 256 < N + 256 && 2 * parts * tiles * 3 <= 4 * (int64_t)cus) parts *= 2;
+    return parts;
+}
 
 // Groups of four tiles where adapters have tokens enough to fill them and the
 // work outweighs the longer way of a workgroup.  One MI355X, K 7168, N 2048,
@@ -154,6 +172,7 @@ struct AdapterPlan {
 AdapterPlan adapter_plan(int64_t T, int64_t L, int64_t rows, int64_t N, int64_t K, int64_t R, int cus) {
     AdapterPlan pl{};
     pl.tiles = rows / 16;
+    pl.whole = adapter_whole_parts(T, pl.tiles, N, R, cus);
     pl.group = T >= 64 * (L + 1) && T * R >= 96 << 10 ? 4 : 1;
     pl.groups = std::max<int64_t>(cdiv(pl.tiles, pl.group), 1);
     auto share = [&](int64_t len, int64_t most, int64_t step, int64_t wgs) {
@@ -408,6 +427,7 @@ fp8_status fp8_adapters_plan(int64_t T, int32_t L, int64_t rows, int64_t N, int6
     plan->k_range = pl.k_range;
     plan->n_range = pl.n_range;
     plan->workspace_bytes = pl.bytes(R);
+    plan->whole = pl.whole;
     return FP8_OK;
 }
 
@@ -434,6 +454,13 @@ fp8_status fp8_add_adapters(const uint16_t* x, const uint16_t* a, const uint16_t
     p.T = T; p.N = N; p.K = K; p.tiles = pl.tiles; p.k_range = pl.k_range; p.n_range = pl.n_range;
     p.L = L; p.R = R; p.splits = (int32_t)pl.splits; p.parts = (int32_t)cdiv(N, pl.n_range);
     const hipStream_t s = (hipStream_t)stream;
+    if (pl.whole) {
+        p.parts = pl.whole;
+        const dim3 grid((unsigned)(cdiv(pl.tiles, 8) * 8 * pl.whole)), block(64 * fp8k::kWholeWaves);
+        if (R <= 32) hipLaunchKernelGGL(fp8k::adapter_whole_kernel<1>, grid, block, 0, s, p);
+        else hipLaunchKernelGGL(fp8k::adapter_whole_kernel<2>, grid, block, 0, s, p);
+        return launch_status();
+    }
     // (one tile: as many steps of K in flight as two chunks leave registers for)
     if (R <= 16) launch_adapter_down<1, 4>(p, pl, s);
     else if (R <= 32) launch_adapter_down<2, 4>(p, pl, s);

@@ -660,7 +660,9 @@ typedef struct {
     int64_t k_splits;       /* workgroups along K of the first kernel */
     int64_t k_range, n_range;   /* of a workgroup of the first and the second kernel */
     size_t workspace_bytes;
-    int32_t group;          /* tiles per workgroup: 1 or 4 */
+    int32_t group;          /* tiles per workgroup of the two: 1 or 4 */
+    int32_t whole;          /* not 0: one kernel instead of the two, with as many workgroups
+                             * per tile and no workspace */
 } fp8_adapters_plan_t;
 fp8_status fp8_adapters_plan(int64_t T, int32_t L, int64_t rows, int64_t N, int64_t K,
                              int32_t R, int32_t compute_units, fp8_adapters_plan_t* plan);

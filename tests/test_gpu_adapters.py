@@ -78,6 +78,61 @@ def test_many_tiles():
         _check(rng, T, L, R, K, N, idx, "many tiles")
 
 
+@pytest.mark.parametrize("R", [8, 16, 24, 40, 56, 64])
+def test_one_kernel(R):
+    """Few tokens per adapter, of which each workgroup of a tile takes a share or
+    a part of N: from one token to a full tile, K and N long and short."""
+    rng = np.random.default_rng(100 + R)
+    for T, L, K, N in ((1, 4, 128, 1), (1, 1, 640, 4099), (2, 40, 7168, 2100), (16, 200, 1152, 2048), (16, 40, 128, 9000),
+                       (30, 60, 512, 600), (40, 70, 8192, 130)):
+        plan = fp8.adapters_plan(T, L, N, K, R)
+        assert plan["whole"] > 0 and plan["workspace_bytes"] == 0
+        for name, idx in (("any", rng.integers(-1, L + 1, T)), ("one", np.full(T, L - 1)), ("pairs", np.arange(T) // 2 % L),
+                          ("sevens", np.arange(T) // 7 % L), ("none", np.full(T, -1))):
+            say("adapters one kernel", R, T, L, K, N, name)
+            _check(rng, T, L, R, K, N, idx, f"{name} {R} {T} {L} {K} {N}")
+
+
+def test_either_side_of_one_kernel():
+    """The sizes beside each bound of the rule, and both forms on the same tokens."""
+    rng = np.random.default_rng(9)
+    for T, L, R, whole in ((84, 200, 16, True), (86, 200, 16, False), (8, 8, 64, True), (8, 8, 72, False), (21, 4, 64, False),
+                           (9, 0, 64, True)):
+        L = L or 9
+        assert (fp8.adapters_plan(T, L, 300, 256, R)["whole"] > 0) == whole, (T, L, R)
+        say("adapters beside a bound", T, L, R)
+        _check(rng, T, L, R, 256, 300, rng.integers(-1, L, T), f"{T} {L} {R}")
+    # the same rows in a table with more tiles: two kernels
+    T, L, R, K, N = 20, 30, 16, 2048, 1000
+    x, a, b, s, y = _operands(rng, T, L, R, K, N)
+    idx = rng.integers(-1, 5, T)
+    rows = fp8.adapter_rows(torch.from_numpy(idx).cuda(), L)
+    more = torch.full((2, 16 * 90), -1, dtype=torch.int32, device="cuda")
+    more[:, :rows.shape[1]] = rows
+    r, err = ref.adapters(_f64(x), _f64(a), _f64(b), _f64(s), idx, _f64(y))
+    for table in (rows, more):
+        ref.assert_near(_f64(fp8.add_adapters(x, a, b, s, table, y)), r, ref.rounded(err, r, True), "both forms")
+
+
+def test_infinities_stay_with_their_token():
+    """What one token, adapter or column holds does not reach another's."""
+    say("adapters infinities")
+    rng = np.random.default_rng(10)
+    T, L, R, K, N = 20, 40, 24, 640, 200
+    x, a, b, s, y = _operands(rng, T, L, R, K, N)
+    idx = np.array([3] * 7 + [4] * 6 + [-1] * 3 + [5] * 4)
+    r, err = ref.adapters(_f64(x), _f64(a), _f64(b), _f64(s), idx, _f64(y))
+    x[2, 639], a[4, 23, 600], b[5, 199, 23], y[14, 3] = float("inf"), float("nan"), float("-inf"), float("nan")
+    rows = fp8.adapter_rows(torch.from_numpy(idx).cuda(), L)
+    assert fp8.adapters_plan(T, L, N, K, R)["whole"] > 0
+    out = fp8.add_adapters(x, a, b, s, rows, y)
+    bad = torch.zeros((T, N), dtype=torch.bool)
+    bad[2], bad[7:13], bad[16:20, 199], bad[14, 3] = True, True, True, True
+    assert not bool(torch.isfinite(out.cpu()[bad]).any())
+    good = ~bad.numpy()
+    ref.assert_near(_f64(out)[good], r[good], ref.rounded(err, r, True)[good], "infinities")
+
+
 def test_given_tables():
     """Rows outside the tokens, tiles of mixed indices, tiles without a row."""
     say("adapters given tables")

@@ -153,7 +153,11 @@ def test_adapter_plan_covers_the_problem(T, adapters, N, K):
         assert p["group"] == (4 if T >= 64 * (adapters + 1) and T * 16 >= 96 << 10 else 1)
         assert p["k_range"] % 128 == 0 and (p["k_splits"] - 1) * p["k_range"] < K <= p["k_splits"] * p["k_range"]
         assert p["n_range"] % 256 == 0 and p["n_range"] > 0
-        assert p["workspace_bytes"] == p["k_splits"] * rows * 16 * 4
+        if p["whole"]:          # a power of two of workgroups per tile, about one per compute unit in all
+            assert p["whole"] in (1, 2, 4, 8, 16) and 3 * p["tiles"] * p["whole"] <= 4 * cus and p["workspace_bytes"] == 0
+            assert 16 * T <= 64 * p["tiles"]
+        else:
+            assert p["workspace_bytes"] == p["k_splits"] * rows * 16 * 4
 
 
 def test_binding_refuses_cpu_tensors():
