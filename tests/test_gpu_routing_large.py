@@ -56,3 +56,23 @@ def test_adapters_behind_four_gigabytes(L, N, group):
             want = want + 0.5 * (b[i].double() @ (a[i].double() @ x[t].double()))
         # whole and half numbers that both products hold exactly: one rounding
         assert float((out[t].double() - want).abs().max()) <= 2.0 ** -8 * float(want.abs().max())
+
+
+def test_adapters_of_few_tokens_behind_four_gigabytes():
+    """The one kernel, at both ends of a and b of more than 5 GB each."""
+    say("large adapters, few tokens")
+    T, L, K, N, R = 4, 1000, 43008, 40000, 64
+    assert fp8.adapters_plan(T, L, N, K, R)["whole"] > 0
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randint(-1, 2, (T, K), generator=gen, device="cuda", dtype=torch.int8).bfloat16()
+    a = torch.randint(-1, 2, (L, R, K), generator=gen, device="cuda", dtype=torch.int8).bfloat16()
+    b = torch.randint(-1, 2, (L, N, R), generator=gen, device="cuda", dtype=torch.int8).bfloat16()
+    y = torch.randint(-3, 4, (T, N), generator=gen, device="cuda", dtype=torch.int8).bfloat16()
+    idx = torch.tensor([L - 1, 0, -1, 499], device="cuda", dtype=torch.int32)
+    out = fp8.add_adapters(x, a, b, torch.full((L,), 0.5, device="cuda"), fp8.adapter_rows(idx, L), y)
+    for t in range(T):
+        i, want = int(idx[t]), y[t].double()
+        if i >= 0:
+            want = want + 0.5 * (b[i].double() @ (a[i].double() @ x[t].double()))
+        # whole and half numbers that both products hold exactly: one rounding
+        assert float((out[t].double() - want).abs().max()) <= 2.0 ** -8 * float(want.abs().max())
