@@ -163,12 +163,15 @@ int adapter_whole_parts(int64_t T, int64_t tiles, int64_t N, int64_t R, int cus)
 // tiles / groups, us: 8 adapters, 1000 tokens, R 16 13 / 17; 4000, R 16 25 / 28;
 // 2000, R 64 35 / 30; 8192, R 16 67 / 48 and R 64 136 / 65; 100 adapters, 4000
 // tokens, R 32 52 / 50; 200 adapters 53 / 72.
-// Workgroups per compute unit: along K two (tiles) or four (groups: one more
+// Workgroups per compute unit of the table: along K eight (tiles: most of a
+// table may be empty, and a full one loses little; 256 tiles, R 64, K 7168, 2 splits / 8, us:
+// 14 in use 17.5 / 6.3, all 34 / 35; R 16 8.1 / 3.7, 10.8 / 11.6) or four (groups: one more
 // than fit, so that the last round is short; 8192 tokens, R 64: 4 splits 65 us,
-// 5 64, 7 62, 10 70), along N four or eight; parts of K of 512 and parts of N of
-// 256 at least.  A single tile has 8 splits at most, whose sums are loaded at
-// once (one token, R 16, 14 splits of 512 3.2 + 5.7 us, 8 of 896 3.6 + 4.7; R 64
-// 4.9 + 8.8, 6.2 + 6.3).
+// 5 64, 7 62, 10 70), along N four or eight, and parts of at most 1024 of N (400
+// tiles, R 16, N 7168, 2 parts / 7: 64 in use 21.7 / 10.6, 256 22.6 / 22.9); parts
+// of K of 512 and parts of N of 256 at least.  A single tile has 8 splits at
+// most, whose sums are loaded at once (one token, R 16, 14 splits of 512 3.2 +
+// 5.7 us, 8 of 896 3.6 + 4.7; R 64 4.9 + 8.8, 6.2 + 6.3).
 AdapterPlan adapter_plan(int64_t T, int64_t L, int64_t rows, int64_t N, int64_t K, int64_t R, int cus) {
     AdapterPlan pl{};
     pl.tiles = rows / 16;
@@ -180,9 +183,10 @@ AdapterPlan adapter_plan(int64_t T, int64_t L, int64_t rows, int64_t N, int64_t 
         return std::max(cdiv(cdiv(len, parts), step), (int64_t)1) * step;
     };
     const int64_t k_most = cdiv(K, 512);
-    pl.k_range = share(K, pl.group == 1 ? std::min<int64_t>(k_most, 8) : k_most, 128, (pl.group == 1 ? 2 : 4) * cus);
+    pl.k_range = share(K, pl.group == 1 ? std::min<int64_t>(k_most, 8) : k_most, 128, (pl.group == 1 ? 8 : 4) * cus);
     pl.splits = cdiv(K, pl.k_range);
     pl.n_range = share(N, cdiv(N, 256), 256, (pl.group == 1 ? 4 : 8) * cus);
+    if (pl.group == 1) pl.n_range = std::min<int64_t>(pl.n_range, 1024);
     return pl;
 }
 
