@@ -1,6 +1,8 @@
 """Low-rank adapters of many requests against their 64-bit form: every rank's
 kernel, one token to long prompts, tokens without an adapter, in place and
 out of place, shared and split tiles."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -133,11 +135,15 @@ def test_infinities_stay_with_their_token():
     ref.assert_near(_f64(out)[good], r[good], ref.rounded(err, r, True)[good], "infinities")
 
 
-def test_given_tables():
+@pytest.mark.parametrize("R,whole", [(16, False), (8, True)])
+def test_given_tables(R, whole):
     """Rows outside the tokens, tiles of mixed indices, tiles without a row."""
-    say("adapters given tables")
+    say("adapters given tables", R)
     rng = np.random.default_rng(3)
-    T, L, R, K, N = 20, 3, 16, 256, 100
+    T, L, K, N = 20, 3, 256, 100
+    plan = fp8.AdaptersPlan()
+    assert fp8.load_library().fp8_adapters_plan(T, L, 64, N, K, R, 256, ctypes.byref(plan)) == 0
+    assert (plan.whole > 0) == whole
     x, a, b, s, y = _operands(rng, T, L, R, K, N)
     src = torch.full((64,), -1, dtype=torch.int32, device="cuda")
     index = torch.full((64,), 1, dtype=torch.int32, device="cuda")
@@ -178,3 +184,43 @@ def test_workspace_and_refusals():
         fp8.add_adapters(x, a[:, :12].contiguous(), b[:, :, :12].contiguous(), s, rows, y)
     assert fp8.add_adapters(x[:0], a, b, s, fp8.adapter_rows(torch.zeros(0, dtype=torch.int32, device="cuda"), 3),
                             y[:0]).shape == (0, 1200)
+
+
+@pytest.mark.parametrize("T,L,whole", [(6, 40, True), (70, 3, False)])
+def test_graph_replays(T, L, whole):
+    """Two captured projections of one table, replayed with other tokens and
+    other adapters, eager calls on another stream in between."""
+    say("adapters graph", T, L)
+    rng = np.random.default_rng(11)
+    K, N, R = 768, 200, 16
+    assert (fp8.adapters_plan(T, L, N, K, R)["whole"] > 0) == whole
+    x, a, b, s, y = _operands(rng, T, L, R, K, N)
+    a2, b2 = b.new_empty(a.shape).copy_(a.flip(1)), b.flip(1).contiguous()
+    idx = torch.zeros(T, dtype=torch.int32, device="cuda")
+
+    def step():
+        rows = fp8.adapter_rows(idx, L)
+        return fp8.add_adapters(x, a, b, s, rows, y), fp8.add_adapters(x, a2, b2, s, rows, y)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in range(4):
+        new = np.random.default_rng(20 + seed)
+        x.copy_(torch.from_numpy(new.normal(size=(T, K)).astype(np.float32)))
+        idx.copy_(torch.from_numpy(new.integers(-1, L if seed else 1, T).astype(np.int32)))
+        graph.replay()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            want = step()
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w), seed
+        r, err = ref.adapters(_f64(x), _f64(a), _f64(b), _f64(s), idx.cpu().numpy(), _f64(y))
+        ref.assert_near(_f64(got[0]), r, ref.rounded(err, r, True), f"replay {seed}")
