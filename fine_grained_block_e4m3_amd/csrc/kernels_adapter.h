@@ -24,8 +24,8 @@
 // instructions that wait anyway.
 //
 // Measured (one MI355X, K 7168): 1 token, R 16, N 2048 6.0 us (one kernel); 100
-// tokens of 64 adapters, N 2112 9.6 (one kernel); 8192 tokens of 8, R 64, N 2048 30 + 27
-// (two; 4.3 and 3.1 TB/s).
+// tokens of 64 adapters, N 2112 9.6 (one kernel); 8192 tokens of 8, R 64, N 2048 28 + 25
+// (two; 4.2 and 3.3 TB/s).
 //
 // The index of a tile is that of its first row with a token; a row of another
 // index is not computed.  Rows of an index outside the adapters take y as it is.
@@ -209,106 +209,123 @@ __global__ __launch_bounds__(256) void adapter_down_kernel(AdapterParams p) {
 }
 
 // z of groups of four tiles: a product of 64 rows of x with A's R rows, K in
-// stages of 64 elements.  Each wave loads whole 128-byte pieces of rows into
-// LDS; one wave's 16 rows and all of A are read back as operands.  A group of
-// several adapters goes through K once for each.
-// LDS row of 128 bytes: its eight 16-byte chunks at slot chunk ^ lds_swz(row).
-__device__ __forceinline__ void dma_lds16_from(uint32_t m0, const void* p) {
-    int saved;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-                 "global_load_lds_dwordx4 %2, off\n\t"
-                 "s_mov_b32 m0, %0"
-                 : "=&s"(saved) : "s"(m0), "v"(p));
+// chunks of CHUNK elements.  Both come into registers in whole 256-byte (128-byte)
+// pieces of their rows, A one chunk ahead and x XD - 1, and from there as the
+// matrix instruction's operands through LDS: a wave's 16 rows of x for itself,
+// A, which all waves share, in two places in turn.  A group of several adapters
+// goes through K once for each.
+// Three chunks of x in registers at R 33 to 64, two at others, and chunks of 64
+// above 64, measured (K 7168, 8192 tokens, us): R 64 two 35.2, three 32.2, chunks
+// of 64 33.4; R 16 26.7, 27.3, 31.1; R 128 29.8, 30.6 and in chunks of 128 39.8.  With x
+// straight in the operands' layout, 16 rows of 64 bytes per load, R 64 35.3, R 16
+// 28.0; through LDS by direct loads, three stages of 64 elements of x and A 34.6, 28.9.
+// LDS row of 2 CHUNK bytes: its 16-byte pieces at place piece ^ adapter_swz(row).
+template <int CHUNK>
+__device__ __forceinline__ int adapter_swz(int row) {       // 16 rows at one piece cover all banks
+    return CHUNK == 128 ? row & 15 : (row >> 1) & 7;
 }
-
-template <int RT, int STAGES>
-__global__ __launch_bounds__(256) void adapter_down_group_kernel(AdapterParams p, int64_t groups) {
-    constexpr int AROWS = (RT + 1) / 2 * 32, ROWS = 64 + AROWS, PER = ROWS / 32;     // 1 KB loads of a wave per stage
-    constexpr int STAGE = ROWS * 128;
-    static_assert((STAGES - 1) * PER <= 63, "vmcnt range");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE];
+template <int RT, int CHUNK, int XD>
+__global__ __launch_bounds__(256, RT <= 4 ? 4 : 2) void adapter_down_group_kernel(AdapterParams p, int64_t groups) {
+    constexpr int PIECES = CHUNK / 8, ROW = 2 * CHUNK;
+    constexpr int XROWS = 64 / PIECES, XN = 16 / XROWS;             // rows of a wave's load of x, and its loads
+    constexpr int AROWS = 256 / PIECES, AN = (16 * RT + AROWS - 1) / AROWS;
+    constexpr int STAGE = AN * AROWS * ROW;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE + 64 * ROW];
+    __shared__ int32_t adapter[4];          // of the tiles, -1: none
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int64_t per = (groups * p.splits + 7) / 8, work = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if ((int64_t)(blockIdx.x >> 3) >= per || work >= groups * p.splits) return;
     const int64_t group = work / p.splits, split = work - group * p.splits;
-    const uint32_t lds0 = (uint32_t)uniform((int)lds_addr(smem));
-    FP8K_LDS const uint8_t* lds = (FP8K_LDS const uint8_t*)smem;
-    AdapterTile t[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) t[m] = adapter_tile(p, group * 4 + m, lane);
+    const AdapterTile t = adapter_tile(p, group * 4 + wave, lane);
+    if (lane == 0) adapter[wave] = t.adds ? t.index : -1;
+    __syncthreads();
     const int64_t k0 = split * p.k_range, k1 = k0 + p.k_range < p.K ? k0 + p.k_range : p.K;
-    const int blocks = (int)((k1 - k0) / 64);
-    // the lane's place in a 1 KB load: row of 8, and the chunk that its slot holds
-    const int lrow = lane >> 3;
-    const uint16_t* from[PER];
+    const int chunks = (int)((k1 - k0) / CHUNK);
+    const int piece = threadIdx.x % PIECES;         // the thread's, of row x_row of every XROWS and a_row of every AROWS
+    const int x_row = lane / PIECES, a_row = threadIdx.x / PIECES;
+    uint8_t* xs = smem + 2 * STAGE + wave * 16 * ROW;
+    const uint16_t* x[XN];
+#pragma unroll
+    for (int j = 0; j < XN; ++j)
+        x[j] = p.x + (int64_t)__shfl((int)t.token, XROWS * j + x_row) * p.K + k0 + 8 * piece;
     f32x4 acc[RT] = {};
-    uint32_t todo = 0;
-#pragma unroll
-    for (int m = 0; m < 4; ++m) todo |= t[m].adds ? 1u << m : 0u;
-    while (todo) {
-        int index = 0, mine = 0;            // this pass's adapter; whether the wave's tile is one of its
-#pragma unroll
-        for (int m = 3; m >= 0; --m)
-            if (todo >> m & 1) index = t[m].index;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-            if ((todo >> m & 1) && t[m].index == index) {
-                todo &= ~(1u << m);
-                mine |= wave == m;
-            }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int row = 8 * (wave * PER + i) + lrow, chunk = (lane & 7) ^ lds_swz(row);
-            if (row < 64) {
-                // (a row without a token: another's values, not used)
-                const int64_t at = group * 64 + row;
-                const int src = at < p.tiles * 16 ? p.src[at] : -1;
-                from[i] = p.x + (int64_t)(src >= 0 && src < p.T ? src : 0) * p.K + k0 + 8 * chunk;
-            } else {
-                const int r = row - 64 < p.R ? row - 64 : p.R - 1;
-                from[i] = p.a + ((int64_t)index * p.R + r) * p.K + k0 + 8 * chunk;
-            }
-        }
-        // (every address is at hand: the compiler's own loads do not count among the stages')
-        auto issue = [&](int kb) FP8K_INLINE {
-            const uint32_t dst = lds0 + (uint32_t)(kb % STAGES * STAGE + wave * PER * 1024);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) dma_lds16_from(dst + i * 1024, from[i] + (int64_t)kb * 64);
-        };
-        for (int kb = 0; kb < STAGES - 1 && kb < blocks; ++kb) issue(kb);
-        for (int kb = 0; kb < blocks; ++kb) {
-            // block kb has landed; the blocks behind it, if there are enough, are under way
-            if (kb + STAGES - 2 < blocks) wait_vmcnt<(STAGES - 2) * PER>();
-            else wait_vmcnt<0>();
-            lds_barrier();
-            // (its stage was read in the last round, which every wave has left)
-            if (kb + STAGES - 1 < blocks) issue(kb + STAGES - 1);
-            if (mine) {
-                FP8K_LDS const uint8_t* base = lds + kb % STAGES * STAGE;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    auto read = [&](int row) FP8K_INLINE {
-                        const int slot = (4 * s + (lane >> 4)) ^ lds_swz(row);
-                        return __builtin_bit_cast(bf16x8, *(FP8K_LDS const i32x4*)(base + row * 128 + 16 * slot));
-                    };
-                    const bf16x8 xv = read(16 * wave + (lane & 15));
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(read(64 + 16 * r + (lane & 15)), xv, acc[r], 0, 0, 0);
-                }
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        }
-        lds_barrier();                      // (before another pass's first stages)
-    }
+    int of[4], todo = 0;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-        if (wave != m || !t[m].adds || !t[m].valid) continue;
-        float* z = p.z + (split * p.tiles * 16 + (group * 4 + m) * 16 + (lane & 15)) * p.R + 4 * (lane >> 4);
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-            if (16 * r + 4 * (lane >> 4) < p.R) *reinterpret_cast<f32x4*>(z + 16 * r) = acc[r];
+        of[m] = uniform(adapter[m]);
+        todo |= of[m] >= 0 ? 1 << m : 0;
     }
+    while (todo) {
+        int index = 0;                      // this pass's adapter
+#pragma unroll
+        for (int m = 3; m >= 0; --m)
+            if (todo >> m & 1) index = of[m];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            if (of[m] == index) todo &= ~(1 << m);
+        const bool mine = t.adds && t.index == index;
+        const uint16_t* a[AN];
+#pragma unroll
+        for (int j = 0; j < AN; ++j) {
+            const int row = AROWS * j + a_row;
+            a[j] = p.a + ((int64_t)index * p.R + (row < p.R ? row : p.R - 1)) * p.K + k0 + 8 * piece;
+        }
+        bf16x8 av[AN], xv[XD][XN];
+        auto load_a = [&](int c) FP8K_INLINE {
+#pragma unroll
+            for (int j = 0; j < AN; ++j) av[j] = load_bf16x8(a[j] + (int64_t)c * CHUNK);
+        };
+        auto load_x = [&](int h, int c) FP8K_INLINE {
+#pragma unroll
+            for (int j = 0; j < XN; ++j) xv[h][j] = load_bf16x8(x[j] + (int64_t)c * CHUNK);
+        };
+        auto put = [&](uint8_t* rows, int row, bf16x8 v) FP8K_INLINE {
+            *reinterpret_cast<bf16x8*>(rows + row * ROW + 16 * (piece ^ adapter_swz<CHUNK>(row))) = v;
+        };
+        auto get = [&](const uint8_t* rows, int row, int s) FP8K_INLINE {
+            return *reinterpret_cast<const bf16x8*>(rows + row * ROW + 16 * ((4 * s + (lane >> 4)) ^ adapter_swz<CHUNK>(row)));
+        };
+        load_a(0);
+        if (mine) {
+#pragma unroll
+            for (int u = 0; u < XD - 1; ++u)
+                if (u < chunks) load_x(u, u);
+        }
+        for (int c0 = 0; c0 < chunks; c0 += XD) {
+#pragma unroll
+            for (int u = 0; u < XD; ++u) {
+                const int c = c0 + u;
+                if (c >= chunks) break;
+                uint8_t* as = smem + (c & 1) * STAGE;       // (read two chunks ago, before the last barrier)
+#pragma unroll
+                for (int j = 0; j < AN; ++j) put(as, AROWS * j + a_row, av[j]);
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < XN; ++j) put(xs, XROWS * j + x_row, xv[u][j]);
+                }
+                if (c + 1 < chunks) load_a(c + 1);
+                if (mine && c + XD - 1 < chunks) load_x((u + XD - 1) % XD, c + XD - 1);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // (the last chunk's reads too)
+                lds_barrier();
+                if (mine) {
+#pragma unroll
+                    for (int s = 0; s < CHUNK / 32; ++s) {
+                        const bf16x8 v = get(xs, lane & 15, s);
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+                            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(get(as, 16 * r + (lane & 15), s), v, acc[r], 0, 0, 0);
+                    }
+                }
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        lds_barrier();                      // (before another pass's first chunk)
+    }
+    if (!t.adds || !t.valid) return;
+    float* z = p.z + (split * p.tiles * 16 + (group * 4 + wave) * 16 + (lane & 15)) * p.R + 4 * (lane >> 4);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+        if (16 * r + 4 * (lane >> 4) < p.R) *reinterpret_cast<f32x4*>(z + 16 * r) = acc[r];
 }
 
 // The sum of eight elements of z over the splits.
@@ -571,12 +588,17 @@ __global__ __launch_bounds__(64 * kWholeWaves) void adapter_whole_kernel(Adapter
 // whole cache lines, read and written with the nontemporal hint (8192 tokens,
 // N 2048, both kernels: R 64 69 us without, 62 with it, R 16 55, 47; 3000 tokens
 // whose y stays cached 34.7, 35.6).
+// Eight waves above R 32, so that z, 64 R values per split for each workgroup,
+// is read half as often (R 64, 8192 tokens, N 2048 28.2 -> 26.1 us, 4000, N 7168
+// 39.0 -> 35.3; R 128 46.7 -> 44.9; R 16 19.8 -> 20.1: four there).
+constexpr int adapter_up_waves(int RS) { return RS == 1 ? 4 : 8; }
+
 template <int RS, bool STREAM>
-__global__ __launch_bounds__(256, RS <= 2 ? 4 : 2) void adapter_up_group_kernel(AdapterParams p, int64_t groups) {
+__global__ __launch_bounds__(64 * adapter_up_waves(RS), RS <= 2 ? 4 : 2) void adapter_up_group_kernel(AdapterParams p, int64_t groups) {
     constexpr int ZROW = 32 * RS + 8;       // elements; 16 rows at one place cover all banks
-    constexpr int DROW = 68;
+    constexpr int DROW = 68, WAVES = adapter_up_waves(RS);
     __shared__ __attribute__((aligned(16))) uint16_t zp[2][64][ZROW];
-    __shared__ __attribute__((aligned(16))) float ds[4][16][DROW];
+    __shared__ __attribute__((aligned(16))) float ds[WAVES][16][DROW];
     __shared__ int32_t token[64], adapter[4];       // -1: none
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int g = lane >> 4, i = lane & 15;
@@ -584,13 +606,13 @@ __global__ __launch_bounds__(256, RS <= 2 ? 4 : 2) void adapter_up_group_kernel(
     if ((int64_t)(blockIdx.x >> 3) >= per || work >= groups * p.parts) return;
     const int64_t group = work / p.parts, n_lo = (work - group * p.parts) * p.n_range;
     const int64_t n_end = n_lo + p.n_range < p.N ? n_lo + p.n_range : p.N;
-    {
+    if (wave < 4) {
         const AdapterTile t = adapter_tile(p, group * 4 + wave, lane);
         if (lane < 16) token[16 * wave + lane] = t.valid ? (int32_t)t.token : -1;
         if (lane == 0) adapter[wave] = t.adds ? t.index : -1;
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < 64 * 4 * RS; k += 256) {
+    for (int k = threadIdx.x; k < 64 * 4 * RS; k += 64 * WAVES) {
         const int row = k / (4 * RS), e0 = 8 * (k % (4 * RS)), a = adapter[row >> 4];
         float f[8] = {};
         bf16x8 hi, lo;
@@ -601,7 +623,7 @@ __global__ __launch_bounds__(256, RS <= 2 ? 4 : 2) void adapter_up_group_kernel(
     }
     __syncthreads();
     const int r8 = lane >> 3, c8 = 8 * (lane & 7);      // the lane's rows r8 and r8 + 8, and its columns
-    for (int64_t n = n_lo + wave * 64; n < n_end; n += 256) {
+    for (int64_t n = n_lo + wave * 64; n < n_end; n += 64 * WAVES) {
         const bool full = n + 64 <= p.N;
         i32x4 base[4][2];
 #pragma unroll

@@ -185,7 +185,8 @@ AdapterPlan adapter_plan(int64_t T, int64_t L, int64_t rows, int64_t N, int64_t 
     const int64_t k_most = cdiv(K, 512);
     pl.k_range = share(K, pl.group == 1 ? std::min<int64_t>(k_most, 8) : k_most, 128, (pl.group == 1 ? 8 : 4) * cus);
     pl.splits = cdiv(K, pl.k_range);
-    pl.n_range = share(N, cdiv(N, 256), 256, (pl.group == 1 ? 4 : 8) * cus);
+    const int64_t n_step = pl.group == 4 && R > 32 ? 512 : 256;       // 64 columns per wave
+    pl.n_range = share(N, cdiv(N, n_step), n_step, (pl.group == 1 ? 4 : 8) * cus);
     if (pl.group == 1) pl.n_range = std::min<int64_t>(pl.n_range, 1024);
     return pl;
 }
@@ -202,17 +203,17 @@ template <int RT, int G>
 void launch_adapter_down(const fp8k::AdapterParams& p, const AdapterPlan& pl, hipStream_t s) {
     const int64_t wgs = pl.groups * p.splits;
     if (pl.group == 1) hipLaunchKernelGGL((fp8k::adapter_down_kernel<RT, G>), dim3((unsigned)wgs), dim3(256), 0, s, p);
-    else hipLaunchKernelGGL((fp8k::adapter_down_group_kernel<RT, 3>), dim3((unsigned)(cdiv(wgs, 8) * 8)), dim3(256), 0, s, p, pl.groups);
+    else hipLaunchKernelGGL((fp8k::adapter_down_group_kernel<RT, RT <= 4 ? 128 : 64, RT == 4 ? 3 : 2>), dim3((unsigned)(cdiv(wgs, 8) * 8)), dim3(256), 0, s, p, pl.groups);
 }
 template <int RS>
 void launch_adapter_up(const fp8k::AdapterParams& p, const AdapterPlan& pl, hipStream_t s) {
     const int64_t wgs = pl.groups * p.parts;
     if (pl.group == 1) hipLaunchKernelGGL((fp8k::adapter_up_kernel<RS>), dim3((unsigned)wgs), dim3(256), 0, s, p);
     else {
-        const dim3 grid((unsigned)(cdiv(wgs, 8) * 8));
+        const dim3 grid((unsigned)(cdiv(wgs, 8) * 8)), block(64 * fp8k::adapter_up_waves(RS));
         const bool lines = whole_lines(p.N, FP8_TYPE_BF16, p.y) && aligned(p.out, kLine);
-        if (lines) hipLaunchKernelGGL((fp8k::adapter_up_group_kernel<RS, true>), grid, dim3(256), 0, s, p, pl.groups);
-        else hipLaunchKernelGGL((fp8k::adapter_up_group_kernel<RS, false>), grid, dim3(256), 0, s, p, pl.groups);
+        if (lines) hipLaunchKernelGGL((fp8k::adapter_up_group_kernel<RS, true>), grid, block, 0, s, p, pl.groups);
+        else hipLaunchKernelGGL((fp8k::adapter_up_group_kernel<RS, false>), grid, block, 0, s, p, pl.groups);
     }
 }
 
