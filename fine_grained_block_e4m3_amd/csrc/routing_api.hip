@@ -158,11 +158,12 @@ int adapter_whole_parts(int64_t T, int64_t tiles, int64_t N, int64_t R, int cus)
     return parts;
 }
 
-// Groups of four tiles where adapters have tokens enough to fill them and the
-// work outweighs the longer way of a workgroup.  One MI355X, K 7168, N 2048,
-// tiles / groups, us: 8 adapters, 1000 tokens, R 16 13 / 17; 4000, R 16 25 / 28;
-// 2000, R 64 35 / 30; 8192, R 16 67 / 48 and R 64 136 / 65; 100 adapters, 4000
-// tokens, R 32 52 / 50; 200 adapters 53 / 72.
+// Groups of four tiles where adapters have tokens enough to share their loads
+// and the work outweighs the longer way of a workgroup.  One MI355X, tiles /
+// groups, us: 8 adapters, K 7168, N 2048: 1000 tokens R 16 11 / 15, R 64 25 / 22; 2000 R 16
+// 17 / 19, R 32 23 / 20; 8192 R 16 51 / 41, R 64 110 / 51; K 4096, N 2048: 8 adapters R
+// 128, 300 tokens 21 / 35, 600 35 / 29; 200 adapters R 64, 2000 tokens 45 / 53, 4000
+// 63 / 59; 8192 tokens of 256 adapters R 32 68 / 57.
 // Workgroups per compute unit of the table: along K eight (tiles: most of a
 // table may be empty, and a full one loses little; 256 tiles, R 64, K 7168, 2 splits / 8, us:
 // 14 in use 17.5 / 6.3, all 34 / 35; R 16 8.1 / 3.7, 10.8 / 11.6) or four (groups: one more
@@ -176,7 +177,7 @@ AdapterPlan adapter_plan(int64_t T, int64_t L, int64_t rows, int64_t N, int64_t 
     AdapterPlan pl{};
     pl.tiles = rows / 16;
     pl.whole = adapter_whole_parts(T, pl.tiles, N, R, cus);
-    pl.group = T >= 64 * (L + 1) && T * R >= 96 << 10 ? 4 : 1;
+    pl.group = T >= 24 * (L + 1) && T * R >= 48 << 10 ? 4 : 1;
     pl.groups = std::max<int64_t>(cdiv(pl.tiles, pl.group), 1);
     auto share = [&](int64_t len, int64_t most, int64_t step, int64_t wgs) {
         const int64_t parts = std::clamp(wgs / pl.groups, (int64_t)1, std::max<int64_t>(most, 1));

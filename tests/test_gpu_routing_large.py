@@ -34,7 +34,7 @@ def test_rows_behind_four_gigabytes():
     assert torch.equal(xq[pos[at, 0].long()], q) and torch.equal(sa[:, pos[at, 0].long()], s)
 
 
-@pytest.mark.parametrize("L,N,group", [(4, 7000, 4), (6000, 64, 1)])
+@pytest.mark.parametrize("L,N,group", [(4, 7000, 4), (20000, 64, 1)])
 def test_adapters_behind_four_gigabytes(L, N, group):
     """In groups of tiles, and in single tiles (many adapters, of which some occur)."""
     say("large adapters", L)

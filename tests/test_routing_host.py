@@ -150,7 +150,7 @@ def test_adapter_plan_covers_the_problem(T, adapters, N, K):
         p = fp8.adapters_plan(T, adapters, N, K, 16, compute_units=cus)
         rows = fp8.expert_rows(T, adapters + 1, 16)
         assert p["tiles"] * 16 == rows
-        assert p["group"] == (4 if T >= 64 * (adapters + 1) and T * 16 >= 96 << 10 else 1)
+        assert p["group"] == (4 if T >= 24 * (adapters + 1) and T * 16 >= 48 << 10 else 1)
         assert p["k_range"] % 128 == 0 and (p["k_splits"] - 1) * p["k_range"] < K <= p["k_splits"] * p["k_range"]
         assert p["n_range"] % 256 == 0 and p["n_range"] > 0
         if p["whole"]:          # a power of two of workgroups per tile, about one per compute unit in all
