@@ -73,7 +73,8 @@ def test_many_tiles():
     rng = np.random.default_rng(2)
     for T, L, R, K, N, group in ((8301, 5, 16, 128, 72, 4), (4000, 300, 24, 256, 130, 1), (2700, 40, 64, 384, 65, 4),
                                  (3080, 12, 32, 2048, 600, 4), (3080, 12, 32, 512, 640, 4), (2000, 3, 64, 256, 192, 4),
-                                 (1000, 3, 128, 1152, 340, 4), (1400, 5, 72, 640, 128, 4)):
+                                 (1000, 3, 128, 1152, 340, 4), (1400, 5, 72, 640, 128, 4), (2100, 60, 24, 1152, 333, 4),
+                                 (1500, 60, 40, 896, 520, 4), (500, 19, 104, 640, 1030, 4), (6200, 250, 8, 128, 64, 4)):
         idx = rng.integers(-1, L, T)
         assert fp8.adapters_plan(T, L, N, K, R)["group"] == group
         say("adapters many tiles", T, L, R)
@@ -186,14 +187,15 @@ def test_workspace_and_refusals():
                             y[:0]).shape == (0, 1200)
 
 
-@pytest.mark.parametrize("T,L,whole", [(6, 40, True), (70, 3, False)])
-def test_graph_replays(T, L, whole):
+@pytest.mark.parametrize("T,L,R,whole,group", [(6, 40, 16, True, 1), (70, 3, 16, False, 1), (1600, 5, 32, False, 4)])
+def test_graph_replays(T, L, R, whole, group):
     """Two captured projections of one table, replayed with other tokens and
     other adapters, eager calls on another stream in between."""
     say("adapters graph", T, L)
     rng = np.random.default_rng(11)
-    K, N, R = 768, 200, 16
-    assert (fp8.adapters_plan(T, L, N, K, R)["whole"] > 0) == whole
+    K, N = 768, 200
+    plan = fp8.adapters_plan(T, L, N, K, R)
+    assert (plan["whole"] > 0) == whole and plan["group"] == group
     x, a, b, s, y = _operands(rng, T, L, R, K, N)
     a2, b2 = b.new_empty(a.shape).copy_(a.flip(1)), b.flip(1).contiguous()
     idx = torch.zeros(T, dtype=torch.int32, device="cuda")
