@@ -170,13 +170,14 @@ __device__ __forceinline__ void adapter_multiply(const bf16x8 (&w)[4][RS], const
 }
 
 // The scaled z of the lane's token, elements 32 s + 8 (l / 16) + 0..7, as two
-// BF16 parts.
+// BF16 parts: the first cut, so that no finite value becomes an infinity; an
+// infinity or NaN stands in it alone.
 __device__ __forceinline__ void adapter_parts(const float (&f)[8], float scale, bf16x8& hi, bf16x8& lo) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float v = scale * f[e];
-        hi[e] = (__bf16)v;
-        lo[e] = (__bf16)(v - (float)hi[e]);
+        const float v = scale * f[e], cut = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+        hi[e] = (__bf16)cut;
+        lo[e] = (__bf16)(__builtin_isfinite(v) ? v - cut : 0.f);
     }
 }
 

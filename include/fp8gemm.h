@@ -642,7 +642,8 @@ fp8_status fp8_expert_combine_grad(const void* dout, const void* y, const int32_
  *   row whose index differs from that of its tile of 16 (the first of its rows
  *   that has a token) is not computed.  Each token stands in at most one row.
  * The products' sums are FP32, x A^T is kept to 16 bits or more, and out is
- * rounded once.  x, a, b and workspace 16-byte aligned; workspace:
+ * rounded once.  Infinities and NaN give what the formula, with scale applied to
+ * x A^T, makes of them.  x, a, b and workspace 16-byte aligned; workspace:
  * fp8_adapters_workspace_size() bytes, else FP8_ERR_SCRATCH; no clearing;
  * calls that overlap in time need one each.
  */
