@@ -171,7 +171,8 @@ __device__ __forceinline__ void adapter_multiply(const bf16x8 (&w)[4][RS], const
 
 // The scaled z of the lane's token, elements 32 s + 8 (l / 16) + 0..7, as two
 // BF16 parts: the first cut, so that no finite value becomes an infinity; an
-// infinity or NaN stands in it alone.
+// infinity or NaN stands in it alone.  Elements behind R take a scale of 0, as
+// an infinite one would make NaN of their zeros.
 __device__ __forceinline__ void adapter_parts(const float (&f)[8], float scale, bf16x8& hi, bf16x8& lo) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -412,7 +413,7 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterParams p) {
         for (int s = 0; s < RS; ++s) {
             float f[8] = {};
             if (t.valid && 32 * s + 8 * g < p.R) adapter_z_sum(p, tile * 16 + i, 32 * s + 8 * g, f);
-            adapter_parts(f, c, hi[s], lo[s]);
+            adapter_parts(f, 32 * s + 8 * g < p.R ? c : 0.f, hi[s], lo[s]);
         }
     }
     for (int64_t n = n0; n < n_end; n += 256) {
@@ -572,7 +573,7 @@ __global__ __launch_bounds__(64 * kWholeWaves) void adapter_whole_kernel(Adapter
                     for (int e = 0; e < 8; ++e) f[e] += e < 4 ? u[e] : v[e - 4];
                 }
             }
-            adapter_parts(f, c, hi[s], lo[s]);
+            adapter_parts(f, e0 < p.R ? c : 0.f, hi[s], lo[s]);
         }
     }
     while (n < n_end) {
@@ -618,7 +619,7 @@ __global__ __launch_bounds__(64 * adapter_up_waves(RS), RS <= 2 ? 4 : 2) void ad
         float f[8] = {};
         bf16x8 hi, lo;
         if (a >= 0 && token[row] >= 0 && e0 < p.R) adapter_z_sum(p, group * 64 + row, e0, f);
-        adapter_parts(f, a >= 0 ? p.scale[a] : 0.f, hi, lo);
+        adapter_parts(f, a >= 0 && e0 < p.R ? p.scale[a] : 0.f, hi, lo);
         *reinterpret_cast<bf16x8*>(&zp[0][row][e0]) = hi;
         *reinterpret_cast<bf16x8*>(&zp[1][row][e0]) = lo;
     }

@@ -88,3 +88,25 @@ def test_magnitudes_at_the_end_of_the_type(form, R):
     assert np.abs(want).max() > 100
     out = fp8.add_adapters(x, a, b, s, fp8.adapter_rows(torch.from_numpy(idx).cuda(), L), y)
     _same(_f64(out), want, err)
+
+
+@pytest.mark.parametrize("form,R", CASES)
+def test_infinite_scales(form, R):
+    """An infinite scale of terms of one sign gives infinities of that sign,
+    whatever the rank is rounded up to; other adapters' tokens see nothing of it."""
+    say("adapters infinite scale", form, R)
+    rng = np.random.default_rng(200 + R)
+    T, L, K, N = _sizes(form, R)
+    x, a = _bf16(rng.uniform(0.5, 2, (T, K))), _bf16(rng.uniform(0.5, 2, (L, R, K)) / K)
+    b = rng.uniform(0.5, 2, (L, N, R)) * rng.choice([-1.0, 1.0], (L, N, 1))
+    b, y = _bf16(b), _bf16(_signs(rng, (T, N)))
+    s = torch.ones(L, device="cuda")
+    s[0], s[1] = float("inf"), float("-inf")
+    idx = rng.integers(-1, L, T)
+    idx[:4] = [0, 1, 0, 1]
+    finite = torch.ones(L, device="cuda")
+    want, err = ref.adapters(_f64(x), _f64(a), _f64(b), _f64(finite), idx, _f64(y))
+    for i, sign in ((0, 1.0), (1, -1.0)):
+        want[idx == i] = sign * np.sign(_f64(b)[i, :, 0]) * np.inf
+    out = fp8.add_adapters(x, a, b, s, fp8.adapter_rows(torch.from_numpy(idx).cuda(), L), y)
+    _same(_f64(out), want, err)
