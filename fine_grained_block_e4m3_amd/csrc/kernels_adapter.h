@@ -19,9 +19,9 @@
 // 105, measured: that is why whole multiplies by rows, and why many tokens go
 // through LDS.)
 // All are bounded by memory otherwise; the products are a few operations per
-// byte.  z enters the second product as the sum of two BF16 values, which keeps
-// 16 bits of it (one part could cost 2^-8 of the added term) and costs only
-// instructions that wait anyway.
+// byte.  z enters the second product as the sum of three BF16 values, which hold
+// all of an FP32 value (one could cost 2^-8 of the added term, two 2^-16); they
+// cost matrix instructions where the kernels wait for memory.
 //
 // Measured (one MI355X, K 7168): 1 token, R 16, N 2048 6.0 us (one kernel); 100
 // tokens of 64 adapters, N 2112 9.6 (one kernel); 8192 tokens of 8, R 64, N 2048 28 + 25
@@ -158,27 +158,32 @@ __device__ __forceinline__ void adapter_b_load(const AdapterParams& p, int32_t i
         }
 }
 template <int RS>
-__device__ __forceinline__ void adapter_multiply(const bf16x8 (&w)[4][RS], const bf16x8 (&hi)[RS], const bf16x8 (&lo)[RS],
-                                                 f32x4 (&acc)[4]) {
+__device__ __forceinline__ void adapter_multiply(const bf16x8 (&w)[4][RS], const bf16x8 (&z)[RS][3], f32x4 (&acc)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int s = 0; s < RS; ++s)
 #pragma unroll
-        for (int s = 0; s < RS; ++s) {
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j][s], hi[s], acc[j], 0, 0, 0);
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j][s], lo[s], acc[j], 0, 0, 0);
-        }
+        for (int h = 0; h < 3; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j][s], z[s][h], acc[j], 0, 0, 0);
 }
 
-// The scaled z of the lane's token, elements 32 s + 8 (l / 16) + 0..7, as two
-// BF16 parts: the first cut, so that no finite value becomes an infinity; an
-// infinity or NaN stands in it alone.  Elements behind R take a scale of 0, as
-// an infinite one would make NaN of their zeros.
-__device__ __forceinline__ void adapter_parts(const float (&f)[8], float scale, bf16x8& hi, bf16x8& lo) {
+// The scaled z of the lane's token, elements 32 s + 8 (l / 16) + 0..7, as three
+// BF16 parts, each the next eight bits of it, cut: together all 24 of an FP32
+// value.  (Two parts left 2^-16 of it, which shows where y takes away the
+// leading bits of what is added.)  No finite value becomes an infinity by the
+// cut; an infinity or NaN stands in the first part alone.  Elements behind R
+// take a scale of 0, as an infinite one would make NaN of their zeros.
+__device__ __forceinline__ void adapter_parts(const float (&f)[8], float scale, bf16x8 (&z)[3]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float v = scale * f[e], cut = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-        hi[e] = (__bf16)cut;
-        lo[e] = (__bf16)(__builtin_isfinite(v) ? v - cut : 0.f);
+        float v = scale * f[e];
+        const bool finite = __builtin_isfinite(v);
+#pragma unroll
+        for (int h = 0; h < 3; ++h) {
+            const float cut = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+            z[h][e] = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(v) >> 16));
+            v = h == 0 && !finite ? 0.f : v - cut;
+        }
     }
 }
 
@@ -376,10 +381,9 @@ __device__ __forceinline__ void adapter_up_load(const AdapterParams& p, const Ad
 }
 template <int RS>
 __device__ __forceinline__ void adapter_up_store(const AdapterParams& p, const AdapterTile& t, int64_t n, int lane,
-                                                 const bf16x8 (&w)[4][RS], const bf16x8 (&hi)[RS], const bf16x8 (&lo)[RS],
-                                                 const i32x4 (&base)[2]) {
+                                                 const bf16x8 (&w)[4][RS], const bf16x8 (&z)[RS][3], const i32x4 (&base)[2]) {
     f32x4 acc[4] = {};
-    if (t.adds) adapter_multiply<RS>(w, hi, lo, acc);
+    if (t.adds) adapter_multiply<RS>(w, z, acc);
     if (!t.valid) return;
     const int64_t c0 = n + 16 * (lane >> 4);
     uint16_t* out = p.out + t.token * p.N + c0;
@@ -404,7 +408,7 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterParams p) {
     if (n0 >= n_end) return;
     const AdapterTile t = adapter_tile(p, tile, lane);
     if (!t.any || (!t.adds && p.out == p.y)) return;
-    bf16x8 w[4][RS], hi[RS], lo[RS];
+    bf16x8 w[4][RS], z[RS][3];
     i32x4 base[2];
     adapter_up_load<RS>(p, t, n0, lane, w, base);
     if (t.adds) {
@@ -413,12 +417,12 @@ __global__ __launch_bounds__(256) void adapter_up_kernel(AdapterParams p) {
         for (int s = 0; s < RS; ++s) {
             float f[8] = {};
             if (t.valid && 32 * s + 8 * g < p.R) adapter_z_sum(p, tile * 16 + i, 32 * s + 8 * g, f);
-            adapter_parts(f, 32 * s + 8 * g < p.R ? c : 0.f, hi[s], lo[s]);
+            adapter_parts(f, 32 * s + 8 * g < p.R ? c : 0.f, z[s]);
         }
     }
     for (int64_t n = n0; n < n_end; n += 256) {
         if (n > n0) adapter_up_load<RS>(p, t, n, lane, w, base);
-        adapter_up_store<RS>(p, t, n, lane, w, hi, lo, base);
+        adapter_up_store<RS>(p, t, n, lane, w, z, base);
     }
 }
 
@@ -552,7 +556,7 @@ __global__ __launch_bounds__(64 * kWholeWaves) void adapter_whole_kernel(Adapter
             }
         }
     }
-    bf16x8 w[4][RS], hi[RS], lo[RS];
+    bf16x8 w[4][RS], z[RS][3];
     i32x4 base[2];
     int64_t n = n_lo + 64 * wave;
     if (n < n_end) adapter_up_load<RS>(p, t, n, lane, w, base);
@@ -567,17 +571,17 @@ __global__ __launch_bounds__(64 * kWholeWaves) void adapter_whole_kernel(Adapter
             if (e0 < p.R && t.valid) {
 #pragma unroll 4
                 for (int k = 0; k < KP; ++k) {
-                    const float* z = zs + (k * 16 + i) * p.R + e0;
-                    const f32x4 u = *reinterpret_cast<const f32x4*>(z), v = *reinterpret_cast<const f32x4*>(z + 4);
+                    const float* sum = zs + (k * 16 + i) * p.R + e0;
+                    const f32x4 u = *reinterpret_cast<const f32x4*>(sum), v = *reinterpret_cast<const f32x4*>(sum + 4);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[e] += e < 4 ? u[e] : v[e - 4];
                 }
             }
-            adapter_parts(f, e0 < p.R ? c : 0.f, hi[s], lo[s]);
+            adapter_parts(f, e0 < p.R ? c : 0.f, z[s]);
         }
     }
     while (n < n_end) {
-        adapter_up_store<RS>(p, t, n, lane, w, hi, lo, base);
+        adapter_up_store<RS>(p, t, n, lane, w, z, base);
         n += 64 * kWholeWaves;
         if (n < n_end) adapter_up_load<RS>(p, t, n, lane, w, base);
     }
@@ -599,7 +603,7 @@ template <int RS, bool STREAM>
 __global__ __launch_bounds__(64 * adapter_up_waves(RS), RS <= 2 ? 4 : 2) void adapter_up_group_kernel(AdapterParams p, int64_t groups) {
     constexpr int ZROW = 32 * RS + 8;       // elements; 16 rows at one place cover all banks
     constexpr int DROW = 68, WAVES = adapter_up_waves(RS);
-    __shared__ __attribute__((aligned(16))) uint16_t zp[2][64][ZROW];
+    __shared__ __attribute__((aligned(16))) uint16_t zp[3][64][ZROW];
     __shared__ __attribute__((aligned(16))) float ds[WAVES][16][DROW];
     __shared__ int32_t token[64], adapter[4];       // -1: none
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -617,11 +621,11 @@ __global__ __launch_bounds__(64 * adapter_up_waves(RS), RS <= 2 ? 4 : 2) void ad
     for (int k = threadIdx.x; k < 64 * 4 * RS; k += 64 * WAVES) {
         const int row = k / (4 * RS), e0 = 8 * (k % (4 * RS)), a = adapter[row >> 4];
         float f[8] = {};
-        bf16x8 hi, lo;
+        bf16x8 z[3];
         if (a >= 0 && token[row] >= 0 && e0 < p.R) adapter_z_sum(p, group * 64 + row, e0, f);
-        adapter_parts(f, a >= 0 && e0 < p.R ? p.scale[a] : 0.f, hi, lo);
-        *reinterpret_cast<bf16x8*>(&zp[0][row][e0]) = hi;
-        *reinterpret_cast<bf16x8*>(&zp[1][row][e0]) = lo;
+        adapter_parts(f, a >= 0 && e0 < p.R ? p.scale[a] : 0.f, z);
+#pragma unroll
+        for (int h = 0; h < 3; ++h) *reinterpret_cast<bf16x8*>(&zp[h][row][e0]) = z[h];
     }
     __syncthreads();
     const int r8 = lane >> 3, c8 = 8 * (lane & 7);      // the lane's rows r8 and r8 + 8, and its columns
@@ -651,14 +655,13 @@ __global__ __launch_bounds__(64 * adapter_up_waves(RS), RS <= 2 ? 4 : 2) void ad
                     adapter_b_load<RS>(p, a, [&](int j) FP8K_INLINE { return n + 16 * j + i; }, g, w);
                     held = a;
                 }
-                bf16x8 hi[RS], lo[RS];
+                bf16x8 z[RS][3];
 #pragma unroll
-                for (int s = 0; s < RS; ++s) {
-                    hi[s] = *reinterpret_cast<const bf16x8*>(&zp[0][16 * m + i][32 * s + 8 * g]);
-                    lo[s] = *reinterpret_cast<const bf16x8*>(&zp[1][16 * m + i][32 * s + 8 * g]);
-                }
+                for (int s = 0; s < RS; ++s)
+#pragma unroll
+                    for (int h = 0; h < 3; ++h) z[s][h] = *reinterpret_cast<const bf16x8*>(&zp[h][16 * m + i][32 * s + 8 * g]);
                 f32x4 acc[4] = {};
-                adapter_multiply<RS>(w, hi, lo, acc);
+                adapter_multiply<RS>(w, z, acc);
                 // (the wave's own buffer: its LDS operations run in order)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4*>(&ds[wave][i][16 * j + 4 * g]) = acc[j];

@@ -641,8 +641,8 @@ fp8_status fp8_expert_combine_grad(const void* dout, const void* y, const int32_
  *   tokens in no row are not written: sort with `keep` where out is not y.  A
  *   row whose index differs from that of its tile of 16 (the first of its rows
  *   that has a token) is not computed.  Each token stands in at most one row.
- * The products' sums are FP32, x A^T is kept to 16 bits or more, and out is
- * rounded once.  Infinities and NaN give what the formula, with scale applied to
+ * The products' sums are FP32, x A^T enters the second one as an FP32 value, and
+ * out is rounded once.  Infinities and NaN give what the formula, with scale applied to
  * x A^T, makes of them.  x, a, b and workspace 16-byte aligned; workspace:
  * fp8_adapters_workspace_size() bytes, else FP8_ERR_SCRATCH; no clearing;
  * calls that overlap in time need one each.

@@ -110,3 +110,30 @@ def test_infinite_scales(form, R):
         want[idx == i] = sign * np.sign(_f64(b)[i, :, 0]) * np.inf
     out = fp8.add_adapters(x, a, b, s, fp8.adapter_rows(torch.from_numpy(idx).cuda(), L), y)
     _same(_f64(out), want, err)
+
+
+@pytest.mark.parametrize("form,R", CASES)
+@pytest.mark.parametrize("scale", [1.0, -0.125])
+def test_every_bit_of_the_first_product(form, R, scale):
+    """What is left where y takes away the leading bits of the added term.
+
+    x and a are whole numbers up to 255 and x has 128 places that are not zero:
+    every z and every sum on the way to it is a whole number below 2^23, which
+    FP32 holds.  b has one 1 per column and y is the term rounded to BF16: the
+    last sum is exact in FP32 too, and out is its one rounding."""
+    say("adapters every bit", form, R, scale)
+    rng = np.random.default_rng(300 + R)
+    T, L, K, N = _sizes(form, R)
+    x, a = rng.integers(100, 256, (T, K)), rng.integers(100, 256, (L, R, K))
+    x[:, rng.permutation(K)[128:]] = 0
+    b = np.zeros((L, N, R))
+    b[:, np.arange(N), np.arange(N) % R] = 1.0
+    idx = rng.integers(0, L, T)
+    z = np.stack([a[i] @ x[t] for t, i in enumerate(idx)])
+    assert z.max() < 2 ** 23 and (z & 0xFF).any()
+    term = torch.from_numpy(np.ascontiguousarray(scale * z[:, np.arange(N) % R], np.float32))
+    y = -term.bfloat16()
+    want = (y.float() + term).bfloat16()                    # both operands and the sum exact
+    x, a, b, s = _bf16(x), _bf16(a), _bf16(b), torch.full((L,), scale, device="cuda")
+    out = fp8.add_adapters(x, a, b, s, fp8.adapter_rows(torch.from_numpy(idx).cuda(), L), y.cuda())
+    assert torch.equal(out.cpu(), want)
