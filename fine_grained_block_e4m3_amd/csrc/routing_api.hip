@@ -17,7 +17,8 @@ namespace {
 
 using namespace fp8h;
 
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+// Workgroups of a launch: a grid has fewer than 2^32 threads.
+constexpr int64_t max_grid(int threads) { return 0xFFFFFFFFll / threads; }
 
 bool row_type_ok(int32_t t) { return t == FP8_TYPE_F32 || t == FP8_TYPE_BF16; }
 size_t type_size(int32_t t) { return t == FP8_TYPE_F32 ? 4 : 2; }
@@ -31,7 +32,7 @@ constexpr int kMaxRouteE = 1024, kMaxRouteK = 64;
 fp8_status check_route(int64_t T, int32_t E, int32_t k, int32_t type) {
     if (!dims_ok(T) || E < 1 || k < 1 || !row_type_ok(type)) return FP8_ERR_INVALID_ARG;
     if (k > E) return FP8_ERR_SHAPE;
-    if (E > kMaxRouteE || k > kMaxRouteK) return FP8_ERR_UNSUPPORTED;
+    if (E > kMaxRouteE || k > kMaxRouteK || cdiv(T, 4) > max_grid(256)) return FP8_ERR_UNSUPPORTED;
     return FP8_OK;
 }
 
@@ -121,13 +122,15 @@ constexpr int64_t kCacheBytes = (int64_t)256 << 20;
 constexpr size_t kLine = 128;
 bool whole_lines(int64_t W, int32_t type, const void* p) { return W * (int64_t)type_size(type) % kLine == 0 && aligned(p, kLine); }
 
-// Waves (4 a workgroup) that move rows, and those that look for rows to clear.
-fp8_status rows_grid(fp8k::RowsParams& p, int64_t per_seg, dim3* grid) {
+// Waves (4 a workgroup) that move rows, and those that look for rows to clear;
+// workgroups in whole `step`s.
+fp8_status rows_grid(fp8k::RowsParams& p, int64_t per_seg, dim3* grid, int64_t step = 1) {
     p.segs = cdiv(p.W, per_seg);
     p.work = p.T * p.segs;
     const int64_t waves = p.work + (p.src ? cdiv(p.rows, fp8k::kClearRows) : 0);
-    if (cdiv(waves, 4) > kMaxGrid) return FP8_ERR_UNSUPPORTED;
-    *grid = dim3((unsigned)cdiv(waves, 4));
+    const int64_t wgs = cdiv(cdiv(waves, 4), step) * step;
+    if (wgs > max_grid(256)) return FP8_ERR_UNSUPPORTED;
+    *grid = dim3((unsigned)wgs);
     return FP8_OK;
 }
 
@@ -190,6 +193,13 @@ AdapterPlan adapter_plan(int64_t T, int64_t L, int64_t rows, int64_t N, int64_t 
     pl.n_range = share(N, cdiv(N, n_step), n_step, (pl.group == 1 ? 4 : 8) * cus);
     if (pl.group == 1) pl.n_range = std::min<int64_t>(pl.n_range, 1024);
     return pl;
+}
+
+// Both launches fit, found before the first one is enqueued.  The grids of groups
+// are whole 8s, and their second kernel has up to 512 threads.
+bool adapter_grids_ok(const AdapterPlan& pl, int64_t N) {
+    const int64_t wgs = pl.groups * std::max(pl.splits, cdiv(N, pl.n_range));
+    return pl.group == 1 ? wgs <= max_grid(256) : cdiv(wgs, 8) * 8 <= max_grid(512);
 }
 
 fp8_status check_adapters(int64_t T, int64_t N, int64_t K, int32_t L, int32_t R, int64_t rows) {
@@ -308,17 +318,17 @@ fp8_status fp8_expert_dispatch(const void* x, const int32_t* pos, const int32_t*
     const fp8_status st = check_rows(T, k, rows, K, type);
     if (st != FP8_OK) return st;
     if (rows == 0 || K == 0 || (T == 0 && !src)) return FP8_OK;
+    fp8k::RowsParams p{};
+    p.x = x; p.out = xs; p.pos = pos; p.src = src; p.T = T; p.rows = rows; p.W = K; p.k = k;
+    dim3 grid;
+    const fp8_status g = rows_grid(p, 64 * fp8k::kRowVecs * 16 / (int64_t)type_size(type), &grid);
+    if (g != FP8_OK) return g;
     if ((T && (!x || !pos)) || !xs) return FP8_ERR_INVALID_ARG;
     if (!aligned(x, type_size(type)) || !aligned(xs, type_size(type)) || !aligned(pos, 4) || !aligned(src, 4))
         return FP8_ERR_ALIGNMENT;
     int cus = 0;
     const fp8_status dev = current_device_cus(&cus);
     if (dev != FP8_OK) return dev;
-    fp8k::RowsParams p{};
-    p.x = x; p.out = xs; p.pos = pos; p.src = src; p.T = T; p.rows = rows; p.W = K; p.k = k;
-    dim3 grid;
-    const fp8_status g = rows_grid(p, 64 * fp8k::kRowVecs * 16 / (int64_t)type_size(type), &grid);
-    if (g != FP8_OK) return g;
     if (type == FP8_TYPE_F32) hipLaunchKernelGGL(fp8k::expert_dispatch_kernel<float>, grid, dim3(256), 0, (hipStream_t)stream, p);
     else hipLaunchKernelGGL(fp8k::expert_dispatch_kernel<uint16_t>, grid, dim3(256), 0, (hipStream_t)stream, p);
     return launch_status();
@@ -331,17 +341,16 @@ fp8_status fp8_expert_dispatch_quant(const void* x, const int32_t* pos, uint8_t*
     if (flags & ~FP8_FLAG_UE8M0) return FP8_ERR_INVALID_ARG;
     if (K % 128) return FP8_ERR_SHAPE;
     if (T == 0 || rows == 0 || K == 0) return FP8_OK;
+    fp8k::RowsParams p{};
+    p.x = x; p.out = xq; p.sa = sa; p.pos = pos; p.T = T; p.rows = rows; p.W = K; p.k = k;
+    dim3 grid;
+    const fp8_status g = rows_grid(p, 1024, &grid, 8);
+    if (g != FP8_OK) return g;
     if (!x || !pos || !xq || !sa) return FP8_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(xq) || !aligned16(sa) || !aligned(pos, 4)) return FP8_ERR_ALIGNMENT;
     int cus = 0;
     const fp8_status dev = current_device_cus(&cus);
     if (dev != FP8_OK) return dev;
-    fp8k::RowsParams p{};
-    p.x = x; p.out = xq; p.sa = sa; p.pos = pos; p.T = T; p.rows = rows; p.W = K; p.k = k;
-    dim3 grid;
-    const fp8_status g = rows_grid(p, 1024, &grid);
-    grid.x = (grid.x + 7) / 8 * 8;
-    if (g != FP8_OK) return g;
     const hipStream_t s = (hipStream_t)stream;
     const bool pow2 = flags & FP8_FLAG_UE8M0;
     const bool past = T * k * K > kCacheBytes;
@@ -361,17 +370,17 @@ fp8_status fp8_expert_combine(const void* y, const int32_t* pos, const float* we
     const fp8_status st = check_rows(T, k, rows, N, type);
     if (st != FP8_OK) return st;
     if (T == 0 || N == 0) return FP8_OK;
+    fp8k::RowsParams p{};
+    p.x = y; p.out = out; p.pos = pos; p.w = weights; p.T = T; p.rows = rows; p.W = N; p.k = k;
+    dim3 grid;
+    const fp8_status g = rows_grid(p, 64 * fp8k::kCombineVecs * 16 / (int64_t)type_size(type), &grid);
+    if (g != FP8_OK) return g;
     if ((rows && !y) || !pos || !out) return FP8_ERR_INVALID_ARG;
     if (!aligned(y, type_size(type)) || !aligned(out, type_size(type)) || !aligned(pos, 4) || !aligned(weights, 4))
         return FP8_ERR_ALIGNMENT;
     int cus = 0;
     const fp8_status dev = current_device_cus(&cus);
     if (dev != FP8_OK) return dev;
-    fp8k::RowsParams p{};
-    p.x = y; p.out = out; p.pos = pos; p.w = weights; p.T = T; p.rows = rows; p.W = N; p.k = k;
-    dim3 grid;
-    const fp8_status g = rows_grid(p, 64 * fp8k::kCombineVecs * 16 / (int64_t)type_size(type), &grid);
-    if (g != FP8_OK) return g;
     const bool lines = whole_lines(N, type, y);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)stream, p); };
     if (type == FP8_TYPE_F32) lines ? go(fp8k::expert_combine_kernel<float, true>) : go(fp8k::expert_combine_kernel<float, false>);
@@ -386,6 +395,8 @@ fp8_status fp8_expert_combine_grad(const void* dout, const void* y, const int32_
     if (st != FP8_OK) return st;
     if (!dy && !dweights) return FP8_OK;
     if (T == 0 && (!dy || !src || rows == 0 || N == 0)) return FP8_OK;
+    const int64_t wgs = T + (dy && src ? cdiv(rows, 4 * fp8k::kClearRows) : 0);
+    if (wgs > max_grid(256)) return FP8_ERR_UNSUPPORTED;
     if ((T && (!pos || (N && !dout))) || (T && rows && N && dweights && !y)) return FP8_ERR_INVALID_ARG;
     for (const void* q : {dout, y, (const void*)dy})
         if (!aligned(q, type_size(type))) return FP8_ERR_ALIGNMENT;
@@ -398,8 +409,6 @@ fp8_status fp8_expert_combine_grad(const void* dout, const void* y, const int32_
     p.x = dout; p.y = y; p.out = dy; p.dw = dweights; p.pos = pos; p.w = weights; p.src = dy ? src : nullptr;
     p.T = T; p.rows = rows; p.W = N; p.k = k;
     p.work = T;
-    const int64_t wgs = T + (p.src ? cdiv(rows, 4 * fp8k::kClearRows) : 0);
-    if (wgs > kMaxGrid) return FP8_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)wgs);
     const bool few = k <= 4, lines = whole_lines(N, type, y) && aligned(dy, kLine);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, (hipStream_t)stream, p); };
@@ -417,7 +426,8 @@ size_t fp8_adapters_workspace_size(int64_t T, int32_t L, int64_t rows, int64_t N
     if (check_adapters(T, N, K, L, R, rows) != FP8_OK) return 0;
     int cus = 0;
     if (current_device_cus(&cus) != FP8_OK) return 0;
-    return adapter_plan(T, L, rows, N, K, R, cus).bytes(R);
+    const AdapterPlan pl = adapter_plan(T, L, rows, N, K, R, cus);
+    return adapter_grids_ok(pl, N) ? pl.bytes(R) : 0;
 }
 
 fp8_status fp8_adapters_plan(int64_t T, int32_t L, int64_t rows, int64_t N, int64_t K, int32_t R, int32_t compute_units,
@@ -426,6 +436,7 @@ fp8_status fp8_adapters_plan(int64_t T, int32_t L, int64_t rows, int64_t N, int6
     const fp8_status st = check_adapters(T, N, K, L, R, rows);
     if (st != FP8_OK) return st;
     const AdapterPlan pl = adapter_plan(T, L, rows, N, K, R, compute_units);
+    if (!adapter_grids_ok(pl, N)) return FP8_ERR_UNSUPPORTED;
     *plan = fp8_adapters_plan_t{};
     plan->tiles = pl.tiles;
     plan->group = pl.group;
@@ -452,8 +463,8 @@ fp8_status fp8_add_adapters(const uint16_t* x, const uint16_t* a, const uint16_t
     const fp8_status dev = current_device_cus(&cus);
     if (dev != FP8_OK) return dev;
     const AdapterPlan pl = adapter_plan(T, L, rows, N, K, R, cus);
+    if (!adapter_grids_ok(pl, N)) return FP8_ERR_UNSUPPORTED;
     if (workspace_bytes < pl.bytes(R)) return FP8_ERR_SCRATCH;
-    if ((pl.tiles + 8) * std::max(pl.splits, cdiv(N, pl.n_range)) > kMaxGrid) return FP8_ERR_UNSUPPORTED;
     fp8k::AdapterParams p{};
     p.x = x; p.a = a; p.b = b; p.scale = scale; p.src = src; p.index = index; p.y = y; p.out = out;
     p.z = static_cast<float*>(workspace);
