@@ -1022,8 +1022,11 @@ def expert_dispatch_quant(x, pos, rows, ue8m0: bool = False, out=None):
     T, K = x.shape
     k = _pairs(pos, T)
     _same_device(x, pos)
-    shape = (rows, K) if isinstance(rows, int) else (*rows, K)
-    n = rows if isinstance(rows, int) else rows[0] * rows[1]
+    if isinstance(rows, int):
+        shape, n = (rows, K), rows
+    else:
+        experts, max_m = rows
+        shape, n = (experts, max_m, K), experts * max_m
     if out is None:
         xq, sa = x.new_empty(shape, dtype=_U8), x.new_empty((K // 128, n), dtype=_F32)
     else:
