@@ -1067,7 +1067,8 @@ def expert_combine_grad(dout, y, pos, weights=None, src=None, need_dy: bool = Tr
     """Gradient of expert_combine: (dy of y's shape and type, dweights fp32
     (T, k)); None for what is not wanted.  dy[pos[t, j]] = weights[t, j] *
     dout[t]; with src (rows) the rows without a pair are zeros, else they stay
-    as they are.  out: (dy, dweights) buffers."""
+    as they are.  Each row is named at most once in pos, as the sorts do.
+    out: (dy, dweights) buffers."""
     L = load_library()
     kind, rows, N = _expert_rows_of(y, "y")
     T, k = pos.shape if isinstance(pos, torch.Tensor) and pos.dim() == 2 else (-1, 0)
@@ -1156,7 +1157,9 @@ def add_adapters(x, a, b, scale, rows, y, out=None, workspace=None) -> torch.Ten
     """A projection's result y (T, N) bf16 with each token's adapter added:
     out[t] = y[t] + scale[i] * (x[t] a[i]^T) b[i]^T.  x (T, K), a (L, R, K),
     b (L, N, R) bf16, scale fp32 (L), rows from adapter_rows(ids, L).  Tokens
-    without an adapter take y as it is.  out may be y."""
+    without an adapter take y as it is.  out may be y.  y is a projection that is
+    still to be transformed: the gate and up projections of gated_nt, which
+    applies the activation in its kernel, need gemm_nt instead."""
     L = load_library()
     T, N, K, n, R, nrows = _adapter_operands(x, a, b, scale, rows, y)
     o = torch.empty_like(y) if out is None else out if out is y else _out(out, "out", _BF16, (T, N), x)

@@ -23,9 +23,9 @@
 // all of an FP32 value (one could cost 2^-8 of the added term, two 2^-16); they
 // cost matrix instructions where the kernels wait for memory.
 //
-// Measured (one MI355X, K 7168): 1 token, R 16, N 2048 6.0 us (one kernel); 100
-// tokens of 64 adapters, N 2112 9.6 (one kernel); 8192 tokens of 8, R 64, N 2048 28 + 25
-// (two; 4.2 and 3.3 TB/s).
+// Measured (one MI355X, K 7168): 1 token, R 16, N 2048 6.1 us (one kernel); 100
+// tokens of 64 adapters, N 2112 10.0 (one kernel); 8192 tokens of 8, R 64, N 2048 28 + 26
+// (two; 4.2 and 3.1 TB/s).
 //
 // The index of a tile is that of its first row with a token; a row of another
 // index is not computed.  Rows of an index outside the adapters take y as it is.
@@ -592,11 +592,12 @@ __global__ __launch_bounds__(64 * kWholeWaves) void adapter_whole_kernel(Adapter
 // each tile's results change places in LDS so that 8 lanes hold 64 columns of a
 // row and y is read and written in whole 128-byte pieces.  STREAM: those are
 // whole cache lines, read and written with the nontemporal hint (8192 tokens,
-// N 2048, both kernels: R 64 69 us without, 62 with it, R 16 55, 47; 3000 tokens
-// whose y stays cached 34.7, 35.6).
+// N 2048, both kernels, three sets of x, y and out in turn: R 64 64.4 us without,
+// 57.9 with it, R 16 51.6, 44.9, R 128 104.3, 97.6; 3000 tokens, R 64 31.5, 30.4).
 // Eight waves above R 32, so that z, 64 R values per split for each workgroup,
-// is read half as often (R 64, 8192 tokens, N 2048 28.2 -> 26.1 us, 4000, N 7168
-// 39.0 -> 35.3; R 128 46.7 -> 44.9; R 16 19.8 -> 20.1: four there).
+// is read half as often (both kernels, four waves / eight, us: R 64, 8192 tokens,
+// N 2048 54.0 / 51.7, 4000, N 7168 58.3 / 48.7; R 128 80.5 / 79.8; R 32 41.3 / 42.5, R 16
+// 39.3 / 40.2: four there).
 constexpr int adapter_up_waves(int RS) { return RS == 1 ? 4 : 8; }
 
 template <int RS, bool STREAM>

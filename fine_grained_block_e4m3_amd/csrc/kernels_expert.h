@@ -17,7 +17,7 @@
 // Measured (one MI355X, kernel time): sort of 65536 pairs over 256 experts 10.8
 // us, of up to 512 3.2; 8192 x 8 rows of 7168: codes 119 (5.1 TB/s), combine
 // 179 (5.9 TB/s); 4096 x 2: combine 30, gradient 53 (5.8 TB/s); 3001 x 4 rows of
-// 1530 copied 11.7 (5.2 TB/s).
+// 1530 copied 11.6 (4.6 TB/s).
 #pragma once
 
 #include "rows_common.h"
@@ -417,7 +417,8 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(RowsParams p) {
 // of y once.  STREAM: rows of whole cache lines are read and written with the
 // nontemporal hint (4096 x 2, N 7168: 66 us without, 55 with it, and 117, 115
 // with a pass that reads dy; 1024 x 8 86, 76; 8192 x 8 510, 496; rows of 3060
-// bytes 26.4, 26.9).
+// bytes 26.4, 26.9).  With 8 pairs at a time the compiler keeps up to 43 scalars
+// (rows and their bases) in lanes of vector registers; nothing goes to memory.
 template <typename T, int PAIRS, bool STREAM>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(RowsParams p) {
     constexpr int VN = RowElem<T>::VN;

@@ -148,12 +148,12 @@ struct AdapterPlan {
 // table) and four workgroups per tile are about one per compute unit: a table's
 // tiles are those it has room for, of which a quarter or more is empty in most
 // batches.  One MI355X, one kernel / two, us, tiles in use x tokens of each:
-// K 7168, N 2048: 1 x 1 R 16 6.0 / 7.6, R 64 11.8 / 11.9; 64 x 1 R 16 6.4 / 8.7, R 64
-// 17.1 / 18.9; 64 x 4 R 16 8.8 / 9.4; K 2048, N 7168: 1 x 1 R 16 6.6 / 7.1; 64 x 1 7.2 /
-// 10.8; and a launch less.  The other side, K 7168, N 2048: 24 x 16 R 16 9.9 / 8.4, R 64
-// 20.7 / 15.7; 96 x 1 with four workgroups each 11.9 / 10.4, with two 7.8, but
-// with two a tile of 16 tokens takes 13.8 / 8.1.  Parts of N of 256 columns or more (1 x 1,
-// N 2048, R 16: 8 parts 6.0, 16 6.2, N 300: 2 4.8, 16 6.4).
+// K 7168, N 2048: 1 x 1 R 16 6.2 / 7.4, R 64 12.1 / 11.8; 64 x 1 R 16 6.9 / 9.2, R 64
+// 17.4 / 19.1; 64 x 4 R 16 9.5 / 9.8; K 2048, N 7168: 1 x 1 R 16 5.9 / 6.8; 64 x 1 7.7 /
+// 11.4; and a launch less.  The other side, K 7168, N 2048: 24 x 16 R 16 11.4 / 8.5, R 64
+// 25.3 / 16.2; 96 x 1 with four workgroups each 12.5 / 11.2, with two 8.3, but
+// with two a tile of 16 tokens takes 14.0 / 7.9.  Parts of N of 256 columns or more (1 x 1,
+// R 16: N 2048 8 parts 6.2, 16 6.1, N 300 2 parts 5.7, 16 6.2).
 int adapter_whole_parts(int64_t T, int64_t tiles, int64_t N, int64_t R, int cus) {
     if (R > 64 || T * R > 64 * tiles || 3 * tiles > cus) return 0;
     int parts = 1;
@@ -163,19 +163,27 @@ int adapter_whole_parts(int64_t T, int64_t tiles, int64_t N, int64_t R, int cus)
 
 // Groups of four tiles where adapters have tokens enough to share their loads
 // and the work outweighs the longer way of a workgroup.  One MI355X, tiles /
-// groups, us: 8 adapters, K 7168, N 2048: 1000 tokens R 16 11 / 15, R 64 25 / 22; 2000 R 16
-// 17 / 19, R 32 23 / 20; 8192 R 16 51 / 41, R 64 110 / 51; K 4096, N 2048: 8 adapters R
-// 128, 300 tokens 21 / 35, 600 35 / 29; 200 adapters R 64, 2000 tokens 45 / 53, 4000
-// 63 / 59; 8192 tokens of 256 adapters R 32 68 / 57.
+// groups, us: 8 adapters, K 7168, N 2048: 1000 tokens R 16 14.2 / 15.4, R 64 33.9 / 23.1;
+// 2000 R 16 17.0 / 18.8, R 32 26.7 / 20.4; 8192 R 16 50.9 / 41.8, R 64 108.7 / 56.0; K
+// 4096, N 2048: 8 adapters R 128, 300 tokens 21.3 / 29.3, 600 35.8 / 29.6.  Around 24
+// tokens per adapter the two are about even where the tokens are spread over all
+// adapters (R 64, of 255 adapters, K 7168, N 2048: 16 each 91 / 104, 20 115 / 113, 24 120 /
+// 119; K 4096: 10 each 49 / 54, 20 64 / 58, 32 106 / 92; K 2048, N 5000, of 60: 16 29 / 37,
+// 24 33 / 32; R 16, K 4096: 16 28.7 / 32.7, 23 40.5 / 39.9, 32 47.8 / 47.7).
+// The count is that of the table's adapters: which of them occur the host does
+// not know.  Few long runs of tokens over a large table therefore keep to tiles
+// (7 runs, 255 adapters, K 4096, N 2048: R 64, 4000 tokens 38.8 / 33.6, 6000 55.9 / 45.4;
+// at R 16, 21.1 / 25.6 and 27.7 / 35.9, tiles are the faster ones).
 // Workgroups per compute unit of the table: along K eight (tiles: most of a
-// table may be empty, and a full one loses little; 256 tiles, R 64, K 7168, 2 splits / 8, us:
-// 14 in use 17.5 / 6.3, all 34 / 35; R 16 8.1 / 3.7, 10.8 / 11.6) or four (groups: one more
-// than fit, so that the last round is short; 8192 tokens, R 64: 4 splits 65 us,
-// 5 64, 7 62, 10 70), along N four or eight, and parts of at most 1024 of N (400
-// tiles, R 16, N 7168, 2 parts / 7: 64 in use 21.7 / 10.6, 256 22.6 / 22.9); parts
-// of K of 512 and parts of N of 256 at least.  A single tile has 8 splits at
-// most, whose sums are loaded at once (one token, R 16, 14 splits of 512 3.2 +
-// 5.7 us, 8 of 896 3.6 + 4.7; R 64 4.9 + 8.8, 6.2 + 6.3).
+// table may be empty, and a full one loses little; 256 tiles, R 64, K 7168, first
+// kernel, 2 splits / 8, us: 14 in use 17.5 / 6.3, all 34 / 35; R 16 8.1 / 3.7, 10.8 / 11.6)
+// or four (groups; 8192 tokens, K 7168, N 2048, both kernels: R 64 3 splits 54.6 us, 5
+// 52.7, 7 51.8, 8 53.8, 10 56.4; R 16 44.4, 42.3, 39.5, 40.2, 41.2), along N four or eight,
+// and parts of at most 1024 of N (440 and 631 tiles, R 16, K 2048, N 7168, both kernels, 2
+// or 1 parts / 7: 64 in use 25.7 / 15.2, 256 49.6 / 40.4); parts of K of 512 and parts
+// of N of 256 at least.  A single tile has 8 splits at most, whose sums are
+// loaded at once (K 7168, N 2048, 14 splits of 512 / 8 of 896: one token R 104 21.1 / 18.8;
+// 200 of 3 adapters R 64 15.9 / 14.9).
 AdapterPlan adapter_plan(int64_t T, int64_t L, int64_t rows, int64_t N, int64_t K, int64_t R, int cus) {
     AdapterPlan pl{};
     pl.tiles = rows / 16;

@@ -622,7 +622,8 @@ fp8_status fp8_expert_combine(const void* y, const int32_t* pos, const float* we
 
 /*
  * Its gradient: dy[pos[t][j]] = weights[t][j] * dout[t], and dweights[t][j] =
- * <dout[t], y[pos[t][j]]> in FP32 (0 for a pair without a row).
+ * <dout[t], y[pos[t][j]]> in FP32 (0 for a pair without a row).  Each row is named
+ * at most once, as the sorts do: of a row named twice dy holds one pair's part.
  *   dout (T,N), y and dy (rows,N) of one type; dy or dweights may be NULL (not
  *   computed; y is read for dweights only).  src as for fp8_expert_dispatch.
  */
