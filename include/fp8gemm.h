@@ -518,10 +518,11 @@ size_t fp8_clip_workspace_size(const int64_t* sizes, int32_t count);
  * Around the experts' products: the router's choice, tokens sorted by expert
  * and back.  Unlike the calls above these take pointers of any alignment that
  * their elements have, except where a call says otherwise.  A call whose launch
- * would have 2^32 threads or more is FP8_ERR_UNSUPPORTED: the router's from 2^26
- * rows on, the combine's gradient from 2^24 tokens and 32s of rows to clear, the
- * moving of rows from 2^26 runs of 4 KB of a token (the combine's of 2 KB, the
- * quantizing dispatch's of 1024 elements) and 8s of rows to clear.
+ * would have 2^32 threads or more is FP8_ERR_UNSUPPORTED: the router's of more
+ * than 2^26 - 4 rows, the combine's gradient of more than 2^24 - 1 tokens and 32s
+ * of rows to clear, the moving of rows of more than 2^26 - 4 runs of 4 KB of a
+ * token (the combine's of 2 KB) and 8s of rows to clear, the quantizing
+ * dispatch's of more than 2^26 - 32 runs of 1024 elements.
  * ------------------------------------------------------------------------- */
 
 /*
